@@ -17,8 +17,9 @@ from . import build as _build
 ATTN_F16, ATTN_BF16 = 0, 1
 STATUS = {0: "ATTN_OK", 1: "ATTN_ERR_NULL", 2: "ATTN_ERR_SHAPE", 3: "ATTN_ERR_HEADDIM",
           4: "ATTN_ERR_DTYPE", 5: "ATTN_ERR_ALIGN", 6: "ATTN_ERR_LAUNCH", 7: "ATTN_ERR_TIMEOUT",
-          8: "ATTN_ERR_NODEVICE", 9: "ATTN_ERR_SCRATCH"}
-ATTN_OK, ATTN_ERR_TIMEOUT, ATTN_ERR_SCRATCH = 0, 7, 9
+          8: "ATTN_ERR_NODEVICE", 9: "ATTN_ERR_SCRATCH", 10: "ATTN_ERR_PAGE", 11: "ATTN_ERR_POOL"}
+ATTN_OK, ATTN_ERR_SHAPE, ATTN_ERR_TIMEOUT, ATTN_ERR_SCRATCH = 0, 2, 7, 9
+ATTN_ERR_PAGE, ATTN_ERR_POOL = 10, 11
 
 _lock = threading.Lock()
 _lib = None
@@ -28,6 +29,14 @@ class AttnError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
         super().__init__(f"{what}: {STATUS.get(status, status)}")
+
+
+class KVCache(ctypes.Structure):
+    """attn_kv_cache_t: a paged key/value cache as the C entry points take it."""
+
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("k", "v", "table", "lens", "refs", "scratch")]
+                + [(n, ctypes.c_int) for n in ("n_layers", "n_pages", "page", "Hkv", "D", "n_rows",
+                                               "table_width", "dtype")])
 
 
 def load(path: str | None = None):
@@ -61,6 +70,31 @@ def load(path: str | None = None):
         lib.attn_fwd_kv_split.restype = i
         lib.attn_fwd_kv_split_workspace.argtypes = [i, i, i, i, i, i, i, ctypes.POINTER(ctypes.c_size_t)]
         lib.attn_fwd_kv_split_workspace.restype = i
+        sz, pc = ctypes.c_size_t, ctypes.POINTER(KVCache)
+        lib.attn_fwd_varlen.argtypes = [vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, vp,
+                                        ctypes.c_float, i, i, vp]
+        lib.attn_fwd_varlen.restype = i
+        lib.attn_fwd_tree_workspace.argtypes = [i, i, ctypes.POINTER(sz)]
+        lib.attn_fwd_tree_workspace.restype = i
+        lib.attn_fwd_tree.argtypes = [vp, pc, i, vp, vp, vp, vp, vp, i, i, i, vp, ctypes.c_float, vp,
+                                      sz, vp]
+        lib.attn_fwd_tree.restype = i
+        lib.attn_kv_scratch.argtypes = [i, i, ctypes.POINTER(sz)]
+        lib.attn_kv_scratch.restype = i
+        lib.attn_kv_extend.argtypes = [pc, vp, vp, i, vp]
+        lib.attn_kv_extend.restype = i
+        lib.attn_kv_append.argtypes = [pc, i, vp, vp, vp, vp, vp, i, i, vp]
+        lib.attn_kv_append.restype = i
+        lib.attn_kv_accept.argtypes = [pc, vp, vp, vp, i, vp, i, vp]
+        lib.attn_kv_accept.restype = i
+        lib.attn_kv_copy.argtypes = [pc, vp, vp, i, vp]
+        lib.attn_kv_copy.restype = i
+        lib.attn_kv_fork.argtypes = [pc, vp, vp, i, vp]
+        lib.attn_kv_fork.restype = i
+        lib.attn_kv_free.argtypes = [pc, vp, i, vp]
+        lib.attn_kv_free.restype = i
+        lib.attn_kv_compact.argtypes = [pc, vp, vp]
+        lib.attn_kv_compact.restype = i
         lib.attn_test_force_splits.argtypes = [i]
         lib.attn_test_force_splits.restype = None
         lib.attn_status_str.argtypes = [i]
@@ -297,4 +331,341 @@ def attention(q, k, v, causal: bool = True, scale: float | None = None, with_lse
         st = attn_fwd_kv(q, k, v, o, lse, B, Hq, Hkv, N, Nk, D, scale, causal, q.dtype, stream)
     if st != ATTN_OK:
         raise AttnError(st, f"attn_fwd ({attn_last_cuda_error()})")
+    return o, lse
+
+
+# ------------------------------------------------------------------ packed sequences
+def _strides(values):
+    """Element strides as the C entry points take them (None stays None)."""
+    return None if values is None else (ctypes.c_longlong * len(values))(*values)
+
+
+def attn_fwd_varlen(q, k, v, o, lse, cu_q, cu_k, n_seqs, total_q, total_k, Hq, Hkv, D, strides, scale,
+                    causal, dtype, stream=None) -> int:
+    """The C entry point with the same name; returns its status code.  ``strides``:
+    None or 8 element strides."""
+    return load().attn_fwd_varlen(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(cu_q), _ptr(cu_k),
+                                  int(n_seqs), int(total_q), int(total_k), int(Hq), int(Hkv), int(D),
+                                  _strides(strides), float(scale), int(bool(causal)), _dtype_code(dtype),
+                                  _stream_handle(stream))
+
+
+def _rows(t, name):
+    """(rows, heads, D) of a packed tensor and its row and head strides."""
+    if t.dim() != 3 or t.stride(2) != 1:
+        raise ValueError(f"{name} must be [tokens, heads, D] with the last axis contiguous")
+    return t.shape, (t.stride(0), t.stride(1))
+
+
+def _ints(t, name, device, shape=None):
+    """Checks an int32 index tensor."""
+    import torch
+
+    if t.dtype != torch.int32 or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor on {device}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    return t
+
+
+def _same(t, name, dtype, device):
+    if t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name} must be {dtype} on {device}")
+
+
+def _launch(what, device, stream, call):
+    """Runs call(stream handle) with ``device`` current; raises AttnError unless it succeeds."""
+    import torch
+
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    if device.index is None or device.index == torch.cuda.current_device():
+        st = call(_stream_handle(stream))
+    else:
+        with torch.cuda.device(device):
+            st = call(_stream_handle(stream))
+    if st != ATTN_OK:
+        raise AttnError(st, f"{what} ({attn_last_cuda_error()})")
+
+
+def _outputs(q, Hq, total, with_lse, out, lse_out, stream):
+    """The output tensors: given ones are checked; new ones belong to ``stream`` too."""
+    import torch
+
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if stream is not None and not isinstance(stream, int):
+            out.record_stream(stream)
+    else:
+        _same(out, "out", q.dtype, q.device)
+        if out.shape != q.shape:
+            raise ValueError(f"out must have shape {tuple(q.shape)}")
+    lse = None
+    if with_lse:
+        lse = lse_out
+        if lse is None:
+            lse = torch.empty((Hq, total), dtype=torch.float32, device=q.device)
+            if stream is not None and not isinstance(stream, int):
+                lse.record_stream(stream)
+        elif lse.dtype != torch.float32 or lse.device != q.device or tuple(lse.shape) != (Hq, total) \
+                or not lse.is_contiguous():
+            raise ValueError(f"lse_out must be contiguous float32 [{Hq}, {total}] on {q.device}")
+    return out, lse
+
+
+def attention_varlen(q, k, v, cu_q, cu_k=None, causal: bool = True, scale: float | None = None,
+                     with_lse: bool = True, out=None, lse_out=None, stream=None):
+    """attn_fwd_varlen for torch CUDA tensors q [total_q,Hq,D], k/v [total_k,Hkv,D] (any row and
+    head strides that the C entry point takes, e.g. heads cut from one projection's output).
+
+    ``cu_q`` (and ``cu_k`` where the keys' offsets differ): int32 [n_seqs + 1] offsets on the
+    device, never read by the host.  Returns (o [total_q,Hq,D], lse [Hq,total_q]) without waiting;
+    rows behind the last sequence are not written."""
+    (total_q, Hq, D), sq = _rows(q, "q")
+    (total_k, Hkv, Dk), sk = _rows(k, "k")
+    (total_v, Hv, Dv), sv = _rows(v, "v")
+    if (total_v, Hv, Dv) != (total_k, Hkv, Dk) or Dk != D:
+        raise ValueError("k and v must have one shape [total_k, Hkv, D] with q's D")
+    for t, name in ((k, "k"), (v, "v")):
+        _same(t, name, q.dtype, q.device)
+    _ints(cu_q, "cu_q", q.device)
+    if cu_q.dim() != 1 or cu_q.numel() < 1:
+        raise ValueError("cu_q must hold n_seqs + 1 offsets")
+    if cu_k is not None:
+        _ints(cu_k, "cu_k", q.device, cu_q.shape)
+    o, lse = _outputs(q, Hq, total_q, with_lse, out, lse_out, stream)
+    so = _rows(o, "out")[1]
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    _launch("attn_fwd_varlen", q.device, stream, lambda s: attn_fwd_varlen(
+        q, k, v, o, lse, cu_q, cu_k, cu_q.numel() - 1, total_q, total_k, Hq, Hkv, D, sq + sk + sv + so,
+        scale, causal, q.dtype, s))
+    return o, lse
+
+
+# ------------------------------------------------------------------ paged cache
+def attn_kv_scratch(n_pages, n_rows):
+    """(status, bytes) of the C entry point with the same name."""
+    n = ctypes.c_size_t(0)
+    st = load().attn_kv_scratch(int(n_pages), int(n_rows), ctypes.byref(n))
+    return st, n.value
+
+
+class KVPages:
+    """A paged key/value cache over torch CUDA tensors (attn_kv_cache_t).
+
+    k, v   [n_layers, n_pages, Hkv, page, D] pools (fp16 or bf16)
+    table  int32 [n_rows, table_width] pages of each sequence, -1 behind the last
+    lens   int32 [n_rows] positions of each sequence
+    refs   int32 [n_pages] table entries that name the page; 0: free
+
+    The tensors stay the caller's and are changed in place; the object holds them and the
+    scratch of the calls.  Calls on one cache must be ordered on the device."""
+
+    def __init__(self, k, v, table, lens, refs, scratch=None):
+        import torch
+
+        if k.dim() != 5 or v.shape != k.shape or not (k.is_contiguous() and v.is_contiguous()):
+            raise ValueError("k and v must be contiguous [n_layers, n_pages, Hkv, page, D]")
+        _same(v, "v", k.dtype, k.device)
+        n_layers, n_pages, Hkv, page, D = k.shape
+        if table.dim() != 2:
+            raise ValueError("table must be [n_rows, table_width]")
+        _ints(table, "table", k.device)
+        _ints(lens, "lens", k.device, (table.shape[0],))
+        _ints(refs, "refs", k.device, (n_pages,))
+        st, nbytes = attn_kv_scratch(n_pages, table.shape[0])
+        if st != ATTN_OK:
+            raise AttnError(st, "attn_kv_scratch")
+        if scratch is None:
+            scratch = torch.empty(nbytes // 4, dtype=torch.int32, device=k.device)
+        _ints(scratch, "scratch", k.device)
+        if scratch.numel() * 4 < nbytes:
+            raise ValueError(f"scratch must hold {nbytes // 4} ints")
+        self.k, self.v, self.table, self.lens, self.refs, self.scratch = k, v, table, lens, refs, scratch
+        self.device = k.device
+        self.n_rows, self.table_width = table.shape
+        self.n_layers, self.n_pages, self.Hkv, self.page, self.D = n_layers, n_pages, Hkv, page, D
+        self.c = KVCache(_ptr(k), _ptr(v), _ptr(table), _ptr(lens), _ptr(refs), _ptr(scratch), n_layers,
+                         n_pages, page, Hkv, D, self.n_rows, self.table_width, _dtype_code(k.dtype))
+
+    @classmethod
+    def empty(cls, n_layers, n_pages, Hkv, page, D, n_rows, table_width, dtype, device="cuda"):
+        """A cache without sequences (pool contents undefined)."""
+        import torch
+
+        k, v = (torch.empty((n_layers, n_pages, Hkv, page, D), dtype=dtype, device=device) for _ in "kv")
+        i32 = dict(dtype=torch.int32, device=device)
+        return cls(k, v, torch.full((n_rows, table_width), -1, **i32), torch.zeros(n_rows, **i32),
+                   torch.zeros(n_pages, **i32))
+
+
+def _c(cache):
+    """The C structure of a KVPages, or what the caller passes in its place."""
+    c = cache.c if isinstance(cache, KVPages) else cache
+    return None if c is None else ctypes.byref(c)
+
+
+def attn_kv_extend(cache, seqs, n_new, n, stream=None) -> int:
+    """The C entry point with the same name; returns its status code."""
+    return load().attn_kv_extend(_c(cache), _ptr(seqs), _ptr(n_new), int(n), _stream_handle(stream))
+
+
+def attn_kv_append(cache, layer, k_new, v_new, strides, cu, seqs, n, total, stream=None) -> int:
+    """The C entry point with the same name; returns its status code."""
+    return load().attn_kv_append(_c(cache), int(layer), _ptr(k_new), _ptr(v_new), _strides(strides), _ptr(cu),
+                                 _ptr(seqs), int(n), int(total), _stream_handle(stream))
+
+
+def attn_kv_accept(cache, cu, seqs, path, path_width, taken, n, stream=None) -> int:
+    """The C entry point with the same name; returns its status code."""
+    return load().attn_kv_accept(_c(cache), _ptr(cu), _ptr(seqs), _ptr(path), int(path_width), _ptr(taken),
+                                 int(n), _stream_handle(stream))
+
+
+def attn_kv_copy(cache, src, dst, n, stream=None) -> int:
+    """The C entry point with the same name; returns its status code."""
+    return load().attn_kv_copy(_c(cache), _ptr(src), _ptr(dst), int(n), _stream_handle(stream))
+
+
+def attn_kv_fork(cache, parents, children, n, stream=None) -> int:
+    """The C entry point with the same name; returns its status code."""
+    return load().attn_kv_fork(_c(cache), _ptr(parents), _ptr(children), int(n), _stream_handle(stream))
+
+
+def attn_kv_free(cache, seqs, n, stream=None) -> int:
+    """The C entry point with the same name; returns its status code."""
+    return load().attn_kv_free(_c(cache), _ptr(seqs), int(n), _stream_handle(stream))
+
+
+def attn_kv_compact(cache, live, stream=None) -> int:
+    """The C entry point with the same name; returns its status code."""
+    return load().attn_kv_compact(_c(cache), _ptr(live), _stream_handle(stream))
+
+
+def attn_fwd_tree_workspace(n_seqs, D):
+    """(status, bytes) of the C entry point with the same name."""
+    n = ctypes.c_size_t(0)
+    st = load().attn_fwd_tree_workspace(int(n_seqs), int(D), ctypes.byref(n))
+    return st, n.value
+
+
+def attn_fwd_tree(q, cache, layer, o, lse, cu, seqs, parents, n_seqs, total_q, Hq, strides, scale, workspace,
+                  workspace_bytes, stream=None) -> int:
+    """The C entry point with the same name; returns its status code.  ``strides``: None or 4
+    element strides."""
+    return load().attn_fwd_tree(_ptr(q), _c(cache), int(layer), _ptr(o), _ptr(lse), _ptr(cu), _ptr(seqs),
+                                _ptr(parents), int(n_seqs), int(total_q), int(Hq), _strides(strides),
+                                float(scale), _ptr(workspace), int(workspace_bytes), _stream_handle(stream))
+
+
+def _list(t, name, cache, n=None):
+    """An int32 list on the cache's device (None stays None)."""
+    if t is None:
+        return None
+    if t.dim() != 1:
+        raise ValueError(f"{name} must be one-dimensional")
+    return _ints(t, name, cache.device, None if n is None else (n,))
+
+
+def kv_extend(cache, n_new, seqs=None, stream=None):
+    """attn_kv_extend: room for n_new[i] more positions of sequence seqs[i] (i, when None)."""
+    n = _list(n_new, "n_new", cache).numel()
+    _list(seqs, "seqs", cache, n)
+    _launch("attn_kv_extend", cache.device, stream, lambda s: attn_kv_extend(cache, seqs, n_new, n, s))
+
+
+def kv_append(cache, k_new, v_new, cu, seqs=None, layer: int = 0, stream=None):
+    """attn_kv_append: packed rows k_new, v_new [total,Hkv,D] become the last positions of the
+    sequences (offsets ``cu`` [n + 1]), whose lens already counts them."""
+    (total, Hkv, D), sk = _rows(k_new, "k_new")
+    (total_v, Hv, Dv), sv = _rows(v_new, "v_new")
+    if (total, Hkv, D) != (total_v, Hv, Dv) or (Hkv, D) != (cache.Hkv, cache.D):
+        raise ValueError("k_new and v_new must be [total, Hkv, D] with the cache's Hkv and D")
+    for t, name in ((k_new, "k_new"), (v_new, "v_new")):
+        _same(t, name, cache.k.dtype, cache.device)
+    n = _list(cu, "cu", cache).numel() - 1
+    _list(seqs, "seqs", cache, n)
+    _launch("attn_kv_append", cache.device, stream, lambda s: attn_kv_append(
+        cache, layer, k_new, v_new, sk + sv, cu, seqs, n, total, s))
+
+
+def kv_accept(cache, cu, path, taken, seqs=None, stream=None):
+    """attn_kv_accept: of each tree (offsets ``cu``), the tokens path[i, :taken[i]] stay."""
+    n = _list(cu, "cu", cache).numel() - 1
+    _list(seqs, "seqs", cache, n)
+    _list(taken, "taken", cache, n)
+    if path.dim() != 2 or path.shape[0] != n:
+        raise ValueError("path must be [n, path_width]")
+    _ints(path, "path", cache.device)
+    _launch("attn_kv_accept", cache.device, stream, lambda s: attn_kv_accept(
+        cache, cu, seqs, path, path.shape[1], taken, n, s))
+
+
+def kv_copy(cache, src, dst, stream=None):
+    """attn_kv_copy: the contents of pages src[i] go to pages dst[i], in every layer."""
+    n = _list(src, "src", cache).numel()
+    _list(dst, "dst", cache, n)
+    _launch("attn_kv_copy", cache.device, stream, lambda s: attn_kv_copy(cache, src, dst, n, s))
+
+
+def kv_fork(cache, parents, children, stream=None):
+    """attn_kv_fork: the empty sequences children[i] become copies of parents[i]."""
+    n = _list(parents, "parents", cache).numel()
+    _list(children, "children", cache, n)
+    _launch("attn_kv_fork", cache.device, stream, lambda s: attn_kv_fork(cache, parents, children, n, s))
+
+
+def kv_free(cache, seqs, stream=None):
+    """attn_kv_free: the sequences become empty and give their pages back."""
+    n = _list(seqs, "seqs", cache).numel()
+    _launch("attn_kv_free", cache.device, stream, lambda s: attn_kv_free(cache, seqs, n, s))
+
+
+def kv_compact(cache, live=None, stream=None):
+    """attn_kv_compact: the live pages become pages 0 .. live - 1.  Returns the int32 [1] tensor
+    that receives ``live``."""
+    import torch
+
+    if live is None:
+        live = torch.empty(1, dtype=torch.int32, device=cache.device)
+        if stream is not None and not isinstance(stream, int):
+            live.record_stream(stream)
+    else:
+        _ints(live, "live", cache.device, (1,))
+    _launch("attn_kv_compact", cache.device, stream, lambda s: attn_kv_compact(cache, live, s))
+    return live
+
+
+def attention_tree(q, cache, cu, seqs=None, parents=None, layer: int = 0, scale: float | None = None,
+                   with_lse: bool = True, workspace=None, out=None, lse_out=None, stream=None):
+    """attn_fwd_tree: q [total,Hq,D] holds the queries of each sequence's last tokens (offsets
+    ``cu`` [n + 1]), which form a tree by ``parents`` (None: a chain; one token each: a decoding
+    step), over a KVPages ``cache``.
+
+    ``workspace``: a uint8 CUDA tensor, or None to let torch allocate the size that
+    attn_fwd_tree_workspace asks for.  Returns (o [total,Hq,D], lse [Hq,total]) without waiting."""
+    import torch
+
+    (total, Hq, D), sq = _rows(q, "q")
+    _same(q, "q", cache.k.dtype, cache.device)
+    if D != cache.D or Hq % cache.Hkv != 0:
+        raise ValueError("q must be [total, Hq, D] with the cache's D and Hq a multiple of its Hkv")
+    n = _list(cu, "cu", cache).numel() - 1
+    _list(seqs, "seqs", cache, n)
+    _list(parents, "parents", cache, total)
+    o, lse = _outputs(q, Hq, total, with_lse, out, lse_out, stream)
+    so = _rows(o, "out")[1]
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    if workspace is None:
+        st, nbytes = attn_fwd_tree_workspace(n, D)
+        if st != ATTN_OK:
+            raise AttnError(st, "attn_fwd_tree_workspace")
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+        if stream is not None and not isinstance(stream, int):
+            workspace.record_stream(stream)
+    _launch("attn_fwd_tree", q.device, stream, lambda s: attn_fwd_tree(
+        q, cache, layer, o, lse, cu, seqs, parents, n, total, Hq, sq + so, scale, workspace,
+        workspace.numel(), s))
     return o, lse

@@ -346,7 +346,7 @@ constexpr int kMaxDevices = 64;
 std::mutex g_dev_mu;
 int g_dev_state[kMaxDevices];      // 0 unknown, 1 sm_103, -1 other
 int g_dev_sms[kMaxDevices];        // multiprocessor count
-unsigned g_dev_smem_set[kMaxDevices];  // bit per kernel instantiation
+unsigned long long g_dev_smem_set[kMaxDevices];  // bit per kernel instantiation
 void *g_dev_scratch[kMaxDevices];      // address of g_noalloc_scratch on the device
 
 // Streams and events of attn_fwd_host, created on the first call on a device and
@@ -426,13 +426,13 @@ attn_status_t check_device(int *dev_out) {
 template <typename K>
 attn_status_t set_smem_limit(int dev, int kid, K kern, int smem) {
     std::lock_guard<std::mutex> lk(g_dev_mu);
-    if (!(g_dev_smem_set[dev] >> kid & 1u)) {
+    if (!(g_dev_smem_set[dev] >> kid & 1ull)) {
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) {
             note_cuda_error(e, "cudaFuncSetAttribute");
             return ATTN_ERR_LAUNCH;
         }
-        g_dev_smem_set[dev] |= 1u << kid;
+        g_dev_smem_set[dev] |= 1ull << kid;
     }
     return ATTN_OK;
 }
@@ -928,7 +928,9 @@ const char *attn_status_str(attn_status_t status) {
         case ATTN_ERR_LAUNCH: return "CUDA launch or driver call failed";
         case ATTN_ERR_TIMEOUT: return "in-kernel wait timed out";
         case ATTN_ERR_NODEVICE: return "no sm_103 device is current";
-        case ATTN_ERR_SCRATCH: return "problem needs more scratch than the fixed device buffer holds";
+        case ATTN_ERR_SCRATCH: return "problem needs more scratch than the buffer holds";
+        case ATTN_ERR_PAGE: return "page table entry out of range, missing, or shared where it would be written";
+        case ATTN_ERR_POOL: return "not enough free pages";
     }
     return "unknown status";
 }
@@ -973,3 +975,5 @@ void attn_test_force_splits(int n_splits) { g_force_splits.store(n_splits > 0 ? 
 void attn_test_set_item_order(int order) { g_item_order.store(order == 1 ? 1 : 0); }
 
 }  // extern "C"
+
+#include "entry_packed_paged.cuh"

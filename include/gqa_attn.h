@@ -51,8 +51,12 @@ typedef enum {
     ATTN_ERR_TIMEOUT = 7,  /* a bounded in-kernel wait ran out (reported by
                               attn_last_device_error) */
     ATTN_ERR_NODEVICE = 8, /* no CUDA device of compute capability 10.3 is current */
-    ATTN_ERR_SCRATCH = 9   /* attn_fwd_decode_noalloc: the problem needs more scratch
-                              than the library's fixed device buffer holds */
+    ATTN_ERR_SCRATCH = 9,  /* attn_fwd_decode_noalloc: the problem needs more scratch
+                              than the library's fixed device buffer holds;
+                              attn_fwd_tree: the workspace is too small */
+    ATTN_ERR_PAGE = 10,    /* (attn_last_device_error) a page table entry is missing or out
+                              of range, or names a shared page that would be written */
+    ATTN_ERR_POOL = 11     /* (attn_last_device_error) the pool has not enough free pages */
 } attn_status_t;
 
 /*
@@ -248,6 +252,153 @@ attn_status_t attn_fwd_host(const void *q_h, const void *k_h, const void *v_h, v
                             float *lse_h, void *q_d, void *k_d, void *v_d, void *o_d, float *lse_d,
                             int B, int Hq, int Hkv, int Nq, int Nk, int D, float scale, int causal,
                             attn_dtype_t dtype, void *stream);
+
+/*
+ * attn_fwd_varlen -- attention over packed sequences of different lengths (the
+ * prompts of a batch, without padding), one kernel launch.
+ *
+ * Sequence s owns query rows [cu_q[s], cu_q[s+1]) of q, o and lse and rows
+ * [cu_k[s], cu_k[s+1]) of k and v.  Each of its rows attends over its keys
+ * only; with the causal mask the queries are the last Nq_s positions of the
+ * Nk_s-long sequence, as in attn_fwd_kv, so row i sees keys j <= i + Nk_s - Nq_s.
+ * A row that sees no key (causal with Nq_s > Nk_s, or no keys at all) gets
+ * o = 0 and lse = -inf.
+ *
+ * q, o    [total_q, Hq, D], k, v  [total_k, Hkv, D], 16-byte aligned; other layouts
+ *         through `strides`
+ * lse     [Hq, total_q] fp32 (written), or NULL
+ * cu_q, cu_k  device pointers, [n_seqs + 1] ints that ascend from 0; the lengths are
+ *         read on the device, so a captured call replays on new ones.  cu_k NULL: the
+ *         keys' offsets are cu_q's (total_k == total_q).  Lengths of zero are allowed.
+ *         Rows behind the last sequence are left as they are, and nothing in them, nor
+ *         in another sequence, reaches a result (not even infinities or NaN); within a
+ *         sequence a non-finite value of V reaches exactly the rows that see its key.
+ * strides host pointer, NULL for the layouts above, or 8 element strides {q row, q head,
+ *         k row, k head, v row, v head, o row, o head}, each a multiple of 8 and at
+ *         least D, the larger of a pair a multiple of the smaller and no two rows
+ *         overlapping ([heads, rows, D], or heads cut from one projection's output)
+ * Limits: total_q and total_k at most 65535 * 128.
+ * Errors: as attn_fwd_kv (no error for Nq_s > Nk_s); ATTN_ERR_SHAPE for strides.
+ *         Offsets that descend or leave the tensors are clamped, and
+ *         attn_last_device_error reports ATTN_ERR_SHAPE.
+ * Graphs, streams and ownership: as attn_fwd; no workspace.
+ */
+attn_status_t attn_fwd_varlen(const void *q, const void *k, const void *v, void *o, float *lse,
+                              const int *cu_q, const int *cu_k, int n_seqs, int total_q,
+                              int total_k, int Hq, int Hkv, int D, const long long *strides,
+                              float scale, int causal, attn_dtype_t dtype, void *stream);
+
+/*
+ * A paged key/value cache.  All pointers are device memory owned by the caller.
+ *
+ * k, v    pools [n_layers, n_pages, Hkv, page, D] contiguous, dtype, 16-byte aligned
+ * table   [n_rows, table_width]: row s lists the pages of sequence s from its first
+ *         position on, -1 behind the last; position j lies in row j % page of page
+ *         table[s][j / page].  The same page index serves every layer, K and V.
+ * lens    [n_rows] positions of each sequence
+ * refs    [n_pages] number of table entries that name the page; 0: the page is free
+ * scratch attn_kv_scratch bytes that the calls on this cache use; needs no value
+ * page    positions per page, a power of two from 16 to 4096
+ * An empty cache is table = -1, lens = 0, refs = 0.
+ *
+ * The calls below read their lists on the device and never synchronise; calls on
+ * one cache must be ordered (one stream, or events): they change its state and
+ * share its scratch.  Sequences are rows of the table; a list names each at most
+ * once unless said otherwise.  Where a list, a table or the state is wrong, the
+ * sequence is left as it was and attn_last_device_error reports ATTN_ERR_SHAPE
+ * (an index or length out of range, a sequence named twice), ATTN_ERR_PAGE or
+ * ATTN_ERR_POOL.  An empty list launches nothing.  All can be captured.
+ */
+typedef struct {
+    void *k, *v;
+    int *table, *lens, *refs, *scratch;
+    int n_layers, n_pages, page, Hkv, D, n_rows, table_width;
+    attn_dtype_t dtype;
+} attn_kv_cache_t;
+
+/* Bytes of a cache's scratch. */
+attn_status_t attn_kv_scratch(int n_pages, int n_rows, size_t *bytes);
+
+/* Makes room for n_new[i] more positions of sequence seqs[i] (i, when seqs is NULL):
+ * takes the free pages that are missing, lowest index first, and grows lens.  Requests
+ * are served in order; from the first one on that the free pages do not hold, nothing
+ * changes (ATTN_ERR_POOL). */
+attn_status_t attn_kv_extend(const attn_kv_cache_t *cache, const int *seqs, const int *n_new,
+                             int n, void *stream);
+
+/* Writes the keys and values of new tokens into their pages of one layer.  Packed rows
+ * [cu[i], cu[i+1]) of k_new, v_new [total, Hkv, D] are the last positions of sequence
+ * seqs[i] (i, when NULL), whose lens already counts them (attn_kv_extend).  strides: NULL,
+ * or 4 element strides {k row, k head, v row, v head}, multiples of 8.  A page that
+ * another sequence shares is not written (ATTN_ERR_PAGE). */
+attn_status_t attn_kv_append(const attn_kv_cache_t *cache, int layer, const void *k_new,
+                             const void *v_new, const long long *strides, const int *cu,
+                             const int *seqs, int n, int total, void *stream);
+
+/* Keeps the accepted tokens of drafted trees, in every layer.  The last
+ * T = cu[i+1] - cu[i] <= 128 positions of sequence seqs[i] (i, when NULL) are its tree's
+ * tokens; path[i][0 .. taken[i]) are the accepted ones, ascending.  Their rows move to the
+ * positions right behind those before the tree, and the sequence ends there; its pages
+ * stay with it.  path is [n, path_width]. */
+attn_status_t attn_kv_accept(const attn_kv_cache_t *cache, const int *cu, const int *seqs,
+                             const int *path, int path_width, const int *taken, int n,
+                             void *stream);
+
+/* Copies the contents of page src[i] to page dst[i], in every layer.  A page named in dst
+ * must not be named again in src or dst. */
+attn_status_t attn_kv_copy(const attn_kv_cache_t *cache, const int *src, const int *dst, int n,
+                           void *stream);
+
+/* children[i], an empty sequence, becomes a copy of parents[i]: it shares its parent's full
+ * pages, and its own last page, where that is not full, is a copy in the lowest free page.
+ * A parent may be named many times, a child once, and no child as a parent.  Served in
+ * order as attn_kv_extend. */
+attn_status_t attn_kv_fork(const attn_kv_cache_t *cache, const int *parents, const int *children,
+                           int n, void *stream);
+
+/* Empties the sequences: one reference less for each of their pages.  A sequence may be
+ * named twice. */
+attn_status_t attn_kv_free(const attn_kv_cache_t *cache, const int *seqs, int n, void *stream);
+
+/* Moves the live pages to the front of the pool, so that they are pages 0 .. live - 1: the
+ * k-th live page at or past `live` takes the place of the k-th free one before it, and the
+ * table is rewritten.  live: device pointer that receives their number, or NULL. */
+attn_status_t attn_kv_compact(const attn_kv_cache_t *cache, int *live, void *stream);
+
+/*
+ * attn_fwd_tree -- attention of drafted token trees over a paged cache; with one
+ * token per sequence, the decoding step over pages.
+ *
+ * The last T = cu[i+1] - cu[i] <= 128 positions of sequence seqs[i] (i, when seqs is NULL)
+ * are the tokens of its tree, already in the cache (attn_kv_extend, attn_kv_append); their
+ * queries are packed rows [cu[i], cu[i+1]).  Token t sees every position before the tree,
+ * its ancestors and itself.  The Hq / Hkv heads of a kv head and the tokens of a tree share
+ * each K/V tile, and the key tiles of all sequences are shared out evenly over the GPU; cut
+ * pieces are merged by a second kernel.
+ *
+ * q, o      [total_q, Hq, D], cache->dtype, 16-byte aligned; strides: NULL, or 4 element
+ *           strides {q row, q head, o row, o head} as in attn_fwd_varlen, rows outside heads
+ *           in q
+ * lse       [Hq, total_q] fp32, or NULL
+ * parents   device [total_q]: the index within its tree of each token's parent, less than
+ *           its own, or -1 for a child of the last position before the tree.  NULL: a chain
+ *           (each token follows the one before it), the causal mask.
+ * cu, seqs  device pointers; a sequence may be named twice
+ * workspace device pointer, 16-byte aligned, attn_fwd_tree_workspace bytes; needs no
+ *           value.  Calls that can run at the same time must not share it.
+ * Rows behind the last tree are left as they are.  Rows of a page past the sequence's end
+ * may hold anything; a non-finite value of V at a tree's position reaches exactly the tokens
+ * that see it.
+ * Errors: as attn_fwd_kv, ATTN_ERR_SHAPE for Hq / Hkv > 128, ATTN_ERR_SCRATCH for a small
+ * workspace; attn_last_device_error reports a tree of more than 128 tokens or of more than
+ * the sequence's positions and bad offsets or sequences (ATTN_ERR_SHAPE), whose rows are then
+ * undefined, and missing pages (ATTN_ERR_PAGE), which read as zeros.
+ */
+attn_status_t attn_fwd_tree_workspace(int n_seqs, int D, size_t *bytes);
+attn_status_t attn_fwd_tree(const void *q, const attn_kv_cache_t *cache, int layer, void *o,
+                            float *lse, const int *cu, const int *seqs, const int *parents,
+                            int n_seqs, int total_q, int Hq, const long long *strides,
+                            float scale, void *workspace, size_t workspace_bytes, void *stream);
 
 /* Static, human-readable name of a status code. */
 const char *attn_status_str(attn_status_t status);
