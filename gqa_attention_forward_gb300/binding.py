@@ -42,6 +42,8 @@ class KVCache(ctypes.Structure):
 def load(path: str | None = None):
     """Load the built library (no build here: a missing library is an error)."""
     global _lib
+    if _lib is not None and path is None:
+        return _lib
     with _lock:
         if _lib is not None and path is None:
             return _lib
@@ -335,6 +337,9 @@ def attention(q, k, v, causal: bool = True, scale: float | None = None, with_lse
 
 
 # ------------------------------------------------------------------ packed sequences
+_Strides4, _Strides8 = ctypes.c_longlong * 4, ctypes.c_longlong * 8
+
+
 def _strides(values):
     """Element strides as the C entry points take them (None stays None)."""
     return None if values is None else (ctypes.c_longlong * len(values))(*values)
@@ -350,67 +355,81 @@ def attn_fwd_varlen(q, k, v, o, lse, cu_q, cu_k, n_seqs, total_q, total_k, Hq, H
                                   _stream_handle(stream))
 
 
+_torch_module = None
+
+
+def _torch():
+    """torch, imported on first use."""
+    global _torch_module
+    if _torch_module is None:
+        import torch
+
+        _torch_module = torch
+    return _torch_module
+
+
+# What the calls below do per call on the host is kept short: with one short prompt or one
+# draft tree the launch and this code take longer than the kernel.
 def _rows(t, name):
-    """(rows, heads, D) of a packed tensor and its row and head strides."""
-    if t.dim() != 3 or t.stride(2) != 1:
+    """(rows, heads, D) of a packed tensor and its strides."""
+    s = t.stride()
+    if len(s) != 3 or s[2] != 1:
         raise ValueError(f"{name} must be [tokens, heads, D] with the last axis contiguous")
-    return t.shape, (t.stride(0), t.stride(1))
+    return t.shape, s
 
 
-def _ints(t, name, device, shape=None):
-    """Checks an int32 index tensor."""
-    import torch
-
-    if t.dtype != torch.int32 or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 tensor on {device}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+def _ints(t, name, dev, shape=None):
+    """Checks an int32 index tensor on device number ``dev`` (-1: the host)."""
+    if t.dtype != _torch().int32 or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor on the device of the others")
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
     return t
 
 
-def _same(t, name, dtype, device):
-    if t.dtype != dtype or t.device != device:
-        raise ValueError(f"{name} must be {dtype} on {device}")
+def _same(t, name, dtype, dev):
+    if t.dtype != dtype or t.get_device() != dev:
+        raise ValueError(f"{name} must be {dtype} on the device of the others")
 
 
-def _launch(what, device, stream, call):
-    """Runs call(stream handle) with ``device`` current; raises AttnError unless it succeeds."""
-    import torch
-
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-    if device.index is None or device.index == torch.cuda.current_device():
-        st = call(_stream_handle(stream))
+def _run(what, dev, stream, entry, *args):
+    """entry(*args, stream handle) with device ``dev`` current; raises AttnError unless it succeeds."""
+    torch = _torch()
+    handle = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream_handle(stream)
+    if torch._C._cuda_getDevice() == dev:
+        st = entry(*args, handle)
     else:
-        with torch.cuda.device(device):
-            st = call(_stream_handle(stream))
+        with torch.cuda.device(dev):
+            st = entry(*args, handle)
     if st != ATTN_OK:
         raise AttnError(st, f"{what} ({attn_last_cuda_error()})")
 
 
-def _outputs(q, Hq, total, with_lse, out, lse_out, stream):
-    """The output tensors: given ones are checked; new ones belong to ``stream`` too."""
-    import torch
+def _new(q, shape, dtype, stream):
+    """A new tensor beside q; memory of the current stream that ``stream`` uses is kept until then."""
+    t = q.new_empty(shape, dtype=dtype)
+    if stream is not None and not isinstance(stream, int):
+        t.record_stream(stream)
+    return t
 
+
+def _outputs(q, dev, Hq, total, with_lse, out, lse_out, stream):
+    """The output tensors: new ones, or the given ones checked."""
+    torch = _torch()
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        if stream is not None and not isinstance(stream, int):
-            out.record_stream(stream)
+        out = _new(q, q.shape, q.dtype, stream)
     else:
-        _same(out, "out", q.dtype, q.device)
+        _same(out, "out", q.dtype, dev)
         if out.shape != q.shape:
             raise ValueError(f"out must have shape {tuple(q.shape)}")
-    lse = None
-    if with_lse:
-        lse = lse_out
-        if lse is None:
-            lse = torch.empty((Hq, total), dtype=torch.float32, device=q.device)
-            if stream is not None and not isinstance(stream, int):
-                lse.record_stream(stream)
-        elif lse.dtype != torch.float32 or lse.device != q.device or tuple(lse.shape) != (Hq, total) \
-                or not lse.is_contiguous():
-            raise ValueError(f"lse_out must be contiguous float32 [{Hq}, {total}] on {q.device}")
-    return out, lse
+    if not with_lse:
+        return out, None
+    if lse_out is None:
+        return out, _new(q, (Hq, total), torch.float32, stream)
+    _same(lse_out, "lse_out", torch.float32, dev)
+    if lse_out.shape != (Hq, total) or not lse_out.is_contiguous():
+        raise ValueError(f"lse_out must be contiguous [{Hq}, {total}]")
+    return out, lse_out
 
 
 def attention_varlen(q, k, v, cu_q, cu_k=None, causal: bool = True, scale: float | None = None,
@@ -421,25 +440,29 @@ def attention_varlen(q, k, v, cu_q, cu_k=None, causal: bool = True, scale: float
     ``cu_q`` (and ``cu_k`` where the keys' offsets differ): int32 [n_seqs + 1] offsets on the
     device, never read by the host.  Returns (o [total_q,Hq,D], lse [Hq,total_q]) without waiting;
     rows behind the last sequence are not written."""
-    (total_q, Hq, D), sq = _rows(q, "q")
-    (total_k, Hkv, Dk), sk = _rows(k, "k")
-    (total_v, Hv, Dv), sv = _rows(v, "v")
-    if (total_v, Hv, Dv) != (total_k, Hkv, Dk) or Dk != D:
+    shape, sq = _rows(q, "q")
+    kshape, sk = _rows(k, "k")
+    vshape, sv = _rows(v, "v")
+    total_q, Hq, D = shape
+    total_k, Hkv, Dk = kshape
+    if vshape != kshape or Dk != D:
         raise ValueError("k and v must have one shape [total_k, Hkv, D] with q's D")
-    for t, name in ((k, "k"), (v, "v")):
-        _same(t, name, q.dtype, q.device)
-    _ints(cu_q, "cu_q", q.device)
+    dev, dtype = q.get_device(), q.dtype
+    _same(k, "k", dtype, dev)
+    _same(v, "v", dtype, dev)
+    _ints(cu_q, "cu_q", dev)
     if cu_q.dim() != 1 or cu_q.numel() < 1:
         raise ValueError("cu_q must hold n_seqs + 1 offsets")
     if cu_k is not None:
-        _ints(cu_k, "cu_k", q.device, cu_q.shape)
-    o, lse = _outputs(q, Hq, total_q, with_lse, out, lse_out, stream)
-    so = _rows(o, "out")[1]
-    if scale is None:
-        scale = 1.0 / math.sqrt(D)
-    _launch("attn_fwd_varlen", q.device, stream, lambda s: attn_fwd_varlen(
-        q, k, v, o, lse, cu_q, cu_k, cu_q.numel() - 1, total_q, total_k, Hq, Hkv, D, sq + sk + sv + so,
-        scale, causal, q.dtype, s))
+        _ints(cu_k, "cu_k", dev, cu_q.shape)
+    o, lse = _outputs(q, dev, Hq, total_q, with_lse, out, lse_out, stream)
+    so = o.stride()
+    if so[2] != 1:
+        raise ValueError("out must have its last axis contiguous")
+    _run("attn_fwd_varlen", dev, stream, load().attn_fwd_varlen, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+         o.data_ptr(), _ptr(lse), cu_q.data_ptr(), _ptr(cu_k), cu_q.numel() - 1, total_q, total_k, Hq, Hkv, D,
+         _Strides8(sq[0], sq[1], sk[0], sk[1], sv[0], sv[1], so[0], so[1]),
+         D ** -0.5 if scale is None else scale, 1 if causal else 0, _dtype_code(dtype))
     return o, lse
 
 
@@ -467,27 +490,29 @@ class KVPages:
 
         if k.dim() != 5 or v.shape != k.shape or not (k.is_contiguous() and v.is_contiguous()):
             raise ValueError("k and v must be contiguous [n_layers, n_pages, Hkv, page, D]")
-        _same(v, "v", k.dtype, k.device)
+        _same(v, "v", k.dtype, k.get_device())
         n_layers, n_pages, Hkv, page, D = k.shape
         if table.dim() != 2:
             raise ValueError("table must be [n_rows, table_width]")
-        _ints(table, "table", k.device)
-        _ints(lens, "lens", k.device, (table.shape[0],))
-        _ints(refs, "refs", k.device, (n_pages,))
+        dev = k.get_device()
+        _ints(table, "table", dev)
+        _ints(lens, "lens", dev, (table.shape[0],))
+        _ints(refs, "refs", dev, (n_pages,))
         st, nbytes = attn_kv_scratch(n_pages, table.shape[0])
         if st != ATTN_OK:
             raise AttnError(st, "attn_kv_scratch")
         if scratch is None:
             scratch = torch.empty(nbytes // 4, dtype=torch.int32, device=k.device)
-        _ints(scratch, "scratch", k.device)
+        _ints(scratch, "scratch", dev)
         if scratch.numel() * 4 < nbytes:
             raise ValueError(f"scratch must hold {nbytes // 4} ints")
         self.k, self.v, self.table, self.lens, self.refs, self.scratch = k, v, table, lens, refs, scratch
-        self.device = k.device
+        self.device, self.dev, self.dtype = k.device, dev, k.dtype
         self.n_rows, self.table_width = table.shape
         self.n_layers, self.n_pages, self.Hkv, self.page, self.D = n_layers, n_pages, Hkv, page, D
         self.c = KVCache(_ptr(k), _ptr(v), _ptr(table), _ptr(lens), _ptr(refs), _ptr(scratch), n_layers,
                          n_pages, page, Hkv, D, self.n_rows, self.table_width, _dtype_code(k.dtype))
+        self.ref = ctypes.byref(self.c)
 
     @classmethod
     def empty(cls, n_layers, n_pages, Hkv, page, D, n_rows, table_width, dtype, device="cuda"):
@@ -560,81 +585,82 @@ def attn_fwd_tree(q, cache, layer, o, lse, cu, seqs, parents, n_seqs, total_q, H
 
 
 def _list(t, name, cache, n=None):
-    """An int32 list on the cache's device (None stays None)."""
+    """Checks an int32 list on the cache's device (None is taken); returns its length."""
     if t is None:
-        return None
+        return n
     if t.dim() != 1:
         raise ValueError(f"{name} must be one-dimensional")
-    return _ints(t, name, cache.device, None if n is None else (n,))
+    _ints(t, name, cache.dev, None if n is None else (n,))
+    return t.shape[0]
 
 
 def kv_extend(cache, n_new, seqs=None, stream=None):
     """attn_kv_extend: room for n_new[i] more positions of sequence seqs[i] (i, when None)."""
-    n = _list(n_new, "n_new", cache).numel()
+    n = _list(n_new, "n_new", cache)
     _list(seqs, "seqs", cache, n)
-    _launch("attn_kv_extend", cache.device, stream, lambda s: attn_kv_extend(cache, seqs, n_new, n, s))
+    _run("attn_kv_extend", cache.dev, stream, load().attn_kv_extend, cache.ref, _ptr(seqs), n_new.data_ptr(), n)
 
 
 def kv_append(cache, k_new, v_new, cu, seqs=None, layer: int = 0, stream=None):
     """attn_kv_append: packed rows k_new, v_new [total,Hkv,D] become the last positions of the
     sequences (offsets ``cu`` [n + 1]), whose lens already counts them."""
-    (total, Hkv, D), sk = _rows(k_new, "k_new")
-    (total_v, Hv, Dv), sv = _rows(v_new, "v_new")
-    if (total, Hkv, D) != (total_v, Hv, Dv) or (Hkv, D) != (cache.Hkv, cache.D):
+    shape, sk = _rows(k_new, "k_new")
+    vshape, sv = _rows(v_new, "v_new")
+    if shape != vshape or shape[1] != cache.Hkv or shape[2] != cache.D:
         raise ValueError("k_new and v_new must be [total, Hkv, D] with the cache's Hkv and D")
-    for t, name in ((k_new, "k_new"), (v_new, "v_new")):
-        _same(t, name, cache.k.dtype, cache.device)
-    n = _list(cu, "cu", cache).numel() - 1
+    _same(k_new, "k_new", cache.dtype, cache.dev)
+    _same(v_new, "v_new", cache.dtype, cache.dev)
+    n = _list(cu, "cu", cache) - 1
     _list(seqs, "seqs", cache, n)
-    _launch("attn_kv_append", cache.device, stream, lambda s: attn_kv_append(
-        cache, layer, k_new, v_new, sk + sv, cu, seqs, n, total, s))
+    _run("attn_kv_append", cache.dev, stream, load().attn_kv_append, cache.ref, layer, k_new.data_ptr(),
+         v_new.data_ptr(), _Strides4(sk[0], sk[1], sv[0], sv[1]), cu.data_ptr(), _ptr(seqs), n, shape[0])
 
 
 def kv_accept(cache, cu, path, taken, seqs=None, stream=None):
     """attn_kv_accept: of each tree (offsets ``cu``), the tokens path[i, :taken[i]] stay."""
-    n = _list(cu, "cu", cache).numel() - 1
+    n = _list(cu, "cu", cache) - 1
     _list(seqs, "seqs", cache, n)
     _list(taken, "taken", cache, n)
     if path.dim() != 2 or path.shape[0] != n:
         raise ValueError("path must be [n, path_width]")
-    _ints(path, "path", cache.device)
-    _launch("attn_kv_accept", cache.device, stream, lambda s: attn_kv_accept(
-        cache, cu, seqs, path, path.shape[1], taken, n, s))
+    _ints(path, "path", cache.dev)
+    _run("attn_kv_accept", cache.dev, stream, load().attn_kv_accept, cache.ref, cu.data_ptr(), _ptr(seqs),
+         path.data_ptr(), path.shape[1], taken.data_ptr(), n)
 
 
 def kv_copy(cache, src, dst, stream=None):
     """attn_kv_copy: the contents of pages src[i] go to pages dst[i], in every layer."""
-    n = _list(src, "src", cache).numel()
+    n = _list(src, "src", cache)
     _list(dst, "dst", cache, n)
-    _launch("attn_kv_copy", cache.device, stream, lambda s: attn_kv_copy(cache, src, dst, n, s))
+    _run("attn_kv_copy", cache.dev, stream, load().attn_kv_copy, cache.ref, src.data_ptr(), dst.data_ptr(), n)
 
 
 def kv_fork(cache, parents, children, stream=None):
     """attn_kv_fork: the empty sequences children[i] become copies of parents[i]."""
-    n = _list(parents, "parents", cache).numel()
+    n = _list(parents, "parents", cache)
     _list(children, "children", cache, n)
-    _launch("attn_kv_fork", cache.device, stream, lambda s: attn_kv_fork(cache, parents, children, n, s))
+    _run("attn_kv_fork", cache.dev, stream, load().attn_kv_fork, cache.ref, parents.data_ptr(),
+         children.data_ptr(), n)
 
 
 def kv_free(cache, seqs, stream=None):
     """attn_kv_free: the sequences become empty and give their pages back."""
-    n = _list(seqs, "seqs", cache).numel()
-    _launch("attn_kv_free", cache.device, stream, lambda s: attn_kv_free(cache, seqs, n, s))
+    n = _list(seqs, "seqs", cache)
+    _run("attn_kv_free", cache.dev, stream, load().attn_kv_free, cache.ref, seqs.data_ptr(), n)
 
 
 def kv_compact(cache, live=None, stream=None):
     """attn_kv_compact: the live pages become pages 0 .. live - 1.  Returns the int32 [1] tensor
     that receives ``live``."""
-    import torch
-
     if live is None:
-        live = torch.empty(1, dtype=torch.int32, device=cache.device)
-        if stream is not None and not isinstance(stream, int):
-            live.record_stream(stream)
+        live = _new(cache.lens, (1,), cache.lens.dtype, stream)
     else:
-        _ints(live, "live", cache.device, (1,))
-    _launch("attn_kv_compact", cache.device, stream, lambda s: attn_kv_compact(cache, live, s))
+        _ints(live, "live", cache.dev, (1,))
+    _run("attn_kv_compact", cache.dev, stream, load().attn_kv_compact, cache.ref, live.data_ptr())
     return live
+
+
+_tree_bytes = {}  # (device number, sequences, D) -> bytes of attn_fwd_tree_workspace
 
 
 def attention_tree(q, cache, cu, seqs=None, parents=None, layer: int = 0, scale: float | None = None,
@@ -645,27 +671,34 @@ def attention_tree(q, cache, cu, seqs=None, parents=None, layer: int = 0, scale:
 
     ``workspace``: a uint8 CUDA tensor, or None to let torch allocate the size that
     attn_fwd_tree_workspace asks for.  Returns (o [total,Hq,D], lse [Hq,total]) without waiting."""
-    import torch
-
+    torch = _torch()
     (total, Hq, D), sq = _rows(q, "q")
-    _same(q, "q", cache.k.dtype, cache.device)
+    dev = cache.dev
+    _same(q, "q", cache.dtype, dev)
     if D != cache.D or Hq % cache.Hkv != 0:
         raise ValueError("q must be [total, Hq, D] with the cache's D and Hq a multiple of its Hkv")
-    n = _list(cu, "cu", cache).numel() - 1
+    n = _list(cu, "cu", cache) - 1
     _list(seqs, "seqs", cache, n)
     _list(parents, "parents", cache, total)
-    o, lse = _outputs(q, Hq, total, with_lse, out, lse_out, stream)
-    so = _rows(o, "out")[1]
-    if scale is None:
-        scale = 1.0 / math.sqrt(D)
+    o, lse = _outputs(q, dev, Hq, total, with_lse, out, lse_out, stream)
+    so = o.stride()
+    if so[2] != 1:
+        raise ValueError("out must have its last axis contiguous")
     if workspace is None:
-        st, nbytes = attn_fwd_tree_workspace(n, D)
-        if st != ATTN_OK:
-            raise AttnError(st, "attn_fwd_tree_workspace")
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
-        if stream is not None and not isinstance(stream, int):
-            workspace.record_stream(stream)
-    _launch("attn_fwd_tree", q.device, stream, lambda s: attn_fwd_tree(
-        q, cache, layer, o, lse, cu, seqs, parents, n, total, Hq, sq + so, scale, workspace,
-        workspace.numel(), s))
+        nbytes = _tree_bytes.get((dev, n, D))
+        if nbytes is None:
+            with torch.cuda.device(dev):
+                st, nbytes = attn_fwd_tree_workspace(n, D)
+            if st != ATTN_OK:
+                raise AttnError(st, "attn_fwd_tree_workspace")
+            _tree_bytes[dev, n, D] = nbytes
+        workspace = _new(q, (nbytes,), torch.uint8, stream)
+    else:
+        nbytes = workspace.numel()
+        _same(workspace, "workspace", torch.uint8, dev)
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+    _run("attn_fwd_tree", dev, stream, load().attn_fwd_tree, q.data_ptr(), cache.ref, layer, o.data_ptr(),
+         _ptr(lse), cu.data_ptr(), _ptr(seqs), _ptr(parents), n, total, Hq, _Strides4(sq[0], sq[1], so[0], so[1]),
+         D ** -0.5 if scale is None else scale, workspace.data_ptr(), nbytes)
     return o, lse

@@ -28,8 +28,15 @@
 // move down the levels.
 //
 // Roles (384 threads): warp 0 MMA issuer, warp 1 value guard (and TMEM), warp 2 TMA
-// producer, warp 3 scheduler, warps 4-7 and 8-11 the softmax of tile 0 and 1; shared
-// memory, TMEM and the K/V ring are laid out as in the equal-length kernel.
+// producer, warp 3 scheduler, warps 4-7 and 8-11 the softmax of tile 0 and 1.  Shared memory,
+// TMEM and the K/V ring are laid out as in the equal-length kernel.  Units follow each other
+// without a pause: the next unit's first K tile is loaded with the last V tile of the unit
+// before, its first scores are computed right after that unit's last P V of the same tile,
+// and a softmax warp stores O of a unit only after it has handed over the first weights of
+// the next one, when the last P V has long finished.
+//
+// Rounding.  P is rounded to the input type, against a stale row max (weights up to 2^8 of the
+// reference): half a step of each weight, the same as the output's own rounding.
 //
 // Value guard.  A 128-row V box of the last key tile reaches into the next sequence (or
 // into rows behind the last one, which may hold anything), and P = 0 times infinity or
@@ -78,17 +85,16 @@ template <int D>
 struct VlLayout {
     using W = WsLayout<D>;
     static constexpr int kTileBytes = W::kTileBytes;
-    static constexpr int kQ = W::kQ, kKV = W::kKV, kStage = W::kStage;
-    static constexpr int kStageBytes = W::kStageBytes;
+    static constexpr int kQ = W::kQ, kKV = W::kKV;
+    static constexpr int kStageBytes = W::kStageBytes;  // epilogue staging of a softmax warp
+    static constexpr int kStage = kKV + kStagesWs * kTileBytes;
     static constexpr int kBar = kStage + 8 * kStageBytes;
-    // q_full[2], q_empty, kv_full[S], kv_empty[S], s_full[2], p_full[2], o_full[2], mma_done,
-    // v_ask, v_ok, unit_full[slots], unit_empty[slots]
-    static constexpr int kNumBars = 2 + 1 + 2 * kStagesWs + 2 + 2 + 2 + 1 + 2 + 2 * kVlSlots;
-    static constexpr int kFlags = kBar + kNumBars * 8;
-    static constexpr int kTmemSlot = kFlags + 32;
+    // q_full[2], kv_full[S], kv_empty[S], s_full[2], p_full[2], o_full[2], o_empty[2], mma_done,
+    // v_ok[2], unit_full[slots], unit_empty[slots]
+    static constexpr int kNumBars = 2 + 2 * kStagesWs + 4 * 2 + 1 + 2 + 2 * kVlSlots;
+    static constexpr int kTmemSlot = kBar + kNumBars * 8;
     static constexpr int kAbort = kTmemSlot + 4;
-    static constexpr int kAsk = kAbort + 4;
-    static constexpr int kUnits = (kAsk + 4 + 15) & ~15;
+    static constexpr int kUnits = (kAbort + 4 + 15) & ~15;
     static constexpr int kSeqs = kUnits + kVlSlots * static_cast<int>(sizeof(VlUnit));
     static constexpr int kUsed = kSeqs + kVlSeqCache * 4;
     static constexpr int kAlloc = (kUsed + 1024) > 118 * 1024 ? (kUsed + 1024) : 118 * 1024;
@@ -208,6 +214,65 @@ struct VlWalk {
     }
 };
 
+// 16 consecutive 32-bit TMEM columns of this thread's lane (warp-collective).
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+
+// The two products of a key tile, with the matrix descriptors of sdesc_sw128 put together in
+// the instruction's own block: the upper word is a constant, the lower one (start address and
+// leading offset, in 16-byte units) a base plus a constant, so that one register per operand is
+// live and nothing is hoisted out of the issuer's loop (hoisted descriptors spilled there).
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // stride 1024 B, version 1, swizzle 128 B
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo_bytes) {
+    return ((saddr & 0x3FFFFu) >> 4) | ((lbo_bytes >> 4) << 16);
+}
+// D[tmem] (+)= A[smem + off] B[smem + off]^T
+template <uint32_t kIdesc, uint32_t kOff, bool kAcc>
+__device__ __forceinline__ void mma_ss_at(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b32 x, y, h, i;\n\t.reg .b64 a, b;\n\t"
+        "add.u32 x, %1, %5;\n\tadd.u32 y, %2, %5;\n\tmov.u32 h, %3;\n\tmov.u32 i, %4;\n\t"
+        "mov.b64 a, {x, h};\n\tmov.b64 b, {y, h};\n\tsetp.ne.u32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, i, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(b_lo), "n"(kDescHi), "n"(kIdesc), "n"(kOff), "n"(kAcc ? 1 : 0)
+        : "memory");
+}
+// D[tmem] (+)= A[tmem + off_a] B[smem + off]^T
+template <uint32_t kIdesc, uint32_t kOffA, uint32_t kOff>
+__device__ __forceinline__ void mma_ts_at(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b32 x, y, h, i;\n\t.reg .b64 b;\n\t"
+        "add.u32 x, %1, %5;\n\tadd.u32 y, %2, %6;\n\tmov.u32 h, %3;\n\tmov.u32 i, %4;\n\t"
+        "mov.b64 b, {y, h};\n\tsetp.ne.u32 p, %7, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, i, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b_lo), "n"(kDescHi), "n"(kIdesc), "n"(kOffA), "n"(kOff), "r"(acc)
+        : "memory");
+}
+// S = Q K^T of one 128 x 128 tile (K-major operands), and O (+)= P V (P in TMEM, V MN-major)
+template <int D, bool kBF16, int kk = 0>
+__device__ __forceinline__ void mma_qk(uint32_t td, uint32_t q_lo, uint32_t k_lo) {
+    if constexpr (kk < D / 16) {
+        mma_ss_at<idesc_f16_f32acc(kBF16, 128, kBN, false), (kk >> 2) * (kAtomBytes >> 4) + (kk & 3) * 2, (kk > 0)>(
+            td, q_lo, k_lo);
+        mma_qk<D, kBF16, kk + 1>(td, q_lo, k_lo);
+    }
+}
+template <int D, bool kBF16, int kk = 0>
+__device__ __forceinline__ void mma_pv(uint32_t to, uint32_t tp, uint32_t v_lo, uint32_t acc) {
+    if constexpr (kk < kBN / 16) {
+        mma_ts_at<idesc_f16_f32acc(kBF16, 128, D, true), 8u * kk, kk * (2048 >> 4)>(to, tp, v_lo, kk > 0 ? 1u : acc);
+        mma_pv<D, kBF16, kk + 1>(to, tp, v_lo, acc);
+    }
+}
+
 // Packed 16-bit magnitudes: a value is infinite or NaN when its exponent bits are all set.
 template <bool kBF16>
 __device__ __forceinline__ bool nonfinite16(uint32_t h) {
@@ -215,12 +280,34 @@ __device__ __forceinline__ bool nonfinite16(uint32_t h) {
     return (h & kExp) == kExp;
 }
 
+// 0 * x + acc in both 16-bit halves: acc, or NaN from the first non-finite value on.
+template <bool kBF16>
+__device__ __forceinline__ uint32_t zero_times(uint32_t x, uint32_t acc) {
+    uint32_t d;
+    if constexpr (kBF16)
+        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(x), "r"(0u), "r"(acc));
+    else
+        asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(x), "r"(0u), "r"(acc));
+    return d;
+}
+
+// Adds the non-finite values of a row of V to a stored row of O.
+template <int D, bool kBF16>
+__device__ __forceinline__ void add_nonfinite(uint8_t *o_row, const uint8_t *v_row) {
+#pragma unroll 1
+    for (int d = 0; d < D; ++d) {
+        const uint32_t x = reinterpret_cast<const uint16_t *>(v_row)[d];
+        if (!nonfinite16<kBF16>(x)) continue;
+        volatile uint16_t *o = reinterpret_cast<volatile uint16_t *>(o_row) + d;
+        *o = static_cast<uint16_t>(pack2<kBF16>(unpack2<kBF16>(*o).x + unpack2<kBF16>(x).x, 0.f));
+    }
+}
+
 // The guard's work on one V tile in shared memory: rows at or past `rows` become zero;
 // with `scan`, non-finite values of the rows before are zeroed and their rows noted.
 template <int D, bool kBF16>
 __device__ __forceinline__ bool vl_guard_tile(uint8_t *tile, int rows, bool scan, uint32_t *bad_rows, int lane) {
     constexpr int kAtoms = D / 64;
-    constexpr uint32_t kInf = kBF16 ? 0x7F80u : 0x7C00u;
     const uint4 zero = make_uint4(0, 0, 0, 0);
     bool any = false;
 #pragma unroll
@@ -228,15 +315,19 @@ __device__ __forceinline__ bool vl_guard_tile(uint8_t *tile, int rows, bool scan
         uint4 *atom = reinterpret_cast<uint4 *>(tile + a * kAtomBytes);  // 8 chunks of 16 bytes a row
         for (int i = rows * 8 + lane; i < kBN * 8; i += 32) atom[i] = zero;
         if (!scan) continue;
-        uint32_t m0 = 0, m1 = 0;  // largest magnitudes, two 16-bit lanes each
+        // 0 times a value, summed: NaN exactly where one is not finite.  The rows past the end are
+        // zeros by now, so all 128 are taken, with a fixed count of loads in flight.
+        __syncwarp();
+        uint32_t sum[4] = {0u, 0u, 0u, 0u};
 #pragma unroll 8
-        for (int i = lane; i < rows * 8; i += 32) {
-            const uint4 x = atom[i];
-            m0 = __vimax3_u16x2(m0, x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu);
-            m1 = __vimax3_u16x2(m1, x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu);
+        for (int i = 0; i < kBN * 8 / 32; ++i) {
+            const uint4 x = atom[i * 32 + lane];
+            sum[0] = zero_times<kBF16>(x.x, sum[0]);
+            sum[1] = zero_times<kBF16>(x.y, sum[1]);
+            sum[2] = zero_times<kBF16>(x.z, sum[2]);
+            sum[3] = zero_times<kBF16>(x.w, sum[3]);
         }
-        m0 = __vmaxu2(m0, m1);
-        if (!__any_sync(0xffffffffu, (m0 & 0xFFFFu) >= kInf || (m0 >> 16) >= kInf)) continue;
+        if (!__any_sync(0xffffffffu, ((sum[0] | sum[1] | sum[2] | sum[3]) & 0x7FFF7FFFu) != 0)) continue;
         any = true;
         for (int i = lane; i < rows * 8; i += 32) {
             uint4 x = atom[i];
@@ -270,21 +361,18 @@ __global__ void __launch_bounds__(kWsThreads, 1)
     const uint32_t sQ = base + L::kQ, sKV = base + L::kKV;
     const uint32_t bar0 = base + L::kBar;
     auto q_full = [&](int i) { return bar0 + 8u * i; };
-    const uint32_t q_empty = bar0 + 8u * 2;
-    auto kv_full = [&](int s) { return bar0 + 8u * (3 + s); };
-    auto kv_empty = [&](int s) { return bar0 + 8u * (3 + kStagesWs + s); };
-    auto s_full = [&](int i) { return bar0 + 8u * (3 + 2 * kStagesWs + i); };
-    auto p_full = [&](int i) { return bar0 + 8u * (5 + 2 * kStagesWs + i); };
-    auto o_full = [&](int i) { return bar0 + 8u * (7 + 2 * kStagesWs + i); };
-    const uint32_t mma_done = bar0 + 8u * (9 + 2 * kStagesWs);
-    const uint32_t v_ask = bar0 + 8u * (10 + 2 * kStagesWs), v_ok = bar0 + 8u * (11 + 2 * kStagesWs);
-    auto unit_full = [&](int s) { return bar0 + 8u * (12 + 2 * kStagesWs + s); };
-    auto unit_empty = [&](int s) { return bar0 + 8u * (12 + 2 * kStagesWs + kVlSlots + s); };
-    volatile int *ask = reinterpret_cast<volatile int *>(smem + L::kAsk);
+    auto kv_full = [&](int s) { return bar0 + 8u * (2 + s); };
+    auto kv_empty = [&](int s) { return bar0 + 8u * (2 + kStagesWs + s); };
+    auto s_full = [&](int i) { return bar0 + 8u * (2 + 2 * kStagesWs + i); };
+    auto p_full = [&](int i) { return bar0 + 8u * (4 + 2 * kStagesWs + i); };
+    auto o_full = [&](int i) { return bar0 + 8u * (6 + 2 * kStagesWs + i); };
+    auto o_empty = [&](int i) { return bar0 + 8u * (8 + 2 * kStagesWs + i); };  // O_i has been read
+    const uint32_t mma_done = bar0 + 8u * (10 + 2 * kStagesWs);
+    auto v_ok = [&](int b) { return bar0 + 8u * (11 + 2 * kStagesWs + b); };  // stage 1, 3 has passed the guard
+    auto unit_full = [&](int s) { return bar0 + 8u * (13 + 2 * kStagesWs + s); };
+    auto unit_empty = [&](int s) { return bar0 + 8u * (13 + 2 * kStagesWs + kVlSlots + s); };
     volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(smem + L::kTmemSlot);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kAbort);
-    volatile uint32_t *flags = reinterpret_cast<volatile uint32_t *>(smem + L::kFlags);
-    auto split_flag = [&](int i, int w) -> volatile uint32_t & { return flags[4 * i + w]; };
     VlUnit *units = reinterpret_cast<VlUnit *>(smem + L::kUnits);
     uint32_t *seqs = reinterpret_cast<uint32_t *>(smem + L::kSeqs);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -297,21 +385,19 @@ __global__ void __launch_bounds__(kWsThreads, 1)
     }
     if (threadIdx.x == 0) {
         *abort_flag = 0;
-        mbar_init(q_full(0), 1);
-        mbar_init(q_full(1), 1);
-        mbar_init(q_empty, 1);
         for (int s = 0; s < kStagesWs; ++s) {
             mbar_init(kv_full(s), 1);
-            mbar_init(kv_empty(s), 1);
+            mbar_init(kv_empty(s), 1 + (s & 1));  // V (the odd stages) is freed by the issuer and the guard
         }
         for (int i = 0; i < 2; ++i) {
+            mbar_init(v_ok(i), 1);
+            mbar_init(q_full(i), 1);
             mbar_init(s_full(i), 1);
-            mbar_init(p_full(i), 4);  // one arrival per softmax warp
+            mbar_init(p_full(i), 4);  // one arrival per softmax warp of the tile
             mbar_init(o_full(i), 1);
+            mbar_init(o_empty(i), 4);
         }
         mbar_init(mma_done, 1);
-        mbar_init(v_ask, 1);
-        mbar_init(v_ok, 1);
         for (int s = 0; s < kVlSlots; ++s) {
             mbar_init(unit_full(s), 1);
             mbar_init(unit_empty(s), 11);  // producer, MMA issuer, guard, 8 softmax warps
@@ -376,56 +462,78 @@ __global__ void __launch_bounds__(kWsThreads, 1)
             }
         } else if (warp == 2 && lane == 0) {
             // ---------------------------------------------------- TMA producer
+            // The ring holds K_0, then V_j and the K tile after it (K_{j+1}, or the next unit's
+            // K_0) in pairs that complete V_j's barrier together, so that the issuer waits once
+            // per key tile; every stage keeps its own phase bit (fph).
+            struct Cur {
+                int valid, n, n0, n1, q0, q1, head, k0;
+            };
             Ring ring;
             int slot = 0;
-            uint32_t uphase = 0;
-            uint32_t fph = 0, armed = 0;  // full barriers as in the equal-length kernel
-            int q_loads[2] = {0, 0}, q_units = 0;
-            bool ok = true;
+            uint32_t uphase = 0, fph = 0, armed = 0;
+            uint32_t scores[2] = {0, 0};  // score tiles of the units before, per query tile
+            int q_loads[2] = {0, 0};
             auto issue = [&](uint32_t dst, const CUtensorMap *tm, int head_y, int row, int head, uint32_t bar) {
 #pragma unroll
                 for (int a = 0; a < D / 64; ++a)
                     tma_load_3d(dst + a * kAtomBytes, tm, 64 * a, head_y ? head : row, head_y ? row : head, bar);
             };
-            while (ok) {
-                if (!wait_bar(unit_full(slot), uphase, p, abort_flag)) break;
-                const VlUnit u = units[slot];
-                mbar_arrive(unit_empty(slot));
-                if (++slot == kVlSlots) {
-                    slot = 0;
-                    uphase ^= 1u;
+            // the next unit that has keys to load (valid 0: none)
+            auto fetch = [&](Cur &c) -> bool {
+                for (;;) {
+                    if (!wait_bar(unit_full(slot), uphase, p, abort_flag)) return false;
+                    const VlUnit &u = units[slot];
+                    c.valid = u.valid;
+                    if (c.valid) {
+                        const VlTile t0 = vl_tile<kCausal>(p, u, 0), t1 = vl_tile<kCausal>(p, u, 1);
+                        c.n0 = t0.n;
+                        c.n1 = t1.n;
+                        c.n = t0.n > t1.n ? t0.n : t1.n;
+                        c.q0 = u.q0;
+                        c.q1 = u.q0 + t1.row0;
+                        c.head = u.head;
+                        c.k0 = u.k0;
+                    }
+                    mbar_arrive(unit_empty(slot));
+                    if (++slot == kVlSlots) {
+                        slot = 0;
+                        uphase ^= 1u;
+                    }
+                    if (!c.valid || c.n > 0) return true;
                 }
-                if (!u.valid) break;
-                const VlTile t0 = vl_tile<kCausal>(p, u, 0), t1 = vl_tile<kCausal>(p, u, 1);
-                const int n = t0.n > t1.n ? t0.n : t1.n;
-                if (n == 0) continue;
-                const int kvh = u.head / p.group;
-                // first K tile: its own full barrier
-                if (!(ok = wait_bar(kv_empty(ring.s), ring.ph ^ 1u, p, abort_flag))) break;
-                mbar_arrive_expect_tx(kv_full(ring.s), L::kTileBytes);
-                armed |= 1u << ring.s;
-                fph ^= 1u << ring.s;
-                issue(sKV + ring.s * L::kTileBytes, &tmK, p.k_head_y, u.k0, kvh, kv_full(ring.s));
+            };
+            auto load_q = [&](int i, const Cur &c) -> bool {
+                if ((i ? c.n1 : c.n0) == 0) return true;
+                // Q_i is free once the last score product of tile i is done; that barrier cannot
+                // turn again before this load
+                if (scores[i] > 0 && !wait_bar(s_full(i), (scores[i] - 1) & 1u, p, abort_flag)) return false;
+                if (p.inject_stall) return true;
+                mbar_arrive_expect_tx(q_full(i), L::kTileBytes);
+                issue(sQ + i * L::kTileBytes, &tmQ, p.q_head_y, i ? c.q1 : c.q0, c.head + (i & p.pair), q_full(i));
+                ++q_loads[i];
+                return true;
+            };
+            Cur cur{}, nxt{};
+            bool ok = fetch(cur);
+            if (ok && cur.valid) {
+                mbar_arrive_expect_tx(kv_full(0), L::kTileBytes);
+                armed |= 1u;
+                fph ^= 1u;
+                issue(sKV, &tmK, p.k_head_y, cur.k0, cur.head / p.group, kv_full(0));
                 ring.next();
-                // Q: its buffers are free once the S products of the unit before are done
-                if (!(ok = wait_bar(q_empty, (q_units & 1) ^ 1u, p, abort_flag))) break;
-                ++q_units;
-                if (!p.inject_stall) {
-                    if (t0.n > 0) {
-                        mbar_arrive_expect_tx(q_full(0), L::kTileBytes);
-                        issue(sQ, &tmQ, p.q_head_y, u.q0, u.head, q_full(0));
-                        ++q_loads[0];
+                ok = load_q(0, cur) && load_q(1, cur);
+            }
+            while (ok && cur.valid) {
+                const int kvh = cur.head / p.group;
+                for (int j = 0; j < cur.n && ok; ++j) {
+                    bool two = true;
+                    int krow = cur.k0 + (j + 1) * kBN, khead = kvh;
+                    if (j + 1 == cur.n) {
+                        if (!(ok = fetch(nxt))) break;
+                        two = nxt.valid != 0;
+                        krow = nxt.k0;
+                        khead = nxt.head / p.group;
                     }
-                    if (t1.n > 0) {
-                        mbar_arrive_expect_tx(q_full(1), L::kTileBytes);
-                        issue(sQ + L::kTileBytes, &tmQ, p.q_head_y, u.q0 + t1.row0, u.head + (p.pair ? 1 : 0),
-                              q_full(1));
-                        ++q_loads[1];
-                    }
-                }
-                // V_j, and K_{j+1} if any, on V_j's barrier
-                for (int j = 0; j < n && ok; ++j) {
-                    const bool two = j + 1 < n;
                     const int vs = ring.s;
                     if (!(ok = wait_bar(kv_empty(vs), ring.ph ^ 1u, p, abort_flag))) break;
                     Ring nr = ring;
@@ -434,13 +542,18 @@ __global__ void __launch_bounds__(kWsThreads, 1)
                     mbar_arrive_expect_tx(kv_full(vs), L::kTileBytes * (two ? 2u : 1u));
                     armed |= 1u << vs;
                     fph ^= 1u << vs;
-                    issue(sKV + vs * L::kTileBytes, &tmV, p.v_head_y, u.k0 + j * kBN, kvh, kv_full(vs));
+                    issue(sKV + vs * L::kTileBytes, &tmV, p.v_head_y, cur.k0 + j * kBN, kvh, kv_full(vs));
                     ring.next();
                     if (two) {
-                        issue(sKV + ring.s * L::kTileBytes, &tmK, p.k_head_y, u.k0 + (j + 1) * kBN, kvh, kv_full(vs));
+                        issue(sKV + ring.s * L::kTileBytes, &tmK, p.k_head_y, krow, khead, kv_full(vs));
                         ring.next();
                     }
                 }
+                if (!ok) break;
+                scores[0] += cur.n0;
+                scores[1] += cur.n1;
+                cur = nxt;
+                if (cur.valid) ok = load_q(0, cur) && load_q(1, cur);
             }
             // every copy has landed before the CTA exits (also after a timeout)
 #pragma unroll
@@ -450,8 +563,9 @@ __global__ void __launch_bounds__(kWsThreads, 1)
             if (q_loads[1] > 0) drain_bar(q_full(1), (q_loads[1] - 1) & 1, p);
         } else if (warp == 0 && lane == 0) {
             // ---------------------------------------------------- MMA issuer
-            constexpr uint32_t idesc_qk = idesc_f16_f32acc(kBF16, 128, kBN, false);
-            constexpr uint32_t idesc_pv = idesc_f16_f32acc(kBF16, 128, D, true);
+            struct Cur {
+                int valid, n, n0, n1, g0;  // g0: tiles from here on pass the guard before P V reads them
+            };
             Ring ring;
             uint32_t fph = 0;
             auto wait_full = [&](int st) -> bool {
@@ -459,129 +573,134 @@ __global__ void __launch_bounds__(kWsThreads, 1)
                 fph ^= 1u << st;
                 return r;
             };
-            uint32_t pcount[2] = {0, 0}, qcount[2] = {0, 0}, vcount = 0;
+            uint32_t pph = 0, qph = 0, oph = 0, vph = 0;  // phase bits of the tiles' barriers
             int slot = 0;
             uint32_t uphase = 0;
-            bool ok = true;
-            const uint64_t dq0 = sdesc_sw128(sQ, 16, 1024);
-            const uint64_t dkv0 = sdesc_sw128(sKV, 16, 1024);
-            const uint64_t dv0 = sdesc_sw128(sKV, kAtomBytes, 1024);
-            auto qk = [&](int i, int kstage) {
-                const uint64_t a = dq0 + static_cast<uint64_t>(i * (L::kTileBytes >> 4));
-                const uint64_t b = dkv0 + static_cast<uint64_t>(kstage * (L::kTileBytes >> 4));
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint64_t off = (kk >> 2) * (kAtomBytes >> 4) + (kk & 3) * 2;
-                    mma_f16_ss(tmem + 128u * i, a + off, b + off, idesc_qk, kk > 0);
+            const uint32_t dq0 = desc_lo(sQ, 16), dk0 = desc_lo(sKV, 16), dv0 = desc_lo(sKV, kAtomBytes);
+            constexpr uint32_t kTile16 = L::kTileBytes >> 4;
+            auto fetch = [&](Cur &c) -> bool {
+                for (;;) {
+                    if (!wait_bar(unit_full(slot), uphase, p, abort_flag)) return false;
+                    const VlUnit &u = units[slot];
+                    c.valid = u.valid;
+                    if (c.valid) {
+                        const VlTile t0 = vl_tile<kCausal>(p, u, 0), t1 = vl_tile<kCausal>(p, u, 1);
+                        c.n0 = t0.n;
+                        c.n1 = t1.n;
+                        c.n = t0.n > t1.n ? t0.n : t1.n;
+                        c.g0 = vl_first_masked<kCausal>(u, t0);
+                    } else {
+                        c.n0 = c.n1 = 0;
+                    }
+                    mbar_arrive(unit_empty(slot));
+                    if (++slot == kVlSlots) {
+                        slot = 0;
+                        uphase ^= 1u;
+                    }
+                    if (!c.valid || c.n > 0) return true;
                 }
             };
-            // O_i (+)= P_i V, with the P_lo pass on the lanes of the warps that split
-            auto pv = [&](int i, int vstage, bool acc) {
-                const uint64_t b0 = dv0 + static_cast<uint64_t>(vstage * (L::kTileBytes >> 4));
-                const uint32_t ta = tmem + 128u * i, td = tmem + 256u + 128u * i;
-                uint32_t lo_off[4];
-                bool split = false;
-#pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    const bool sw = split_flag(i, w) != 0;
-                    lo_off[w] = sw ? 0u : ~0u;
-                    split |= sw;
-                }
-                const int passes = split ? 2 : 1;
-#pragma unroll 1
-                for (int h = 0; h < passes; ++h) {
-                    const uint32_t off[4] = {h ? lo_off[0] : 0u, h ? lo_off[1] : 0u, h ? lo_off[2] : 0u,
-                                             h ? lo_off[3] : 0u};
-#pragma unroll
-                    for (int kk = 0; kk < kBN / 16; ++kk)
-                        mma_f16_ts_lanes(td, ta + 64u * h + 8u * kk, b0 + kk * (2048 >> 4), idesc_pv, off,
-                                         (acc || kk > 0 || h > 0) ? 1u : 0u);
-                }
-            };
-            while (ok) {
-                if (!wait_bar(unit_full(slot), uphase, p, abort_flag)) break;
-                const VlUnit &us = units[slot];
-                VlUnit u;
-                u.valid = us.valid, u.rows = us.rows, u.nk = us.nk, u.rel = us.rel;
-                mbar_arrive(unit_empty(slot));
-                if (++slot == kVlSlots) {
-                    slot = 0;
-                    uphase ^= 1u;
-                }
-                if (!u.valid) break;
-                const VlTile t0 = vl_tile<kCausal>(p, u, 0), t1 = vl_tile<kCausal>(p, u, 1);
-                const int n0 = t0.n, n1 = t1.n, n = n0 > n1 ? n0 : n1;
-                if (n == 0) continue;
-                // tiles from here on pass the guard before P V reads them
-                const int g0 = vl_first_masked<kCausal>(u, t0);
-                if (!(ok = wait_full(ring.s))) break;
-                if (n0 > 0) {
-                    if (!(ok = wait_bar(q_full(0), qcount[0]++ & 1u, p, abort_flag))) break;
-                    tc_fence_after();
-                    qk(0, ring.s);
-                    mma_commit(s_full(0));
-                }
-                if (n1 > 0) {
-                    if (!(ok = wait_bar(q_full(1), qcount[1]++ & 1u, p, abort_flag))) break;
-                    tc_fence_after();
-                    qk(1, ring.s);
-                    mma_commit(s_full(1));
-                }
-                mma_commit(kv_empty(ring.s));
-                if (n == 1) mma_commit(q_empty);
-                ring.next();
-                for (int j = 0; j < n; ++j) {
-                    const int vs = ring.s;
-                    if (!(ok = wait_full(vs))) break;  // V_j, and K_{j+1} if any
-                    if (j >= g0) {
-                        // V_j lies in its stage: the guard looks at it while P is computed
-                        *ask = vs;
-                        mbar_arrive(v_ask);
-                        if (!(ok = wait_bar(v_ok, vcount++ & 1u, p, abort_flag))) break;
-                    }
-                    tc_fence_after();
-                    ring.next();
-                    const bool more = j + 1 < n;
-                    const int ks = ring.s;
-                    if (j < n0) {
-                        if (!(ok = wait_bar(p_full(0), pcount[0]++ & 1u, p, abort_flag))) break;
-                        tc_fence_after();
-                        pv(0, vs, j > 0);
-                        if (j == n0 - 1) mma_commit(o_full(0));
-                    }
-                    if (j + 1 < n0) {
-                        qk(0, ks);
-                        mma_commit(s_full(0));
-                    }
-                    if (j < n1) {
-                        if (!(ok = wait_bar(p_full(1), pcount[1]++ & 1u, p, abort_flag))) break;
-                        tc_fence_after();
-                        pv(1, vs, j > 0);
-                        if (j == n1 - 1) mma_commit(o_full(1));
-                    }
-                    mma_commit(kv_empty(vs));
-                    if (more) {
-                        if (j + 1 < n1) {
-                            qk(1, ks);
+            // The products are written out twice.  The loop over whole steps in the middle of a
+            // long unit has its own, with both tiles unrolled: the issuer must not spend a cycle
+            // between the products.  Everything else (first and last steps, masked tiles, the
+            // change of unit, before the first unit a step without a V tile) shares one copy for
+            // both tiles: instructions that run once per unit have left the cache by then, which
+            // cost 3000 cycles per unit with a copy for each case.
+            Cur cur{1, 1, 0, 0, INT_MAX}, nxt{};
+            bool ok = true, start = true;
+            while (ok && cur.valid) {
+                // steps [1, inner) are whole for both tiles, with no guard and no change of unit
+                int inner = (cur.n0 < cur.n1 ? cur.n0 : cur.n1) - 1;
+                if (cur.g0 < inner) inner = cur.g0;
+                for (int j = 0; j < cur.n; ++j) {
+                    if (j == 1) {
+                        for (; j < inner; ++j) {
+                            const int vs = ring.s;
+                            if (!(ok = wait_full(vs))) break;  // V_j and K_{j+1}
+                            tc_fence_after();
+                            ring.next();
+                            const int ks = ring.s;
+                            const uint32_t dv = dv0 + vs * kTile16, dk = dk0 + ks * kTile16;
+                            if (!(ok = wait_bar(p_full(0), pph & 1u, p, abort_flag))) break;
+                            tc_fence_after();
+                            mma_pv<D, kBF16>(tmem + 256u, tmem, dv, 1u);
+                            mma_qk<D, kBF16>(tmem, dq0, dk);
+                            mma_commit(s_full(0));
+                            if (!(ok = wait_bar(p_full(1), (pph >> 1) & 1u, p, abort_flag))) break;
+                            pph ^= 3u;
+                            tc_fence_after();
+                            mma_pv<D, kBF16>(tmem + 384u, tmem + 128u, dv, 1u);
+                            mma_commit(kv_empty(vs));
+                            mma_qk<D, kBF16>(tmem + 128u, dq0 + kTile16, dk);
                             mma_commit(s_full(1));
+                            mma_commit(kv_empty(ks));
+                            ring.next();
                         }
+                        if (!ok) break;
+                    }
+                    const int vs = ring.s;
+                    if (!start) ring.next();
+                    const int ks = ring.s;
+                    const bool last = j + 1 == cur.n;
+                    if (last && !(ok = fetch(nxt))) break;
+                    if (start && !nxt.valid) break;
+                    if (!(ok = wait_full(vs))) break;  // V_j and the K tile after it
+                    if (j >= cur.g0) {
+                        const int b = vs >> 1;
+                        if (!(ok = wait_bar(v_ok(b), (vph >> b) & 1u, p, abort_flag))) break;
+                        vph ^= 1u << b;
+                    }
+#pragma unroll 1
+                    for (int i = 0; i < 2; ++i) {
+                        const int n_i = i ? cur.n1 : cur.n0;
+                        const uint32_t td = tmem + 128u * i;
+                        if (j < n_i) {
+                            // O_i (+)= P_i V_j: P_i from the first 64 columns of S_i, V MN-major; a
+                            // unit's first one waits until the O_i of the unit before has been read
+                            if (!(ok = wait_bar(p_full(i), (pph >> i) & 1u, p, abort_flag))) break;
+                            pph ^= 1u << i;
+                            if (j == 0) {
+                                if (!(ok = wait_bar(o_empty(i), ((oph >> i) & 1u) ^ 1u, p, abort_flag))) break;
+                                oph ^= 1u << i;
+                            }
+                            tc_fence_after();
+                            mma_pv<D, kBF16>(td + 256u, td, dv0 + vs * kTile16, j > 0 ? 1u : 0u);
+                            if (j == n_i - 1) mma_commit(o_full(i));
+                        }
+                        if (i == 1 && !start) mma_commit(kv_empty(vs));
+                        const bool first = last && (i ? nxt.n1 : nxt.n0) > 0;
+                        if (j + 1 < n_i || first) {
+                            if (first) {  // a unit's first scores: its Q tile must have arrived
+                                if (!(ok = wait_bar(q_full(i), (qph >> i) & 1u, p, abort_flag))) break;
+                                qph ^= 1u << i;
+                            }
+                            tc_fence_after();
+                            mma_qk<D, kBF16>(td, dq0 + i * kTile16, dk0 + ks * kTile16);
+                            mma_commit(s_full(i));
+                        }
+                    }
+                    if (!ok) break;
+                    if (!last || nxt.valid) {
                         mma_commit(kv_empty(ks));
-                        // the unit's last S product is issued: Q may be replaced
-                        if (j + 2 == n) mma_commit(q_empty);
                         ring.next();
                     }
+                    start = false;
                 }
+                cur = nxt;
             }
             // TMEM and shared memory stay alive until every issued MMA is done.
             mma_commit(mma_done);
             drain_bar(mma_done, 0, p);
         } else if (warp == 1) {
             // ---------------------------------------------------- value guard
-            // The issuer asks for each guarded tile once it has seen the tile arrive, and waits
-            // for the answer: the guard needs no count of the ring's phases of its own.
+            // The t-th V tile of this CTA lies in stage 1 (t even) or 3 (t odd).  The guard sees
+            // every one of them arrive, and a stage is loaded again only after the guard, too, has
+            // released it, so it never misses a phase of the full barriers; it is ahead of the
+            // issuer by up to two key tiles, so that its work is hidden behind theirs.
             int slot = 0;
-            uint32_t uphase = 0, asked = 0;
-            while (true) {
+            uint32_t uphase = 0, t = 0;
+            bool ok = true;
+            while (ok) {
                 if (!__all_sync(0xffffffffu, wait_bar(unit_full(slot), uphase, p, abort_flag))) break;
                 VlUnit &us = units[slot];
                 VlUnit u;
@@ -591,20 +710,23 @@ __global__ void __launch_bounds__(kWsThreads, 1)
                 const int n = t0.n > t1.n ? t0.n : t1.n, g0 = vl_first_masked<kCausal>(u, t0);
                 if (lane < kVlBadTiles * 4) us.bad_rows[lane >> 2][lane & 3] = 0;
                 __syncwarp();
-                bool ok = true;
-                for (int j = g0; j < n; ++j) {
-                    if (!(ok = __all_sync(0xffffffffu, wait_bar(v_ask, asked & 1u, p, abort_flag)))) break;
-                    ++asked;
-                    const int left = u.nk - j * kBN;
-                    const bool any = vl_guard_tile<D, kBF16>(smem + L::kKV + *ask * L::kTileBytes,
-                                                             left < kBN ? left : kBN, kCausal,
-                                                             us.bad_rows[(j - g0) & (kVlBadTiles - 1)], lane);
-                    if (any && lane == 0) us.bad = 1;
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(v_ok);
+                for (int j = 0; j < n; ++j, ++t) {
+                    const int b = t & 1u, vs = 1 + 2 * b;
+                    if (!(ok = __all_sync(0xffffffffu, wait_bar(kv_full(vs), (t >> 1) & 1u, p, abort_flag)))) break;
+                    if (j >= g0) {
+                        const int left = u.nk - j * kBN;
+                        const bool any = vl_guard_tile<D, kBF16>(smem + L::kKV + vs * L::kTileBytes,
+                                                                 left < kBN ? left : kBN, kCausal,
+                                                                 us.bad_rows[(j - g0) & (kVlBadTiles - 1)], lane);
+                        if (any && lane == 0) us.bad = 1;
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(v_ok(b));
+                    }
+                    if (lane == 0) mbar_arrive(kv_empty(vs));
                 }
                 if (!ok) break;
+                __syncwarp();
                 if (lane == 0) mbar_arrive(unit_empty(slot));
                 if (++slot == kVlSlots) {
                     slot = 0;
@@ -625,25 +747,40 @@ __global__ void __launch_bounds__(kWsThreads, 1)
         const uint32_t stage = base + L::kStage + static_cast<uint32_t>(warp - 4) * L::kStageBytes;
         const float c = p.scale_log2;
         uint32_t scount = 0, ocount = 0;
-        int slot = 0;
-        uint32_t uphase = 0;
-        bool ok = true;
-        while (ok) {
-            if (!__all_sync(0xffffffffu, wait_bar(unit_full(slot), uphase, p, abort_flag))) break;
-            const VlUnit &us = units[slot];
-            VlUnit u;
-            u.valid = us.valid, u.rows = us.rows, u.nk = us.nk, u.rel = us.rel;
-            if (!u.valid) break;
-            const VlTile t = vl_tile<kCausal>(p, u, i);
-            const int first_masked = vl_first_masked<kCausal>(u, t);
-            // m_ref: the max the probabilities are taken against (updated lazily);
-            // m_top: the true running row max; l: running sum in units of 2^(m_ref*c).
-            float m_ref = -INFINITY, m_top = -INFINITY, l = 0.f;
-            for (int j = 0; j < t.n; ++j) {
-                if (!__all_sync(0xffffffffu, wait_bar(s_full(i), scount & 1u, p, abort_flag))) {
-                    ok = false;
-                    break;
+        int slot = -1, done_slot = -1;  // the unit at work, and the one whose O is still to be stored
+        uint32_t uphase = 1;
+        float done_m = 0.f, done_l = 0.f;
+        int j = 0, n = 0, first_masked = 0, lim0 = 0;
+        // m_ref: the max the probabilities are taken against (updated lazily);
+        // m_top: the true running row max; l: running sum in units of 2^(m_ref*c).
+        float m_ref = -INFINITY, m_top = -INFINITY, l = 0.f;
+        bool more = true;
+        while (true) {
+            if (j == n) {
+                // the next unit; the one before has its last weights handed over
+                done_slot = slot;
+                done_m = m_ref;
+                done_l = l;
+                if (++slot == kVlSlots) slot = 0;
+                if (slot == 0) uphase ^= 1u;
+                if (!__all_sync(0xffffffffu, wait_bar(unit_full(slot), uphase, p, abort_flag))) break;
+                VlUnit u;
+                u.valid = units[slot].valid, u.rows = units[slot].rows, u.nk = units[slot].nk, u.rel = units[slot].rel;
+                more = u.valid != 0;
+                n = 0;
+                if (more) {
+                    const VlTile t = vl_tile<kCausal>(p, u, i);
+                    n = t.n;
+                    first_masked = vl_first_masked<kCausal>(u, t);
+                    lim0 = u.nk - 1;  // this row keeps the keys up to lim0
+                    if (kCausal && r + t.rel < lim0) lim0 = r + t.rel;
                 }
+                j = 0;
+                m_ref = m_top = -INFINITY;
+                l = 0.f;
+            }
+            if (j < n) {
+                if (!__all_sync(0xffffffffu, wait_bar(s_full(i), scount & 1u, p, abort_flag))) break;
                 ++scount;
                 tc_fence_after();
                 __syncwarp();
@@ -660,9 +797,7 @@ __global__ void __launch_bounds__(kWsThreads, 1)
                     for (int q = 0; q < 4; ++q)
                         tmem_ld32(tS + 32 * q, *reinterpret_cast<uint32_t(*)[32]>(&s[32 * q]));
                     tmem_ld_wait(s);
-                    int lim = u.nk - 1;
-                    if (kCausal && r + t.rel < lim) lim = r + t.rel;
-                    lim -= j * kBN;  // row r keeps keys c <= lim of this tile
+                    const int lim = lim0 - j * kBN;
 #pragma unroll
                     for (int cc = 0; cc < 128; ++cc)
                         if (cc > lim) s[cc] = __float_as_uint(-INFINITY);
@@ -702,10 +837,6 @@ __global__ void __launch_bounds__(kWsThreads, 1)
                 }
                 const float2 sum2 = fadd2(acc[0], acc[1]);
                 l = l * alpha + (sum2.x + sum2.y);
-                // P = P_hi + P_lo for a warp with a row whose weight lies on few keys
-                const bool need = r < t.valid && l * ex2_approx((m_ref - m_top) * c) < kSplitL;
-                const bool split = __any_sync(0xffffffffu, need);
-                if (lane == 0) split_flag(i, wq) = split ? 1u : 0u;
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     uint32_t pk[16];
@@ -713,14 +844,6 @@ __global__ void __launch_bounds__(kWsThreads, 1)
                     for (int e = 0; e < 16; ++e)
                         pk[e] = pack2<kBF16>(u2f(s[32 * q + 2 * e]), u2f(s[32 * q + 2 * e + 1]));
                     tmem_st16(tS + 16 * q, pk);
-                    if (split) {
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const float2 h = unpack2<kBF16>(pk[e]);
-                            pk[e] = pack2<kBF16>(u2f(s[32 * q + 2 * e]) - h.x, u2f(s[32 * q + 2 * e + 1]) - h.y);
-                        }
-                        tmem_st16(tS + 64 + 16 * q, pk);
-                    }
                 }
                 if (__any_sync(0xffffffffu, rescale)) {
                     // O_i holds P_i V_{j-1} already (covered by the S_i(j) commit).
@@ -739,88 +862,88 @@ __global__ void __launch_bounds__(kWsThreads, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_full(i));
+                ++j;
             }
-            if (!ok) break;
-            // ---------------------------------------------------- epilogue
-            const int head = us.head + (p.pair ? i : 0);
-            const int qrow = us.q0 + t.row0;  // packed row of the tile's first row
-            if (t.n > 0) {
-                if (!__all_sync(0xffffffffu, wait_bar(o_full(i), ocount & 1u, p, abort_flag))) break;
-                ++ocount;
-                tc_fence_after();
-                __syncwarp();
-            }
-            if (t.valid > wq * 32) {
-                const bool bad = t.n > 0 && *reinterpret_cast<const volatile int *>(&us.bad) != 0;
-                const float inv_l = l == 0.f ? 0.f : 1.f / l;  // 0: the row saw no key
-                const int rd_row = lane >> 2, rd_c = lane & 3;
-                uint8_t *otile = static_cast<uint8_t *>(p.o) + head * p.o_head + (qrow + wq * 32) * p.o_row;
+            if (done_slot >= 0) {
+                // ---------------------------------------------------- O of the unit before
+                const VlUnit &us = units[done_slot];
+                VlUnit u;
+                u.rows = us.rows, u.nk = us.nk, u.rel = us.rel;
+                const VlTile t = vl_tile<kCausal>(p, u, i);
                 const int wvalid = t.valid - wq * 32;  // rows of this warp
+                if (t.n > 0) {
+                    if (!__all_sync(0xffffffffu, wait_bar(o_full(i), ocount & 1u, p, abort_flag))) break;
+                    ++ocount;
+                    tc_fence_after();
+                    __syncwarp();
+                }
+                uint32_t o[D];
+                if (t.n > 0) {
 #pragma unroll
-                for (int q = 0; q < D / 32; ++q) {
-                    uint32_t o[32];
-                    if (t.n > 0) {
-                        tmem_ld32(tO + 32 * q, o);
-                        tmem_ld_wait(o);
-                    } else {
+                    for (int q = 0; q < D / 32; ++q)
+                        tmem_ld32(tO + 32 * q, *reinterpret_cast<uint32_t(*)[32]>(&o[32 * q]));
+                    tmem_ld_wait(o);
+                    // O_i has been read: the next unit's first P_i V may overwrite it
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(o_empty(i));
+                } else {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = 0u;
+                    for (int e = 0; e < D; ++e) o[e] = 0u;
+                    done_l = 0.f;
+                }
+                if (wvalid > 0) {
+                    const float inv_l = done_l == 0.f ? 0.f : 1.f / done_l;  // 0: the row saw no key
+                    const int head = us.head + (i & p.pair);
+                    const long long qrow = us.q0 + t.row0 + wq * 32;
+                    uint8_t *otile = static_cast<uint8_t *>(p.o) + head * p.o_head + qrow * p.o_row;
+                    uint8_t *oto = otile + (lane >> 2) * p.o_row + (lane & 3) * 16;
+#pragma unroll
+                    for (int q = 0; q < D / 32; ++q) {
+                        // 32 columns: each thread puts its row's 64 bytes into the staging rows (16-byte
+                        // chunk v of row t at v ^ ((t >> 1) & 3): no bank conflict on either side), then
+                        // lanes 4k .. 4k+3 store the 64 bytes of one row
+                        uint32_t w[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            w[e] = pack2<kBF16>(u2f(o[32 * q + 2 * e]) * inv_l, u2f(o[32 * q + 2 * e + 1]) * inv_l);
+#pragma unroll
+                        for (int v = 0; v < 4; ++v)
+                            st_shared_v4(stage + lane * 64 + ((v ^ ((lane >> 1) & 3)) << 4), w[4 * v], w[4 * v + 1],
+                                         w[4 * v + 2], w[4 * v + 3]);
+                        __syncwarp();
+#pragma unroll
+                        for (int s4 = 0; s4 < 4; ++s4) {
+                            const int tr = 8 * s4 + (lane >> 2);
+                            const uint4 x = ld_shared_v4(stage + tr * 64 + (((lane & 3) ^ ((tr >> 1) & 3)) << 4));
+                            if (tr < wvalid) st_global_v4(oto + 8 * s4 * p.o_row + q * 64, x.x, x.y, x.z, x.w);
+                        }
+                        __syncwarp();
                     }
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(u2f(o[e]) * inv_l);
-                    if (bad) {
-                        // non-finite values that the guard took out of V, for the rows that see them
-                        const int g0 = vl_first_masked<kCausal>(u, vl_tile<kCausal>(p, u, 0));
-                        const uint8_t *vh = p.v_ptr + (us.head / p.group) * p.v_head;
+                    if (p.lse != nullptr && lane < wvalid)
+                        p.lse[static_cast<size_t>(head) * p.total_q + qrow + lane] =
+                            done_l == 0.f ? -INFINITY : (done_m * c + log2f(done_l)) * 0.6931471805599453f;
+                    // non-finite values that the guard took out of V, for the rows that see them: added
+                    // to the stored row, whose other values they do not change
+                    if (t.n > 0 && *reinterpret_cast<const volatile int *>(&us.bad) != 0 && lane < wvalid) {
+                        const int g0 = vl_first_masked<kCausal>(u, vl_tile<kCausal>(p, u, 0)) * kBN;
+                        const uint8_t *vh = p.v_ptr + (us.head / p.group) * p.v_head + us.k0 * p.v_row;
                         int lim = u.nk - 1;
                         if (kCausal && r + t.rel < lim) lim = r + t.rel;
-                        if (r >= t.valid) lim = -1;
-                        for (int g = 0; g < kVlBadTiles; ++g)
-                            for (int w = 0; w < 4; ++w)
-                                for (uint32_t bits = us.bad_rows[g][w]; bits != 0; bits &= bits - 1) {
-                                    const int key = (g0 + g) * kBN + 32 * w + __ffs(bits) - 1;
-                                    if (key > lim) continue;
-                                    const uint32_t *vr = reinterpret_cast<const uint32_t *>(
-                                        vh + (us.k0 + key) * p.v_row + q * 64);
-#pragma unroll
-                                    for (int e = 0; e < 16; ++e) {
-                                        const uint32_t x = __ldg(vr + e);
-                                        const float2 f = unpack2<kBF16>(x);
-                                        if (nonfinite16<kBF16>(x & 0xFFFFu)) o[2 * e] = __float_as_uint(u2f(o[2 * e]) + f.x);
-                                        if (nonfinite16<kBF16>(x >> 16)) o[2 * e + 1] = __float_as_uint(u2f(o[2 * e + 1]) + f.y);
-                                    }
-                                }
-                    }
-                    uint32_t w[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) w[e] = pack2<kBF16>(u2f(o[2 * e]), u2f(o[2 * e + 1]));
-                    // whole 64-byte row segments through the warp's staging rows
-                    __syncwarp();
-#pragma unroll
-                    for (int v = 0; v < 4; ++v)
-                        st_shared_v4(stage + lane * 64 + ((v ^ ((lane >> 1) & 3)) << 4), w[4 * v], w[4 * v + 1],
-                                     w[4 * v + 2], w[4 * v + 3]);
-                    __syncwarp();
-#pragma unroll
-                    for (int s4 = 0; s4 < 4; ++s4) {
-                        const int tr = 8 * s4 + rd_row;
-                        const uint4 xv = ld_shared_v4(stage + tr * 64 + ((rd_c ^ ((tr >> 1) & 3)) << 4));
-                        if (tr < wvalid) st_global_v4(otile + tr * p.o_row + q * 64 + rd_c * 16, xv.x, xv.y, xv.z, xv.w);
+#pragma unroll 1
+                        for (int g = 0; g < kVlBadTiles * 4; ++g)
+#pragma unroll 1
+                            for (uint32_t bits = us.bad_rows[g >> 2][g & 3]; bits != 0; bits &= bits - 1) {
+                                const int key = g0 + 32 * g + __ffs(bits) - 1;
+                                if (key <= lim) add_nonfinite<D, kBF16>(otile + lane * p.o_row, vh + key * p.v_row);
+                            }
                     }
                 }
-                if (p.lse != nullptr && r < t.valid)
-                    p.lse[static_cast<size_t>(head) * p.total_q + qrow + r] =
-                        l == 0.f ? -INFINITY : (m_ref * c + log2f(l)) * 0.6931471805599453f;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(unit_empty(done_slot));
+                done_slot = -1;
             }
-            // O_i is read; the next unit's first P_i V waits for this warpgroup's p_full, and
-            // the descriptor may be replaced
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(unit_empty(slot));
-            if (++slot == kVlSlots) {
-                slot = 0;
-                uphase ^= 1u;
-            }
+            if (!more) break;
         }
     }
 
