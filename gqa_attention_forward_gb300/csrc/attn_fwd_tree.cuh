@@ -16,15 +16,19 @@
 //     128-row tile (row = token * G + head in the group), so each K/V tile is read once per
 //     kv head and 128 / G tokens;
 //   * the key tiles of all (sequence, kv head, row tile) units form one list, of which every
-//     CTA takes an equal contiguous share, whatever the lengths are.  A unit cut by a share's
-//     border leaves at most two pieces per CTA (fp32 O and log-sum-exp), merged by a second,
-//     dependent launch; the others write O themselves;
-//   * the load order runs on across the units of a share (the next unit's first K tile is
-//     loaded, and its scores computed, before the last P V of the unit before).
+//     CTA takes an equal contiguous share, whatever the lengths are; a unit counts for one tile
+//     more than it has, which is what its change costs.  A unit cut by a share's border leaves
+//     at most two pieces per CTA (fp32 O and log-sum-exp), merged by a second, dependent
+//     launch; the others write O themselves;
+//   * the load order runs on across the units of a share: the next unit's first K tile is
+//     loaded, and its scores computed, before the last P V of the unit before, the page
+//     indexes of the next unit and of the next 32 pages are fetched ahead, and O has two
+//     buffers, so that a unit's O is stored after the next unit's first weights.
 //
 // Roles (256 threads): warp 0 MMA issuer, warp 1 value guard (and TMEM), warp 2 TMA producer
-// (the lanes issue one page box each), warp 3 scheduler, warps 4-7 softmax (one row per
-// thread).  P stays in TMEM over its scores.  TMEM: S0 [0,128), S1 [128,256), O [256,256+D).
+// of K and V (the lanes issue one page box each), warp 3 scheduler, which also loads Q, warps
+// 4-7 softmax (one row per thread).  P stays in TMEM over its scores.  TMEM: S0 [0,128),
+// S1 [128,256), O0 [256,256+D), O1 [384,384+D).
 //
 // Pages.  A page is [Hkv, page, D]; a tile is min(page, 128)-row boxes.  A page index past
 // the end of the sequence or out of range is replaced by one past the last page, whose box
@@ -42,6 +46,7 @@ constexpr int kTreeThreads = 256;
 constexpr int kTreeSlots = 4;
 constexpr int kTreeMax = 128;      // tokens of one tree
 constexpr int kTreeSeqCache = 512; // sequences whose lengths are kept in shared memory
+constexpr int kMergeThreads = 64;
 constexpr int kTreeBadTiles = 2;   // the tree's positions lie in at most two key tiles
 
 struct TreeParams : Params {
@@ -67,9 +72,9 @@ struct TreeUnit {
     int kvh;
     int k0, k1;   // key tiles
     int piece;    // -1: the whole unit; 0, 1: piece slot of this CTA
-    int bad;
+    int first;    // packed row of the tree's first token
+    int bad;      // set by the guard: some bad_rows bit is set
     uint32_t bad_rows[kTreeBadTiles][4];
-    int par[kTreeMax];  // parents (-1: child of the last position before the tree)
 };
 
 template <int D>
@@ -79,14 +84,14 @@ struct TreeLayout {
     static constexpr int kQ = 0;
     static constexpr int kKV = kQ + kTileBytes;
     static constexpr int kBar = kKV + kStages * kTileBytes;
-    // q_full, q_empty, kv_full[S], kv_empty[S], s_full[2], p_full[2], o_done[2], mma_done, v_ask,
-    // v_ok, unit_full[slots], unit_empty[slots]
-    static constexpr int kNumBars = 2 + 2 * kStages + 2 + 2 + 2 + 3 + 2 * kTreeSlots;
+    // q_full, kv_full[S], kv_empty[S], v_ok[S], s_full[2], p_full[2], o_done[2], o_empty[2],
+    // mma_done, q_empty, unit_full[slots], unit_empty[slots]
+    static constexpr int kNumBars = 1 + 3 * kStages + 8 + 2 + 2 * kTreeSlots;
     static constexpr int kTmemSlot = kBar + kNumBars * 8;
     static constexpr int kAbort = kTmemSlot + 4;
-    static constexpr int kAsk = kAbort + 4;
-    static constexpr int kUnits = (kAsk + 4 + 15) & ~15;
-    static constexpr int kSeqs = (kUnits + kTreeSlots * static_cast<int>(sizeof(TreeUnit)) + 7) & ~7;
+    static constexpr int kUnits = (kAbort + 4 + 15) & ~15;
+    static constexpr int kPar = kUnits + kTreeSlots * static_cast<int>(sizeof(TreeUnit));
+    static constexpr int kSeqs = (kPar + 2 * kTreeMax * 4 + 7) & ~7;
     static constexpr int kUsed = kSeqs + kTreeSeqCache * 8;
     // more than half of an SM's shared memory: one CTA (all 512 TMEM columns) per SM
     static constexpr int kAlloc = (kUsed + 1024) > 118 * 1024 ? (kUsed + 1024) : 118 * 1024;
@@ -140,6 +145,23 @@ __device__ __forceinline__ Bits128 bits_shr(Bits128 b, int n) {
     return {(b.lo >> n) | (b.hi << (64 - n)), b.hi >> n};
 }
 
+// Weights of a unit in the shares: its key tiles and one for its change.
+__device__ __forceinline__ int tree_unit_weight(int key_tiles) { return key_tiles + 1; }
+
+// Ancestors of token t of a tree, itself among them; parents that are no earlier token end
+// the walk.  par(u): the parent of token u.
+template <typename F>
+__device__ __forceinline__ Bits128 tree_ancestors(int t, F par) {
+    Bits128 anc{0ull, 0ull};
+    while (t >= 0 && t < kTreeMax) {
+        if (t < 64) anc.lo |= 1ull << t; else anc.hi |= 1ull << (t - 64);
+        const int up = par(t);
+        if (up >= t) break;
+        t = up;
+    }
+    return anc;
+}
+
 // tmQ: 3-D tensor map (D, Hq, tokens), box 64 x G x (128 / G); tmK, tmV: 3-D maps
 // (D, page, n_pages * Hkv), box 64 x min(page, 128) x 1; all with the 128-byte swizzle.
 template <int D, bool kBF16>
@@ -154,24 +176,23 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     uint8_t *smem = smem_raw + (base - raw);
     const uint32_t sQ = base + L::kQ, sKV = base + L::kKV;
     const uint32_t bar0 = base + L::kBar;
-    const uint32_t q_full = bar0, q_empty = bar0 + 8u;
-    auto kv_full = [&](int s) { return bar0 + 8u * (2 + s); };
-    auto kv_empty = [&](int s) { return bar0 + 8u * (2 + S + s); };
-    auto s_full = [&](int b) { return bar0 + 8u * (2 + 2 * S + b); };
-    auto p_full = [&](int b) { return bar0 + 8u * (4 + 2 * S + b); };
-    auto o_done = [&](int b) { return bar0 + 8u * (6 + 2 * S + b); };
-    const uint32_t mma_done = bar0 + 8u * (8 + 2 * S);
-    const uint32_t v_ask = bar0 + 8u * (9 + 2 * S), v_ok = bar0 + 8u * (10 + 2 * S);
-    auto unit_full = [&](int s) { return bar0 + 8u * (11 + 2 * S + s); };
-    auto unit_empty = [&](int s) { return bar0 + 8u * (11 + 2 * S + kTreeSlots + s); };
-    volatile int *ask = reinterpret_cast<volatile int *>(smem + L::kAsk);
+    const uint32_t q_full = bar0;
+    auto kv_full = [&](int s) { return bar0 + 8u * (1 + s); };
+    auto kv_empty = [&](int s) { return bar0 + 8u * (1 + S + s); };
+    auto v_ok = [&](int s) { return bar0 + 8u * (1 + 2 * S + s); };  // the V tile in stage s has passed the guard
+    auto s_full = [&](int b) { return bar0 + 8u * (1 + 3 * S + b); };
+    auto p_full = [&](int b) { return bar0 + 8u * (3 + 3 * S + b); };
+    auto o_done = [&](int b) { return bar0 + 8u * (5 + 3 * S + b); };
+    auto o_empty = [&](int b) { return bar0 + 8u * (7 + 3 * S + b); };  // O buffer b has been read
+    const uint32_t mma_done = bar0 + 8u * (9 + 3 * S), q_empty = bar0 + 8u * (10 + 3 * S);
+    auto unit_full = [&](int s) { return bar0 + 8u * (11 + 3 * S + s); };
+    auto unit_empty = [&](int s) { return bar0 + 8u * (11 + 3 * S + kTreeSlots + s); };
     volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(smem + L::kTmemSlot);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kAbort);
     TreeUnit *units = reinterpret_cast<TreeUnit *>(smem + L::kUnits);
     int2 *seqs = reinterpret_cast<int2 *>(smem + L::kSeqs);  // (T, L)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    grid_launch_dependents();
     if (threadIdx.x == 64) {
         tma_prefetch_map(&tmQ);
         tma_prefetch_map(&tmK);
@@ -183,16 +204,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         mbar_init(q_empty, 1);
         for (int s = 0; s < S; ++s) {
             mbar_init(kv_full(s), 1);
-            mbar_init(kv_empty(s), 1);
+            mbar_init(kv_empty(s), 2);  // the issuer and the guard
+            mbar_init(v_ok(s), 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(s_full(b), 1);
-            mbar_init(p_full(b), 4);
+            mbar_init(p_full(b), 4);  // one arrival per softmax warp
             mbar_init(o_done(b), 1);
+            mbar_init(o_empty(b), 4);
         }
         mbar_init(mma_done, 1);
-        mbar_init(v_ask, 1);
-        mbar_init(v_ok, 1);
         for (int s = 0; s < kTreeSlots; ++s) {
             mbar_init(unit_full(s), 1);
             mbar_init(unit_empty(s), 7);  // producer, MMA issuer, guard, 4 softmax warps
@@ -203,8 +224,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         tmem_alloc(base + L::kTmemSlot, 512);
         tmem_relinquish();
     }
-    // the set-up above overlaps the kernel before this one; its results are read from here on
+    // The set-up above overlaps the kernel before this one; its results are read from here on.
+    // The merge is let go only now, so that what it reads before its own wait (offsets,
+    // lengths) was written before this kernel.
     grid_dependency_wait();
+    grid_launch_dependents();
     for (int s = threadIdx.x; s < p.n_seqs && s < kTreeSeqCache; s += kTreeThreads) {
         const TreeSeq q = tree_seq(p, s);
         seqs[s] = make_int2(q.T, q.L);
@@ -215,8 +239,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     const uint32_t tmem = *tmem_slot;
 
     if (warp == 3) {
-        // -------------------------------------------------------- scheduler
-        auto tiles_of = [&](int s) -> int {
+        // -------------------------------------------------------- scheduler, and Q
+        auto weight_of = [&](int s) -> int {
             if (s >= p.n_seqs) return 0;
             int T, Ls;
             if (s < kTreeSeqCache) {
@@ -227,7 +251,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 T = q.T;
                 Ls = q.L;
             }
-            return p.Hkv * tree_row_tiles(p, T) * tree_key_tiles(Ls);
+            return p.Hkv * tree_row_tiles(p, T) * tree_unit_weight(tree_key_tiles(Ls));
         };
         auto scan = [&](int x) {  // inclusive prefix sum over the lanes
 #pragma unroll
@@ -239,7 +263,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         };
         int total = 0;
         for (int s0 = 0; s0 < p.n_seqs; s0 += 32) {
-            const int w = tiles_of(s0 + lane), incl = scan(w);
+            const int w = weight_of(s0 + lane), incl = scan(w);
             if (blockIdx.x == 0 && s0 + lane < p.n_seqs) p.plan[1 + s0 + lane] = total + incl - w;
             total += __shfl_sync(0xffffffffu, incl, 31);
         }
@@ -250,16 +274,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         const long long first = static_cast<long long>(blockIdx.x) * share;
         int at = first < total ? static_cast<int>(first) : total;
         const int end = first + share < total ? static_cast<int>(first + share) : total;
-        int slot = 0;
-        uint32_t phase = 0;
-        int s0 = 0, before = 0;  // tiles of the sequences before s0
+        int slot = 0, q_loads = 0;
+        uint32_t phase = 0, n_units = 0;
+        int s0 = 0, before = 0;         // weights of the sequences before s0
         bool ok = true;
         for (;;) {
-            const bool more = at < end;
-            int seq = 0, in_seq = 0;
-            if (more) {
+            int seq = 0, nt = 0, unit = 0, k0 = 0, k1 = 0;
+            while (at < end && k0 == k1) {
+                int in_seq = 0;
                 for (;; s0 += 32) {
-                    const int w = tiles_of(s0 + lane), incl = scan(w);
+                    const int w = weight_of(s0 + lane), incl = scan(w);
                     const int all = __shfl_sync(0xffffffffu, incl, 31);
                     if (at < before + all) {
                         const int src = __ffs(__ballot_sync(0xffffffffu, before + incl > at)) - 1;
@@ -269,41 +293,46 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                     }
                     before += all;
                 }
+                const int Ls = seq < kTreeSeqCache ? seqs[seq].y : tree_seq(p, seq).L;
+                nt = tree_key_tiles(Ls);
+                const int uw = tree_unit_weight(nt);
+                unit = in_seq / uw;  // kv head * row tiles + row tile
+                // weights [0, uw - nt) of a unit are its change, then come its tiles; a share that
+                // ends within the change holds none of them
+                const int w0 = in_seq - unit * uw, w1 = w0 + (end - at) < uw ? w0 + (end - at) : uw;
+                k0 = w0 > uw - nt ? w0 - (uw - nt) : 0;
+                k1 = w1 > uw - nt ? w1 - (uw - nt) : 0;
+                at += w1 - w0;
             }
+            const bool more = k0 < k1;
             if (!__all_sync(0xffffffffu, wait_bar(unit_empty(slot), phase ^ 1u, p, abort_flag))) {
                 ok = false;
                 break;
             }
             TreeUnit &u = units[slot];
+            int q0 = 0, kvh = 0;
             if (more) {
                 const TreeSeq q = tree_seq(p, seq);
-                const int nt = tree_key_tiles(q.L), mt = tree_row_tiles(p, q.T);
-                const int unit = in_seq / nt, k0 = in_seq - unit * nt;  // unit = kv head * row tiles + row tile
-                const int k1 = k0 + (end - at) < nt ? k0 + (end - at) : nt;
-                const int m = unit % mt;
-                const int T = q.T < kTreeMax ? q.T : kTreeMax;
-                for (int t = lane; t < kTreeMax; t += 32) {
-                    int par = t - 1;  // no parents: a chain
-                    if (p.parents != nullptr && t < T) par = __ldg(p.parents + q.q0 + t);
-                    u.par[t] = par;
-                }
+                const int mt = tree_row_tiles(p, q.T), t0 = (unit % mt) * p.rt;
+                q0 = q.q0 + t0;
+                kvh = unit / mt;
                 if (lane < kTreeBadTiles * 4) u.bad_rows[lane >> 2][lane & 3] = 0;
                 if (lane == 0) {
                     u.valid = 1;
-                    u.t0 = m * p.rt;
-                    u.q0 = q.q0 + u.t0;
-                    u.ntok = q.T - u.t0 < p.rt ? q.T - u.t0 : p.rt;
+                    u.t0 = t0;
+                    u.q0 = q0;
+                    u.ntok = q.T - t0 < p.rt ? q.T - t0 : p.rt;
                     u.T = q.T;
                     u.L = q.L;
                     u.base = q.L > q.T ? q.L - q.T : 0;
                     u.row = q.row;
-                    u.kvh = unit / mt;
+                    u.kvh = kvh;
                     u.k0 = k0;
                     u.k1 = k1;
                     u.piece = (k0 == 0 && k1 == nt) ? -1 : (k0 > 0 ? 0 : 1);
+                    u.first = q.q0;
                     u.bad = 0;
                 }
-                at += k1 - k0;
             } else if (lane == 0) {
                 u.valid = 0;
             }
@@ -314,7 +343,24 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 slot = 0;
                 phase ^= 1u;
             }
+            // Q's buffer is free once the last scores of the unit before are computed
+            if (!__all_sync(0xffffffffu, wait_bar(q_empty, (n_units & 1u) ^ 1u, p, abort_flag))) {
+                ok = false;
+                break;
+            }
+            ++n_units;
+            if (!p.inject_stall) {
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(q_full, static_cast<uint32_t>(p.group * p.rt) * D * 2);
+#pragma unroll
+                    for (int a = 0; a < D / 64; ++a)
+                        tma_load_3d(sQ + a * kAtomBytes, &tmQ, 64 * a, kvh * p.group, q0, q_full);
+                }
+                ++q_loads;
+            }
         }
+        if (lane == 0 && q_loads > 0) drain_bar(q_full, (q_loads - 1) & 1, p);  // landed before the CTA exits
+        __syncwarp();
         if (ok && blockIdx.x == 0) {
             bool bad = false;
             for (int s = lane; s < p.n_seqs; s += 32) bad |= tree_seq(p, s).bad;
@@ -330,7 +376,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         // window is on its way while this one is used.  A tile's pages (128 / page of them,
         // from a multiple of that) never cross a window.
         struct Cur {
-            int valid, q0, row, kvh, k0, k1, pages;
+            int valid, row, kvh, k0, k1, pages;
             int win;           // first entry of window a; b holds the 32 after it
             int ent_a, ent_b;
         };
@@ -339,17 +385,18 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         auto entry = [&](const Cur &c, int i) -> int {
             return c.row >= 0 && i < c.pages ? __ldg(p.table + static_cast<long long>(c.row) * p.table_w + i) : -1;
         };
-        auto fetch = [&](Cur &c) -> bool {
-            if (!__all_sync(0xffffffffu, wait_bar(unit_full(slot), uphase, p, abort_flag))) return false;
+        auto take = [&](Cur &c) {  // the descriptor in the slot has arrived
             const TreeUnit &u = units[slot];
             c.valid = u.valid;
             if (c.valid) {
-                c.q0 = u.q0;
                 c.row = u.row;
                 c.kvh = u.kvh;
                 c.k0 = u.k0;
                 c.k1 = u.k1;
                 c.pages = (u.L + p.page - 1) >> p.page_shift;
+                c.win = ((c.k0 << 7) >> p.page_shift) & ~31;
+                c.ent_a = entry(c, c.win + lane);
+                c.ent_b = entry(c, c.win + 32 + lane);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(unit_empty(slot));
@@ -357,92 +404,89 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 slot = 0;
                 uphase ^= 1u;
             }
-            if (c.valid) {
-                c.win = ((c.k0 << 7) >> p.page_shift) & ~31;
-                c.ent_a = entry(c, c.win + lane);
-                c.ent_b = entry(c, c.win + 32 + lane);
-            }
-            return true;
         };
-        int stage = 0, loads = 0, q_units = 0, q_loads = 0;
+        int stage = 0, loads = 0;
         uint32_t phase = 0;
-        auto load_tile_boxes = [&](Cur &c, const CUtensorMap *tm, int kt) -> bool {
-            const int first = (kt << 7) >> p.page_shift;
-            // V is the last to use a window: the one after the next is fetched when V leaves it
-            if (tm == &tmV && first >= c.win + 32) {
-                c.win += 32;
-                c.ent_a = c.ent_b;
-                c.ent_b = entry(c, c.win + 32 + lane);
-            }
-            if (!__all_sync(0xffffffffu, wait_bar(kv_empty(stage), phase ^ 1u, p, abort_flag))) return false;
-            const uint32_t dst = sKV + stage * L::kTileBytes;
-            if (lane == 0) mbar_arrive_expect_tx(kv_full(stage), L::kTileBytes);
-            __syncwarp();
-            // lane b issues box b: atom b % kAtoms of page piece b / kAtoms
-            const int piece = lane / kAtoms, a = lane % kAtoms;
-            const int at = first - c.win + piece;  // in [0, 64)
-            const int ea = __shfl_sync(0xffffffffu, c.ent_a, at & 31);
-            const int eb = __shfl_sync(0xffffffffu, c.ent_b, at & 31);
-            int e = at < 32 ? ea : eb;
-            if (lane < boxes) {
-                if (e < 0 || e >= p.n_pages) {
-                    if (first + piece < c.pages) atomicCAS(&g_error_code, 0, static_cast<int>(ATTN_ERR_PAGE));
-                    e = -1;
-                }
-                tma_load_3d(dst + a * kAtomBytes + piece * box_rows * 128, tm, 64 * a, (kt << 7) & (p.page - 1),
-                            e < 0 ? oob : e * p.Hkv + c.kvh, kv_full(stage));
-            }
-            ++loads;
-            if (++stage == S) {
-                stage = 0;
-                phase ^= 1u;
-            }
-            return true;
-        };
-        // the first K tile of a unit, then its Q
-        auto start = [&](Cur &c) -> bool {
-            if (!load_tile_boxes(c, &tmK, c.k0)) return false;
-            if (!__all_sync(0xffffffffu, wait_bar(q_empty, (q_units & 1) ^ 1u, p, abort_flag))) return false;
-            ++q_units;
-            if (!p.inject_stall) {
-                if (lane == 0) {
-                    const uint32_t bytes = static_cast<uint32_t>(p.group * p.rt) * D * 2;
-                    mbar_arrive_expect_tx(q_full, bytes);
-                    for (int a = 0; a < kAtoms; ++a)
-                        tma_load_3d(sQ + a * kAtomBytes, &tmQ, 64 * a, c.kvh * p.group, c.q0, q_full);
-                }
-                ++q_loads;
-            }
-            return true;
-        };
         Cur cur{}, nxt{};
-        bool ok = fetch(cur) && (!cur.valid || start(cur));
+        bool have = false;  // nxt holds the unit after cur
+        bool ok = __all_sync(0xffffffffu, wait_bar(unit_full(slot), uphase, p, abort_flag));
+        if (ok) take(cur);
+        // The order of the issuer: the first K tile, then for each key tile the K tile after it
+        // (the next unit's first one, behind the last) and its V tile.
+        bool lead = true;
         while (ok && cur.valid) {
             for (int kt = cur.k0; ok && kt < cur.k1; ++kt) {
-                if (kt + 1 < cur.k1)
-                    ok = load_tile_boxes(cur, &tmK, kt + 1);
-                else
-                    ok = fetch(nxt) && (!nxt.valid || start(nxt));
-                ok = ok && load_tile_boxes(cur, &tmV, kt);
+#pragma unroll 1
+                for (int h = lead ? -1 : 0; h < 2 && ok; ++h) {
+                    // h = -1: the very first K tile, 0: the next K tile, 1: V
+                    lead = false;
+                    bool of_next = false;
+                    int t = h == 0 ? kt + 1 : kt;
+                    if (h == 0 && t == cur.k1) {
+                        if (!have) {
+                            if (!(ok = __all_sync(0xffffffffu, wait_bar(unit_full(slot), uphase, p, abort_flag)))) break;
+                            take(nxt);
+                            have = true;
+                        }
+                        if (!nxt.valid) continue;
+                        of_next = true;
+                        t = nxt.k0;
+                    } else if (!have && __all_sync(0xffffffffu, mbar_try_wait(unit_full(slot), uphase))) {
+                        take(nxt);  // its page indexes are on their way by the time they are needed
+                        have = true;
+                    }
+                    const int first = (t << 7) >> p.page_shift;
+                    // V is the last to use a window: the one after the next is fetched when V leaves it
+                    if (h == 1 && first >= cur.win + 32) {
+                        cur.win += 32;
+                        cur.ent_a = cur.ent_b;
+                        cur.ent_b = entry(cur, cur.win + 32 + lane);
+                    }
+                    if (!(ok = __all_sync(0xffffffffu, wait_bar(kv_empty(stage), phase ^ 1u, p, abort_flag)))) break;
+                    const uint32_t dst = sKV + stage * L::kTileBytes;
+                    if (lane == 0) mbar_arrive_expect_tx(kv_full(stage), L::kTileBytes);
+                    __syncwarp();
+                    // lane b issues box b: atom b % kAtoms of page piece b / kAtoms
+                    const int piece = lane / kAtoms, a = lane % kAtoms;
+                    const int at = first - (of_next ? nxt.win : cur.win) + piece;  // in [0, 64)
+                    const int ea = __shfl_sync(0xffffffffu, of_next ? nxt.ent_a : cur.ent_a, at & 31);
+                    const int eb = __shfl_sync(0xffffffffu, of_next ? nxt.ent_b : cur.ent_b, at & 31);
+                    int e = at < 32 ? ea : eb;
+                    if (lane < boxes) {
+                        if (e < 0 || e >= p.n_pages) {
+                            if (first + piece < (of_next ? nxt.pages : cur.pages))
+                                atomicCAS(&g_error_code, 0, static_cast<int>(ATTN_ERR_PAGE));
+                            e = -1;
+                        }
+                        tma_load_3d(dst + a * kAtomBytes + piece * box_rows * 128, h == 1 ? &tmV : &tmK, 64 * a,
+                                    (t << 7) & (p.page - 1), e < 0 ? oob : e * p.Hkv + (of_next ? nxt.kvh : cur.kvh),
+                                    kv_full(stage));
+                    }
+                    ++loads;
+                    if (++stage == S) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
             }
             cur = nxt;
+            have = false;
         }
         if (lane == 0) {
             // every copy has landed before the CTA exits (also after a timeout)
 #pragma unroll
             for (int st = 0; st < S; ++st)
                 if (loads > st) drain_bar(kv_full(st), st < stage ? phase : phase ^ 1u, p);
-            if (q_loads > 0) drain_bar(q_full, (q_loads - 1) & 1, p);
         }
         __syncwarp();
     } else if (warp == 0) {
         if (lane == 0) {
             // ---------------------------------------------------- MMA issuer
-            constexpr uint32_t idesc_qk = idesc_f16_f32acc(kBF16, kBM, kBN, false);
-            constexpr uint32_t idesc_pv = idesc_f16_f32acc(kBF16, kBM, D, true);
-            const uint32_t tO = tmem + 256u;
+            const uint32_t dq = desc_lo(sQ, 16), dk0 = desc_lo(sKV, 16), dv0 = desc_lo(sKV, kAtomBytes);
+            constexpr uint32_t kTile16 = L::kTileBytes >> 4;
             int stage = 0, slot = 0;
-            uint32_t phase = 0, uphase = 0, qn = 0, vn = 0, jj = 0, pj = 0;  // scores issued, P V issued
+            uint32_t phase = 0, uphase = 0, jj = 0, pj = 0;  // scores issued, P V issued
+            uint32_t qn = 0, un = 0, vph = 0;                // Q tiles, units, phases of v_ok
             struct Cur {
                 int valid, k0, k1, guard;
             };
@@ -462,65 +506,52 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 }
                 return true;
             };
-            auto take = [&]() -> int {  // next ring stage
-                const int st = stage;
-                if (++stage == S) {
-                    stage = 0;
-                    phase ^= 1u;
-                }
-                return st;
-            };
-            auto qk = [&](bool last) -> bool {
-                if (!wait_bar(kv_full(stage), phase, p, abort_flag)) return false;
-                tc_fence_after();
-                const int ks = take();
-                const uint32_t sK = sKV + ks * L::kTileBytes, b = jj++ & 1u;
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t koff = (kk >> 2) * kAtomBytes + (kk & 3) * 32;
-                    mma_f16_ss(tmem + 128u * b, sdesc_sw128(sQ + koff, 16, 1024),
-                               sdesc_sw128(sK + koff, 16, 1024), idesc_qk, kk > 0);
-                }
-                mma_commit(s_full(b));
-                mma_commit(kv_empty(ks));
-                if (last) mma_commit(q_empty);  // the unit's last score product: Q may be replaced
-                return true;
-            };
-            auto start = [&](const Cur &c) -> bool {
-                if (!wait_bar(q_full, qn++ & 1u, p, abort_flag)) return false;
-                tc_fence_after();
-                return qk(c.k0 + 1 == c.k1);
-            };
-            Cur cur{}, nxt{};
-            bool ok = fetch(cur) && (!cur.valid || start(cur));
+            // Per key tile: the scores of the tile after it (the next unit's first one, behind the
+            // last), then its P V; before the first unit a step without P V.
+            Cur cur{1, 0, 1, 0}, nxt{};
+            bool ok = true, start = true;
             while (ok && cur.valid) {
-                for (int kt = cur.k0; ok && kt < cur.k1; ++kt) {
-                    if (kt + 1 < cur.k1)
-                        ok = qk(kt + 2 == cur.k1);
-                    else
-                        ok = fetch(nxt) && (!nxt.valid || start(nxt));
-                    if (!ok) break;
-                    // O (+)= P_b V: P from TMEM (first 64 columns of S_b), V MN-major
-                    const uint32_t b = pj & 1u;
+                for (int kt = cur.k0; kt < cur.k1; ++kt) {
+                    const bool last = kt + 1 == cur.k1;
+                    if (last && !(ok = fetch(nxt))) break;
+                    if (!last || nxt.valid) {
+                        if (last && !(ok = wait_bar(q_full, qn++ & 1u, p, abort_flag))) break;
+                        if (!(ok = wait_bar(kv_full(stage), phase, p, abort_flag))) break;
+                        tc_fence_after();
+                        const uint32_t b = jj++ & 1u;
+                        mma_qk<D, kBF16>(tmem + 128u * b, dq, dk0 + stage * kTile16);
+                        mma_commit(s_full(b));
+                        mma_commit(kv_empty(stage));
+                        // the unit's last scores: Q may be replaced
+                        if (last ? nxt.k0 + 1 == nxt.k1 : kt + 2 == cur.k1) mma_commit(q_empty);
+                        if (++stage == S) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
+                    }
+                    if (start) break;
+                    // O (+)= P_b V: P from TMEM (first 64 columns of S_b), V MN-major; a unit's first
+                    // one waits until the O of the unit before the last has been read
+                    const uint32_t b = pj & 1u, ob = un & 1u;
                     if (!(ok = wait_bar(kv_full(stage), phase, p, abort_flag))) break;
                     if (kt >= cur.guard) {
-                        // V lies in its stage: the guard looks at it while P is computed
-                        *ask = stage;
-                        mbar_arrive(v_ask);
-                        if (!(ok = wait_bar(v_ok, vn++ & 1u, p, abort_flag))) break;
+                        if (!(ok = wait_bar(v_ok(stage), (vph >> stage) & 1u, p, abort_flag))) break;
+                        vph ^= 1u << stage;
                     }
+                    if (kt == cur.k0 && !(ok = wait_bar(o_empty(ob), ((un >> 1) & 1u) ^ 1u, p, abort_flag))) break;
                     if (!(ok = wait_bar(p_full(b), (pj >> 1) & 1u, p, abort_flag))) break;
                     tc_fence_after();
-                    const int vs = take();
-                    const uint32_t sV = sKV + vs * L::kTileBytes;
-#pragma unroll
-                    for (int kk = 0; kk < kBN / 16; ++kk)
-                        mma_f16_ts(tO, tmem + 128u * b + 8u * kk, sdesc_sw128(sV + kk * 2048, kAtomBytes, 1024),
-                                   idesc_pv, (kt > cur.k0 || kk > 0) ? 1u : 0u);
+                    mma_pv<D, kBF16>(tmem + 256u + 128u * ob, tmem + 128u * b, dv0 + stage * kTile16, kt > cur.k0 ? 1u : 0u);
                     mma_commit(o_done(b));
-                    mma_commit(kv_empty(vs));
+                    mma_commit(kv_empty(stage));
                     ++pj;
+                    if (++stage == S) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
                 }
+                if (!start) ++un;
+                start = false;
                 cur = nxt;
             }
             mma_commit(mma_done);
@@ -529,76 +560,110 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         __syncwarp();
     } else if (warp == 1) {
         // -------------------------------------------------------- value guard
-        // The issuer asks for each guarded tile once it has seen the tile arrive, and waits for
-        // the answer.
-        int slot = 0;
-        uint32_t uphase = 0, asked = 0;
+        // The guard sees every tile arrive, in the producer's order, and a stage is loaded again
+        // only after the guard, too, has released it: it never misses a phase, and it looks at
+        // V tiles several tiles before their product.
+        int slot = 0, stage = 0;
+        uint32_t uphase = 0, phase = 0;
         bool ok = true;
-        while (ok) {
-            if (!__all_sync(0xffffffffu, wait_bar(unit_full(slot), uphase, p, abort_flag))) break;
-            TreeUnit &u = units[slot];
-            if (!u.valid) break;
-            const int guard = u.base / kBN;
-            for (int kt = u.k0 > guard ? u.k0 : guard; kt < u.k1; ++kt) {
-                if (!(ok = __all_sync(0xffffffffu, wait_bar(v_ask, asked & 1u, p, abort_flag)))) break;
-                ++asked;
-                int left = u.L - kt * kBN;
-                left = left < 0 ? 0 : (left < kBN ? left : kBN);
-                const bool any = vl_guard_tile<D, kBF16>(smem + L::kKV + *ask * L::kTileBytes, left, u.T > 1,
-                                                         u.bad_rows[(kt - guard) & (kTreeBadTiles - 1)], lane);
-                if (any && lane == 0) u.bad = 1;
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(v_ok);
-            }
-            if (!ok) break;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(unit_empty(slot));
+        auto fetch = [&](int &held) -> bool {
+            if (!__all_sync(0xffffffffu, wait_bar(unit_full(slot), uphase, p, abort_flag))) return false;
+            held = slot;
             if (++slot == kTreeSlots) {
                 slot = 0;
                 uphase ^= 1u;
             }
+            return true;
+        };
+        // the next tile: waits for it, lets the guard work on a V tile, releases the stage
+        auto pass = [&](TreeUnit *u, int kt, int guard) -> bool {
+            if (!__all_sync(0xffffffffu, wait_bar(kv_full(stage), phase, p, abort_flag))) return false;
+            if (u != nullptr) {
+                int left = u->L - kt * kBN;
+                left = left < 0 ? 0 : (left < kBN ? left : kBN);
+                const bool any = vl_guard_tile<D, kBF16>(smem + L::kKV + stage * L::kTileBytes, left, u->T > 1,
+                                                         u->bad_rows[(kt - guard) & (kTreeBadTiles - 1)], lane);
+                if (any && lane == 0) u->bad = 1;
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(v_ok(stage));
+            }
+            if (lane == 0) mbar_arrive(kv_empty(stage));
+            if (++stage == S) {
+                stage = 0;
+                phase ^= 1u;
+            }
+            return true;
+        };
+        int cur = 0, nxt = 0;
+        ok = fetch(cur) && (!units[cur].valid || pass(nullptr, 0, 0));
+        while (ok && units[cur].valid) {
+            TreeUnit &u = units[cur];
+            const int k1 = u.k1, guard = u.base / kBN;
+#pragma unroll 1
+            for (int kt = u.k0; ok && kt < k1; ++kt) {
+                if (kt + 1 == k1) ok = fetch(nxt);
+                if (ok && (kt + 1 < k1 || units[nxt].valid)) ok = pass(nullptr, 0, 0);
+                ok = ok && pass(kt >= guard ? &u : nullptr, kt, guard);
+            }
+            __syncwarp();
+            if (ok && lane == 0) mbar_arrive(unit_empty(cur));
+            cur = nxt;
         }
     } else {
         // -------------------------------------------------------- softmax rows
         const int wq = warp & 3;
         const int r = wq * 32 + lane;  // row within the tile == TMEM lane
         const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
-        const uint32_t tO = tmem + 256u + lane_off;
         const float c = p.scale_log2;
-        int slot = 0;
-        uint32_t uphase = 0, jj = 0;  // tiles so far
-        bool ok = true;
-        while (ok) {
-            if (!__all_sync(0xffffffffu, wait_bar(unit_full(slot), uphase, p, abort_flag))) break;
-            const TreeUnit &u = units[slot];
-            if (!u.valid) break;
-            const int k0 = u.k0, k1 = u.k1, tree0 = u.base;
-            const int tok = r / p.group;  // token within the row tile
-            const bool valid = tok < u.ntok && tok < p.rt;
-            const bool active = wq * 32 < u.ntok * p.group;  // some row of this warp is real
-            // ancestors of this row's token, itself among them
-            Bits128 anc{0ull, 0ull};
-            if (valid) {
-                int t = u.t0 + tok;
-                while (t >= 0 && t < kTreeMax) {
-                    if (t < 64) anc.lo |= 1ull << t; else anc.hi |= 1ull << (t - 64);
-                    const int par = u.par[t];
-                    if (par >= t) break;  // not a tree: the walk ends here
-                    t = par;
+        const int tok = r / p.group;  // token within the row tile
+        int *par0 = reinterpret_cast<int *>(smem + L::kPar);
+        int slot = -1, done_slot = -1;  // the unit at work, and the one whose O is still to be stored
+        uint32_t uphase = 1, jj = 0, un = 0;  // tiles and units so far
+        int kt = 0, k0 = 0, k1 = 0, tree0 = 0;
+        bool valid = false, active = false, more = true;  // this row is real; some row of this warp is
+        Bits128 anc{0ull, 0ull};
+        float mrow = -INFINITY, l = 0.f, done_m = 0.f, done_l = 0.f;
+        while (true) {
+            if (kt == k1) {
+                // the next unit; the one before has its last weights handed over
+                done_slot = slot;
+                done_m = mrow;
+                done_l = l;
+                if (++slot == kTreeSlots) slot = 0;
+                if (slot == 0) uphase ^= 1u;
+                if (!__all_sync(0xffffffffu, wait_bar(unit_full(slot), uphase, p, abort_flag))) break;
+                const TreeUnit &u = units[slot];
+                more = u.valid != 0;
+                k0 = k1 = kt = 0;
+                if (more) {
+                    k0 = kt = u.k0;
+                    k1 = u.k1;
+                    tree0 = u.base;
+                    valid = tok < u.ntok && tok < p.rt;
+                    active = wq * 32 < u.ntok * p.group;
+                    anc.lo = 1ull;
+                    anc.hi = 0ull;
+                    if (u.T > 1) {
+                        // the tree's parents (without: a chain), one per thread
+                        int *par = par0 + (un & 1u) * kTreeMax;
+                        par[r] = p.parents != nullptr && r < u.T ? __ldg(p.parents + u.first + r) : r - 1;
+                        asm volatile("bar.sync 1, 128;" ::: "memory");
+                        if (valid) anc = tree_ancestors(u.t0 + tok, [&](int t) { return par[t]; });
+                    }
+                    ++un;
                 }
+                mrow = -INFINITY;
+                l = 0.f;
             }
-            float mrow = -INFINITY, l = 0.f;
-            for (int kt = k0; kt < k1; ++kt, ++jj) {
+            const uint32_t ob = (un - 1) & 1u;  // O buffer of the unit at work
+            if (kt < k1) {
                 const uint32_t b = jj & 1u;
-                if (!__all_sync(0xffffffffu, wait_bar(s_full(b), (jj >> 1) & 1u, p, abort_flag))) {
-                    ok = false;
-                    break;
-                }
+                if (!__all_sync(0xffffffffu, wait_bar(s_full(b), (jj >> 1) & 1u, p, abort_flag))) break;
                 if (active) {
                     tc_fence_after();
                     __syncwarp();
-                    const uint32_t tS = tmem + 128u * b + lane_off;
+                    const uint32_t tS = tmem + 128u * b + lane_off, tO = tmem + 256u + 128u * ob + lane_off;
                     uint32_t s[128];
                     float mt;
                     if ((kt + 1) * kBN <= tree0) {
@@ -641,10 +706,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                     if (kt > k0 && __any_sync(0xffffffffu, m_new > mrow)) {
                         // rescale O: the P V before must have finished writing it
                         if (!__all_sync(0xffffffffu,
-                                        wait_bar(o_done((jj - 1) & 1u), ((jj - 1) >> 1) & 1u, p, abort_flag))) {
-                            ok = false;
+                                        wait_bar(o_done((jj - 1) & 1u), ((jj - 1) >> 1) & 1u, p, abort_flag)))
                             break;
-                        }
                         tc_fence_after();
                         __syncwarp();
 #pragma unroll
@@ -682,80 +745,91 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_full(b));
+                ++jj;
+                ++kt;
             }
-            if (!ok) break;
-            // ---------------------------------------------------- epilogue
-            const uint32_t last = jj - 1;
-            if (!__all_sync(0xffffffffu, wait_bar(o_done(last & 1u), (last >> 1) & 1u, p, abort_flag))) break;
-            if (active) {
-                tc_fence_after();
-                __syncwarp();
-                const bool bad = *reinterpret_cast<const volatile int *>(&u.bad) != 0;
-                const float inv_l = l == 0.f ? 0.f : 1.f / l;  // 0: the row saw no key
-                const float lse = l == 0.f ? -INFINITY : (mrow * c + log2f(l)) * 0.6931471805599453f;
-                const int head = u.kvh * p.group + r % p.group;
-                const long long tok_row = u.q0 + tok;
-                uint8_t *orow = static_cast<uint8_t *>(p.o) + tok_row * p.o_row + head * p.o_head;
-                const size_t prow = (static_cast<size_t>(blockIdx.x) * 2 + (u.piece > 0 ? 1 : 0)) * kBM + r;
+            if (done_slot >= 0) {
+                // ------------------------------------------------ O of the unit before
+                // Its last tile is the one before the unit at work has begun: one tile back, or
+                // none where no unit is left.
+                const uint32_t last = jj - 1 - (more ? 1u : 0u), db = more ? ob ^ 1u : ob;
+                if (!__all_sync(0xffffffffu, wait_bar(o_done(last & 1u), (last >> 1) & 1u, p, abort_flag))) break;
+                const TreeUnit &u = units[done_slot];
+                if (wq * 32 < u.ntok * p.group) {
+                    tc_fence_after();
+                    __syncwarp();
+                    const uint32_t tO = tmem + 256u + 128u * db + lane_off;
+                    const bool real = tok < u.ntok && tok < p.rt;
+                    const float inv_l = done_l == 0.f ? 0.f : 1.f / done_l;  // 0: the row saw no key
+                    const float lse = done_l == 0.f ? -INFINITY : (done_m * c + log2f(done_l)) * 0.6931471805599453f;
+                    const int head = u.kvh * p.group + (r - tok * p.group);
+                    const long long tok_row = u.q0 + tok;
+                    uint8_t *orow = static_cast<uint8_t *>(p.o) + tok_row * p.o_row + head * p.o_head;
+                    const size_t prow = (static_cast<size_t>(blockIdx.x) * 2 + (u.piece > 0 ? 1 : 0)) * kBM + r;
+                    float *part = p.part_o + prow * D;
+                    const bool whole = u.piece < 0;
 #pragma unroll
-                for (int q = 0; q < D / 32; ++q) {
-                    uint32_t o[32];
-                    tmem_ld32(tO + 32 * q, o);
-                    tmem_ld_wait(o);
-                    if (!valid) continue;
+                    for (int q = 0; q < D / 32; ++q) {
+                        uint32_t o[32];
+                        tmem_ld32(tO + 32 * q, o);
+                        tmem_ld_wait(o);
+                        if (!real) continue;
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(u2f(o[e]) * inv_l);
-                    if (bad) {
-                        // non-finite values that the guard took out of V, for the rows that see them
-                        for (int g = 0; g < kTreeBadTiles; ++g)
-                            for (int w = 0; w < 4; ++w)
-                                for (uint32_t bits = u.bad_rows[g][w]; bits != 0; bits &= bits - 1) {
-                                    const int key = (tree0 / kBN + g) * kBN + 32 * w + __ffs(bits) - 1;
-                                    const int node = key - tree0;
-                                    if (node >= 0 && !((node < 64 ? anc.lo >> node : anc.hi >> (node - 64)) & 1ull))
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(u2f(o[e]) * inv_l);
+                        if (!whole) {
+#pragma unroll
+                            for (int v = 0; v < 8; ++v)
+                                st_global_v4(part + q * 32 + v * 4, o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
+                        } else {
+                            uint32_t w[16];
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) w[e] = pack2<kBF16>(u2f(o[2 * e]), u2f(o[2 * e + 1]));
+#pragma unroll
+                            for (int v = 0; v < 4; ++v)
+                                st_global_v4(orow + q * 64 + v * 16, w[4 * v], w[4 * v + 1], w[4 * v + 2], w[4 * v + 3]);
+                        }
+                    }
+                    if (real) {
+                        if (!whole)
+                            p.part_lse[prow] = lse;
+                        else if (p.lse != nullptr)
+                            p.lse[static_cast<size_t>(head) * p.total_q + tok_row] = lse;
+                        if (*reinterpret_cast<const volatile int *>(&u.bad) != 0) {
+                            // non-finite values that the guard took out of V, for the rows that see them:
+                            // added to the stored row, whose other values they do not change
+                            const Bits128 seen = u.T > 1
+                                ? tree_ancestors(u.t0 + tok, [&](int t) {
+                                      return p.parents != nullptr && t < u.T ? __ldg(p.parents + u.first + t) : t - 1;
+                                  })
+                                : Bits128{1ull, 0ull};
+#pragma unroll 1
+                            for (int g = 0; g < kTreeBadTiles * 4; ++g)
+#pragma unroll 1
+                                for (uint32_t bits = u.bad_rows[g >> 2][g & 3]; bits != 0; bits &= bits - 1) {
+                                    const int key = u.base / kBN * kBN + 32 * g + __ffs(bits) - 1, node = key - u.base;
+                                    if (node >= 0 && !((node < 64 ? seen.lo >> node : seen.hi >> (node - 64)) & 1ull))
                                         continue;
                                     const int pg = __ldg(p.table + static_cast<long long>(u.row) * p.table_w +
                                                          (key >> p.page_shift));
-                                    const uint32_t *vr = reinterpret_cast<const uint32_t *>(
-                                        p.v_ptr + ((static_cast<size_t>(pg) * p.Hkv + u.kvh) * p.page +
-                                                   (key & (p.page - 1))) * (D * 2) + q * 64);
-#pragma unroll
-                                    for (int e = 0; e < 16; ++e) {
-                                        const uint32_t x = __ldg(vr + e);
-                                        const float2 f = unpack2<kBF16>(x);
-                                        if (nonfinite16<kBF16>(x & 0xFFFFu)) o[2 * e] = __float_as_uint(u2f(o[2 * e]) + f.x);
-                                        if (nonfinite16<kBF16>(x >> 16)) o[2 * e + 1] = __float_as_uint(u2f(o[2 * e + 1]) + f.y);
-                                    }
+                                    const uint8_t *vr = p.v_ptr + ((static_cast<size_t>(pg) * p.Hkv + u.kvh) * p.page +
+                                                                   (key & (p.page - 1))) * (D * 2);
+                                    if (whole)
+                                        add_nonfinite<D, kBF16>(orow, vr);
+                                    else
+                                        add_nonfinite_f32<D, kBF16>(part, vr);
                                 }
+                        }
                     }
-                    if (u.piece >= 0) {
-                        float *dst = p.part_o + prow * D + q * 32;
-#pragma unroll
-                        for (int v = 0; v < 8; ++v)
-                            st_global_v4(dst + v * 4, o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
-                    } else {
-                        uint32_t w[16];
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) w[e] = pack2<kBF16>(u2f(o[2 * e]), u2f(o[2 * e + 1]));
-#pragma unroll
-                        for (int v = 0; v < 4; ++v)
-                            st_global_v4(orow + q * 64 + v * 16, w[4 * v], w[4 * v + 1], w[4 * v + 2], w[4 * v + 3]);
-                    }
+                    tc_fence_before();
                 }
-                if (valid) {
-                    if (u.piece >= 0)
-                        p.part_lse[prow] = lse;
-                    else if (p.lse != nullptr)
-                        p.lse[static_cast<size_t>(head) * p.total_q + tok_row] = lse;
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(o_empty(db));
+                    mbar_arrive(unit_empty(done_slot));
                 }
-                tc_fence_before();
+                done_slot = -1;
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(unit_empty(slot));
-            if (++slot == kTreeSlots) {
-                slot = 0;
-                uphase ^= 1u;
-            }
+            if (!more) break;
         }
     }
 
@@ -770,16 +844,17 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 // Merges the pieces of the units that were cut: lse = log sum_s exp(lse_s) and
 // O = sum_s exp(lse_s - lse) O_s (the online-softmax update of page "从零开始写Qwen3",
 // deepseek.csdn.net/6a3201f8..., section "在线softmax", across CTAs).  One warp per output
-// row; a row whose unit lay in one share has been written already.  The pieces of a row
-// are consecutive CTAs' and are loaded 16 at a time.
+// row; a row whose unit lay in one share has been written already.  Where a row's pieces lie
+// follows from the offsets and lengths, which are read before the wait for the kernel before,
+// so that after it one round trip brings the log-sum-exps (32 at once) and the first rows;
+// blocks of two warps fit beside that kernel's blocks in the register file.
 template <int D, bool kBF16>
-__global__ void __launch_bounds__(128) attn_tree_merge_kernel(const __grid_constant__ TreeParams p) {
+__global__ void __launch_bounds__(kMergeThreads) attn_tree_merge_kernel(const __grid_constant__ TreeParams p) {
     grid_launch_dependents();
-    grid_dependency_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const long long R = static_cast<long long>(blockIdx.x) * 4 + warp;
-    if (R >= static_cast<long long>(p.total_q) * p.Hq) return;
-    const int tok = static_cast<int>(R / p.Hq), head = static_cast<int>(R % p.Hq);
+    const long long R = static_cast<long long>(blockIdx.x) * (kMergeThreads / 32) + warp;
+    const bool in = R < static_cast<long long>(p.total_q) * p.Hq;
+    const int tok = static_cast<int>(R / p.Hq), head = static_cast<int>(R - static_cast<long long>(tok) * p.Hq);
     // the sequence of this token: the last one that starts at or before it
     int lo = 0, hi = p.n_seqs;  // cu[lo] <= tok < cu[hi], where the offsets ascend
     while (hi - lo > 1) {
@@ -787,7 +862,16 @@ __global__ void __launch_bounds__(128) attn_tree_merge_kernel(const __grid_const
         if (__ldg(p.cu + mid) <= tok) lo = mid; else hi = mid;
     }
     const TreeSeq q = tree_seq(p, lo);
-    if (tok < q.q0 || tok >= q.q0 + q.T) return;
+    const int nt = tree_key_tiles(q.L), mt = tree_row_tiles(p, q.T);
+    const int t = tok - q.q0, m = t / p.rt;
+    const int prow = (t - m * p.rt) * p.group + head % p.group;  // row within the tile
+    grid_dependency_wait();
+    if (!in || t < 0 || t >= q.T) return;
+    const int share = p.plan[0];
+    // the weights of the unit's first and last tile
+    const int uw = tree_unit_weight(nt), u1 = p.plan[1 + lo] + ((head / p.group) * mt + m + 1) * uw - 1;
+    const int c0 = (u1 - nt + 1) / share, c1 = u1 / share;
+    if (c0 == c1) return;
     constexpr int kPer = D / 32;
     uint8_t *dst = static_cast<uint8_t *>(p.o) + tok * p.o_row + head * p.o_head + lane * kPer * 2;
     auto store = [&](const uint32_t (&w)[kPer / 2]) {
@@ -801,36 +885,21 @@ __global__ void __launch_bounds__(128) attn_tree_merge_kernel(const __grid_const
         // the kernel before gave up on a wait: its pieces may be stale
         uint32_t w[kPer / 2];
 #pragma unroll
-        for (int t = 0; t < kPer / 2; ++t) w[t] = kBF16 ? 0x7FC07FC0u : 0x7E007E00u;
+        for (int i = 0; i < kPer / 2; ++i) w[i] = kBF16 ? 0x7FC07FC0u : 0x7E007E00u;
         store(w);
         if (lse_out != nullptr && lane == 0) *lse_out = __int_as_float(0x7FC00000);
         return;
     }
-    const int share = p.plan[0];
-    const int nt = tree_key_tiles(q.L), mt = tree_row_tiles(p, q.T);
-    const int t = tok - q.q0, m = t / p.rt;
-    const int u0 = p.plan[1 + lo] + ((head / p.group) * mt + m) * nt;  // the unit's first tile
-    const int c0 = u0 / share, c1 = (u0 + nt - 1) / share;
-    if (c0 == c1) return;
-    const int prow = (t - m * p.rt) * p.group + head % p.group;  // row within the tile
     // CTA c0's piece begins at the unit's start (slot 1), the others in mid-unit (slot 0)
     auto row_of = [&](int c) { return (static_cast<size_t>(c) * 2 + (c == c0 ? 1 : 0)) * kBM + prow; };
-    constexpr int kBatch = 16;
+    constexpr int kBatch = 4;
     float acc[kPer];
 #pragma unroll
     for (int d = 0; d < kPer; ++d) acc[d] = 0.f;
     float mx = -INFINITY, sum = 0.f;
-    for (int s0 = c0; s0 <= c1; s0 += kBatch) {
-        const int n = c1 + 1 - s0 < kBatch ? c1 + 1 - s0 : kBatch;
+    for (int s0 = c0; s0 <= c1; s0 += 32) {
+        const int n = c1 + 1 - s0 < 32 ? c1 + 1 - s0 : 32;
         const float ls = lane < n ? p.part_lse[row_of(s0 + lane)] : -INFINITY;
-        float v[kBatch][kPer];
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i)
-            if (i < n) {
-                const float *src = p.part_o + row_of(s0 + i) * D + lane * kPer;
-#pragma unroll
-                for (int d = 0; d < kPer; ++d) v[i][d] = src[d];
-            }
         float bm = ls;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, o));
@@ -842,12 +911,23 @@ __global__ void __launch_bounds__(128) attn_tree_merge_kernel(const __grid_const
         mx = m_new;
         const float wl = ls == -INFINITY ? 0.f : expf(ls - mx);
         sum += wl;
+        for (int i0 = 0; i0 < n; i0 += kBatch) {
+            float v[kBatch][kPer];
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            const float w = __shfl_sync(0xffffffffu, wl, i);
-            if (i < n && w != 0.f) {
+            for (int i = 0; i < kBatch; ++i) {
+                const float *src = p.part_o + row_of(i0 + i < n ? s0 + i0 + i : s0) * D + lane * kPer;
+                if constexpr (kPer == 4)
+                    *reinterpret_cast<float4 *>(v[i]) = *reinterpret_cast<const float4 *>(src);
+                else
+                    *reinterpret_cast<float2 *>(v[i]) = *reinterpret_cast<const float2 *>(src);
+            }
 #pragma unroll
-                for (int d = 0; d < kPer; ++d) acc[d] += w * v[i][d];
+            for (int i = 0; i < kBatch; ++i) {
+                const float w = __shfl_sync(0xffffffffu, wl, (i0 + i) & 31);
+                if (i0 + i < n && w != 0.f) {
+#pragma unroll
+                    for (int d = 0; d < kPer; ++d) acc[d] += w * v[i][d];
+                }
             }
         }
     }

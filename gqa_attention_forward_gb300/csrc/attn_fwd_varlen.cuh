@@ -303,6 +303,17 @@ __device__ __forceinline__ void add_nonfinite(uint8_t *o_row, const uint8_t *v_r
     }
 }
 
+// As add_nonfinite, for a row of fp32 partial results.
+template <int D, bool kBF16>
+__device__ __forceinline__ void add_nonfinite_f32(float *o_row, const uint8_t *v_row) {
+#pragma unroll 1
+    for (int d = 0; d < D; ++d) {
+        const uint32_t x = reinterpret_cast<const uint16_t *>(v_row)[d];
+        volatile float *o = o_row + d;
+        if (nonfinite16<kBF16>(x)) *o = *o + unpack2<kBF16>(x).x;
+    }
+}
+
 // The guard's work on one V tile in shared memory: rows at or past `rows` become zero;
 // with `scan`, non-finite values of the rows before are zeroed and their rows noted.
 template <int D, bool kBF16>

@@ -119,7 +119,9 @@ attn_status_t launch_tree(int dev, int kid, const CUtensorMap &tq, const CUtenso
     if (attn_status_t st = launch_dependent(kern, grid, gqa::kTreeThreads, smem, s, tq, tk, tv, prm); st != ATTN_OK)
         return st;
     const long long rows = static_cast<long long>(prm.total_q) * prm.Hq;
-    return launch_dependent(gqa::attn_tree_merge_kernel<D, BF16>, static_cast<unsigned>((rows + 3) / 4), 128, 0, s, prm);
+    constexpr int per = gqa::kMergeThreads / 32;
+    return launch_dependent(gqa::attn_tree_merge_kernel<D, BF16>, static_cast<unsigned>((rows + per - 1) / per),
+                            gqa::kMergeThreads, 0, s, prm);
 }
 
 // Least key tiles per CTA of the tree kernel.
@@ -295,7 +297,7 @@ attn_status_t attn_fwd_tree(const void *q, const attn_kv_cache_t *cache, int lay
     prm.rt = 128 / (Hq / Hkv);
     const long long row_tiles = static_cast<long long>(total_q) / prm.rt + n_seqs;
     const long long key_tiles = (static_cast<long long>(cache->table_width) * cache->page + 127) / 128;
-    if (row_tiles * Hkv > INT_MAX / 2 / key_tiles || static_cast<long long>(total_q) * Hq > INT_MAX) return ATTN_ERR_SHAPE;
+    if (row_tiles * Hkv > INT_MAX / 2 / (key_tiles + 1) || static_cast<long long>(total_q) * Hq > INT_MAX) return ATTN_ERR_SHAPE;
     int dev = 0;
     if (attn_status_t e = check_device(&dev); e != ATTN_OK) return e;
     size_t need = 0;
@@ -334,7 +336,7 @@ attn_status_t attn_fwd_tree(const void *q, const attn_kv_cache_t *cache, int lay
     if (!encode_packed_map(&tq, q, bf16, D, total_q, Hq, st[0], st[1], prm.rt, prm.group, &head_y) || head_y != 1 ||
         !encode_pool_map(&tk, kp, bf16, D, cache->page, slices) || !encode_pool_map(&tv, vp, bf16, D, cache->page, slices))
         return no_map();
-    const long long most = row_tiles * Hkv * key_tiles;
+    const long long most = row_tiles * Hkv * (key_tiles + 1);
     const unsigned grid = static_cast<unsigned>(most < sms ? most : sms);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int kid = (D == 128 ? 2 : 0) + (bf16 ? 1 : 0);
