@@ -16,10 +16,12 @@
 //     128-row tile (row = token * G + head in the group), so each K/V tile is read once per
 //     kv head and 128 / G tokens;
 //   * the key tiles of all (sequence, kv head, row tile) units form one list, of which every
-//     CTA takes an equal contiguous share, whatever the lengths are; a unit counts for one tile
-//     more than it has, which is what its change costs.  A unit cut by a share's border leaves
+//     CTA takes an equal contiguous share, whatever the lengths are; a unit counts for two tiles
+//     more than it has, about what its change costs.  A unit cut by a share's border leaves
 //     at most two pieces per CTA (fp32 O and log-sum-exp), merged by a second, dependent
-//     launch; the others write O themselves;
+//     launch; the others write O themselves.  (Merging in the CTA that brings the last piece
+//     saves the launch, but its round trips come one after another: one token over 4000
+//     positions 22.8 us instead of 16.5, 16 tokens over 32760 positions 86 instead of 47.);
 //   * the load order runs on across the units of a share: the next unit's first K tile is
 //     loaded, and its scores computed, before the last P V of the unit before, the page
 //     indexes of the next unit and of the next 32 pages are fetched ahead, and O has two
@@ -46,7 +48,7 @@ constexpr int kTreeThreads = 256;
 constexpr int kTreeSlots = 4;
 constexpr int kTreeMax = 128;      // tokens of one tree
 constexpr int kTreeSeqCache = 512; // sequences whose lengths are kept in shared memory
-constexpr int kMergeThreads = 64;
+constexpr int kMergeThreads = 32;
 constexpr int kTreeBadTiles = 2;   // the tree's positions lie in at most two key tiles
 
 struct TreeParams : Params {
@@ -59,7 +61,7 @@ struct TreeParams : Params {
     long long o_row, o_head;   // strides in bytes
     float *part_o;             // [2 * CTAs][128][D]
     float *part_lse;           // [2 * CTAs][128]
-    int *plan;                 // [0]: share, [1 + s]: first tile of sequence s
+    int grid;                  // CTAs of the first kernel
 };
 
 struct TreeUnit {
@@ -91,8 +93,8 @@ struct TreeLayout {
     static constexpr int kAbort = kTmemSlot + 4;
     static constexpr int kUnits = (kAbort + 4 + 15) & ~15;
     static constexpr int kPar = kUnits + kTreeSlots * static_cast<int>(sizeof(TreeUnit));
-    static constexpr int kSeqs = (kPar + 2 * kTreeMax * 4 + 7) & ~7;
-    static constexpr int kUsed = kSeqs + kTreeSeqCache * 8;
+    static constexpr int kSeqs = (kPar + 2 * kTreeMax * 4 + 15) & ~15;
+    static constexpr int kUsed = kSeqs + kTreeSeqCache * 16;
     // more than half of an SM's shared memory: one CTA (all 512 TMEM columns) per SM
     static constexpr int kAlloc = (kUsed + 1024) > 118 * 1024 ? (kUsed + 1024) : 118 * 1024;
 };
@@ -145,8 +147,19 @@ __device__ __forceinline__ Bits128 bits_shr(Bits128 b, int n) {
     return {(b.lo >> n) | (b.hi << (64 - n)), b.hi >> n};
 }
 
-// Weights of a unit in the shares: its key tiles and one for its change.
-__device__ __forceinline__ int tree_unit_weight(int key_tiles) { return key_tiles + 1; }
+// Weights of a unit in the shares: its key tiles and two for its change (with none a batch of
+// eight trees takes 71 us, with one 62.5, with two 61.7, with three 60.2; one tree over 131000
+// positions 98.9, 96.2, 94.1 and 96.3).
+__device__ __forceinline__ int tree_unit_weight(int key_tiles) { return key_tiles + 2; }
+
+// Weight of sequence s in the list of units.
+__device__ __forceinline__ int tree_seq_weight(const TreeParams &p, int T, int L) {
+    return p.Hkv * tree_row_tiles(p, T) * tree_unit_weight(tree_key_tiles(L));
+}
+__device__ __forceinline__ int tree_share(const TreeParams &p, int total) {
+    const int share = (total + p.grid - 1) / p.grid;
+    return share < p.min_share ? p.min_share : share;
+}
 
 // Ancestors of token t of a tree, itself among them; parents that are no earlier token end
 // the walk.  par(u): the parent of token u.
@@ -190,7 +203,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(smem + L::kTmemSlot);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kAbort);
     TreeUnit *units = reinterpret_cast<TreeUnit *>(smem + L::kUnits);
-    int2 *seqs = reinterpret_cast<int2 *>(smem + L::kSeqs);  // (T, L)
+    int4 *seqs = reinterpret_cast<int4 *>(smem + L::kSeqs);  // (T, L, q0, row)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 64) {
@@ -231,7 +244,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     grid_launch_dependents();
     for (int s = threadIdx.x; s < p.n_seqs && s < kTreeSeqCache; s += kTreeThreads) {
         const TreeSeq q = tree_seq(p, s);
-        seqs[s] = make_int2(q.T, q.L);
+        seqs[s] = make_int4(q.T, q.L, q.q0, q.row);
     }
     tc_fence_before();
     __syncthreads();
@@ -240,18 +253,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 
     if (warp == 3) {
         // -------------------------------------------------------- scheduler, and Q
+        auto seq_of = [&](int s) -> int4 {
+            if (s < kTreeSeqCache) return seqs[s];
+            const TreeSeq q = tree_seq(p, s);
+            return make_int4(q.T, q.L, q.q0, q.row);
+        };
         auto weight_of = [&](int s) -> int {
             if (s >= p.n_seqs) return 0;
-            int T, Ls;
-            if (s < kTreeSeqCache) {
-                T = seqs[s].x;
-                Ls = seqs[s].y;
-            } else {
-                const TreeSeq q = tree_seq(p, s);
-                T = q.T;
-                Ls = q.L;
-            }
-            return p.Hkv * tree_row_tiles(p, T) * tree_unit_weight(tree_key_tiles(Ls));
+            const int4 q = seq_of(s);
+            return tree_seq_weight(p, q.x, q.y);
         };
         auto scan = [&](int x) {  // inclusive prefix sum over the lanes
 #pragma unroll
@@ -263,100 +273,95 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         };
         int total = 0;
         for (int s0 = 0; s0 < p.n_seqs; s0 += 32) {
-            const int w = weight_of(s0 + lane), incl = scan(w);
-            if (blockIdx.x == 0 && s0 + lane < p.n_seqs) p.plan[1 + s0 + lane] = total + incl - w;
-            total += __shfl_sync(0xffffffffu, incl, 31);
+            total += __reduce_add_sync(0xffffffffu, weight_of(s0 + lane));
         }
-        int share = (total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
-        if (share < p.min_share) share = p.min_share;
-        if (blockIdx.x == 0 && lane == 0) p.plan[0] = share;
+        const int share = tree_share(p, total);
         // 64-bit: the last CTAs' first tiles may lie past the end
         const long long first = static_cast<long long>(blockIdx.x) * share;
         int at = first < total ? static_cast<int>(first) : total;
         const int end = first + share < total ? static_cast<int>(first + share) : total;
-        int slot = 0, q_loads = 0;
-        uint32_t phase = 0, n_units = 0;
-        int s0 = 0, before = 0;         // weights of the sequences before s0
-        bool ok = true;
-        for (;;) {
-            int seq = 0, nt = 0, unit = 0, k0 = 0, k1 = 0;
-            while (at < end && k0 == k1) {
-                int in_seq = 0;
-                for (;; s0 += 32) {
-                    const int w = weight_of(s0 + lane), incl = scan(w);
-                    const int all = __shfl_sync(0xffffffffu, incl, 31);
-                    if (at < before + all) {
-                        const int src = __ffs(__ballot_sync(0xffffffffu, before + incl > at)) - 1;
-                        seq = s0 + src;
-                        in_seq = at - before - __shfl_sync(0xffffffffu, incl - w, src);
-                        break;
+        int slot = 0, q_loads = 0, q_slot = 0;
+        uint32_t phase = 0, emitted = 0, q_done = 0;  // units handed out, and Q tiles of them asked for
+        int s0 = 0, before = 0;                       // weights of the sequences before s0
+        bool ok = true, more = true;
+        while (ok && (more || q_done < emitted)) {
+            // A Q tile that is owed is asked for as soon as the buffer is free (the last scores of
+            // the unit before are computed); until then further units are handed out, as far as
+            // slots are free: one that is not depends on that tile.
+            const bool owed = q_done < emitted;
+            const bool q_ready = owed && __all_sync(0xffffffffu, mbar_try_wait(q_empty, (q_done & 1u) ^ 1u));
+            if (!q_ready && more && (!owed || __all_sync(0xffffffffu, mbar_try_wait(unit_empty(slot), phase ^ 1u)))) {
+                int seq = 0, nt = 0, unit = 0, k0 = 0, k1 = 0;
+                while (at < end && k0 == k1) {
+                    int in_seq = 0;
+                    for (;; s0 += 32) {
+                        const int w = weight_of(s0 + lane), incl = scan(w);
+                        const int all = __shfl_sync(0xffffffffu, incl, 31);
+                        if (at < before + all) {
+                            const int src = __ffs(__ballot_sync(0xffffffffu, before + incl > at)) - 1;
+                            seq = s0 + src;
+                            in_seq = at - before - __shfl_sync(0xffffffffu, incl - w, src);
+                            break;
+                        }
+                        before += all;
                     }
-                    before += all;
+                    nt = tree_key_tiles(seq_of(seq).y);
+                    const int uw = tree_unit_weight(nt);
+                    unit = in_seq / uw;  // kv head * row tiles + row tile
+                    // weights [0, uw - nt) of a unit are its change, then come its tiles; a share that
+                    // ends within the change holds none of them
+                    const int w0 = in_seq - unit * uw, w1 = w0 + (end - at) < uw ? w0 + (end - at) : uw;
+                    k0 = w0 > uw - nt ? w0 - (uw - nt) : 0;
+                    k1 = w1 > uw - nt ? w1 - (uw - nt) : 0;
+                    at += w1 - w0;
                 }
-                const int Ls = seq < kTreeSeqCache ? seqs[seq].y : tree_seq(p, seq).L;
-                nt = tree_key_tiles(Ls);
-                const int uw = tree_unit_weight(nt);
-                unit = in_seq / uw;  // kv head * row tiles + row tile
-                // weights [0, uw - nt) of a unit are its change, then come its tiles; a share that
-                // ends within the change holds none of them
-                const int w0 = in_seq - unit * uw, w1 = w0 + (end - at) < uw ? w0 + (end - at) : uw;
-                k0 = w0 > uw - nt ? w0 - (uw - nt) : 0;
-                k1 = w1 > uw - nt ? w1 - (uw - nt) : 0;
-                at += w1 - w0;
-            }
-            const bool more = k0 < k1;
-            if (!__all_sync(0xffffffffu, wait_bar(unit_empty(slot), phase ^ 1u, p, abort_flag))) {
-                ok = false;
-                break;
-            }
-            TreeUnit &u = units[slot];
-            int q0 = 0, kvh = 0;
-            if (more) {
-                const TreeSeq q = tree_seq(p, seq);
-                const int mt = tree_row_tiles(p, q.T), t0 = (unit % mt) * p.rt;
-                q0 = q.q0 + t0;
-                kvh = unit / mt;
-                if (lane < kTreeBadTiles * 4) u.bad_rows[lane >> 2][lane & 3] = 0;
-                if (lane == 0) {
-                    u.valid = 1;
-                    u.t0 = t0;
-                    u.q0 = q0;
-                    u.ntok = q.T - t0 < p.rt ? q.T - t0 : p.rt;
-                    u.T = q.T;
-                    u.L = q.L;
-                    u.base = q.L > q.T ? q.L - q.T : 0;
-                    u.row = q.row;
-                    u.kvh = kvh;
-                    u.k0 = k0;
-                    u.k1 = k1;
-                    u.piece = (k0 == 0 && k1 == nt) ? -1 : (k0 > 0 ? 0 : 1);
-                    u.first = q.q0;
-                    u.bad = 0;
+                more = k0 < k1;
+                if (!(ok = __all_sync(0xffffffffu, wait_bar(unit_empty(slot), phase ^ 1u, p, abort_flag)))) break;
+                TreeUnit &u = units[slot];
+                if (more) {
+                    const int4 q = seq_of(seq);  // (T, L, q0, row)
+                    const int mt = tree_row_tiles(p, q.x), t0 = (unit % mt) * p.rt;
+                    if (lane < kTreeBadTiles * 4) u.bad_rows[lane >> 2][lane & 3] = 0;
+                    if (lane == 0) {
+                        u.valid = 1;
+                        u.t0 = t0;
+                        u.q0 = q.z + t0;
+                        u.ntok = q.x - t0 < p.rt ? q.x - t0 : p.rt;
+                        u.T = q.x;
+                        u.L = q.y;
+                        u.base = q.y > q.x ? q.y - q.x : 0;
+                        u.row = q.w;
+                        u.kvh = unit / mt;
+                        u.k0 = k0;
+                        u.k1 = k1;
+                        u.piece = (k0 == 0 && k1 == nt) ? -1 : (k0 > 0 ? 0 : 1);
+                        u.first = q.z;
+                        u.bad = 0;
+                    }
+                    ++emitted;
+                } else if (lane == 0) {
+                    u.valid = 0;
                 }
-            } else if (lane == 0) {
-                u.valid = 0;
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(unit_full(slot));
-            if (!more) break;
-            if (++slot == kTreeSlots) {
-                slot = 0;
-                phase ^= 1u;
-            }
-            // Q's buffer is free once the last scores of the unit before are computed
-            if (!__all_sync(0xffffffffu, wait_bar(q_empty, (n_units & 1u) ^ 1u, p, abort_flag))) {
-                ok = false;
-                break;
-            }
-            ++n_units;
-            if (!p.inject_stall) {
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(q_full, static_cast<uint32_t>(p.group * p.rt) * D * 2);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(unit_full(slot));
+                if (++slot == kTreeSlots) {
+                    slot = 0;
+                    phase ^= 1u;
+                }
+            } else {
+                if (!(ok = __all_sync(0xffffffffu, wait_bar(q_empty, (q_done & 1u) ^ 1u, p, abort_flag)))) break;
+                if (!p.inject_stall) {
+                    if (lane == 0) {
+                        const TreeUnit &u = units[q_slot];
+                        mbar_arrive_expect_tx(q_full, static_cast<uint32_t>(p.group * p.rt) * D * 2);
 #pragma unroll
-                    for (int a = 0; a < D / 64; ++a)
-                        tma_load_3d(sQ + a * kAtomBytes, &tmQ, 64 * a, kvh * p.group, q0, q_full);
+                        for (int a = 0; a < D / 64; ++a)
+                            tma_load_3d(sQ + a * kAtomBytes, &tmQ, 64 * a, u.kvh * p.group, u.q0, q_full);
+                    }
+                    ++q_loads;
                 }
-                ++q_loads;
+                ++q_done;
+                if (++q_slot == kTreeSlots) q_slot = 0;
             }
         }
         if (lane == 0 && q_loads > 0) drain_bar(q_full, (q_loads - 1) & 1, p);  // landed before the CTA exits
@@ -408,7 +413,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         int stage = 0, loads = 0;
         uint32_t phase = 0;
         Cur cur{}, nxt{};
-        bool have = false;  // nxt holds the unit after cur
         bool ok = __all_sync(0xffffffffu, wait_bar(unit_full(slot), uphase, p, abort_flag));
         if (ok) take(cur);
         // The order of the issuer: the first K tile, then for each key tile the K tile after it
@@ -423,17 +427,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                     bool of_next = false;
                     int t = h == 0 ? kt + 1 : kt;
                     if (h == 0 && t == cur.k1) {
-                        if (!have) {
-                            if (!(ok = __all_sync(0xffffffffu, wait_bar(unit_full(slot), uphase, p, abort_flag)))) break;
-                            take(nxt);
-                            have = true;
-                        }
+                        if (!(ok = __all_sync(0xffffffffu, wait_bar(unit_full(slot), uphase, p, abort_flag)))) break;
+                        take(nxt);
                         if (!nxt.valid) continue;
                         of_next = true;
                         t = nxt.k0;
-                    } else if (!have && __all_sync(0xffffffffu, mbar_try_wait(unit_full(slot), uphase))) {
-                        take(nxt);  // its page indexes are on their way by the time they are needed
-                        have = true;
                     }
                     const int first = (t << 7) >> p.page_shift;
                     // V is the last to use a window: the one after the next is fetched when V leaves it
@@ -470,7 +468,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 }
             }
             cur = nxt;
-            have = false;
         }
         if (lane == 0) {
             // every copy has landed before the CTA exits (also after a timeout)
@@ -664,40 +661,42 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                     tc_fence_after();
                     __syncwarp();
                     const uint32_t tS = tmem + 128u * b + lane_off, tO = tmem + 256u + 128u * ob + lane_off;
-                    uint32_t s[128];
-                    float mt;
-                    if ((kt + 1) * kBN <= tree0) {
-                        float mq[4];
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            tmem_ld32_max(tS + 32 * q, *reinterpret_cast<uint32_t(*)[32]>(&s[32 * q]), mq[q]);
-                        tmem_ld_wait(s, mq);
-                        mt = fmax3(mq[0], mq[1], fmaxf(mq[2], mq[3]));
-                    } else {
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            tmem_ld32(tS + 32 * q, *reinterpret_cast<uint32_t(*)[32]>(&s[32 * q]));
-                        tmem_ld_wait(s);
-                        // bit c: this row sees key kt * 128 + c
+                    // 32 columns at a time, in two passes over TMEM (the row's max, then its
+                    // weights): a quarter of the instructions of one pass over 128 columns in
+                    // registers, which together with the epilogue's did not stay in the instruction
+                    // cache (the first tile after an epilogue took 4700 cycles instead of 1200).
+                    const bool whole = (kt + 1) * kBN <= tree0;  // every row sees every key of the tile
+                    uint32_t w[4] = {~0u, ~0u, ~0u, ~0u};        // bit c: this row sees key kt * 128 + c
+                    if (!whole) {
                         const int sh = kt * kBN - tree0;
                         Bits128 see = sh >= 0 ? bits_shr(anc, sh) : bits_shl(anc, -sh);
                         const Bits128 old = bits_below(-sh);
                         see.lo |= old.lo;
                         see.hi |= old.hi;
-                        const uint32_t w[4] = {static_cast<uint32_t>(see.lo), static_cast<uint32_t>(see.lo >> 32),
-                                               static_cast<uint32_t>(see.hi), static_cast<uint32_t>(see.hi >> 32)};
+                        w[0] = static_cast<uint32_t>(see.lo);
+                        w[1] = static_cast<uint32_t>(see.lo >> 32);
+                        w[2] = static_cast<uint32_t>(see.hi);
+                        w[3] = static_cast<uint32_t>(see.hi >> 32);
+                    }
+                    float mt = -INFINITY;
+#pragma unroll 1
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t s[32];
+                        if (whole) {
+                            float mq[1];
+                            tmem_ld32_max(tS + 32 * q, s, mq[0]);
+                            tmem_ld_wait(s, mq);
+                            mt = fmaxf(mt, mq[0]);
+                        } else {
+                            tmem_ld32(tS + 32 * q, s);
+                            tmem_ld_wait(s);
+                            const uint32_t wq32 = q == 0 ? w[0] : q == 1 ? w[1] : q == 2 ? w[2] : w[3];
+                            float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                        for (int cc = 0; cc < 128; ++cc)
-                            if (!((w[cc >> 5] >> (cc & 31)) & 1u)) s[cc] = __float_as_uint(-INFINITY);
-                        float mx[8];
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) mx[k] = fmaxf(u2f(s[2 * k]), u2f(s[2 * k + 1]));
-#pragma unroll
-                        for (int cc = 16; cc < 128; cc += 16)
-#pragma unroll
-                            for (int k = 0; k < 8; ++k)
-                                mx[k] = fmax3(mx[k], u2f(s[cc + 2 * k]), u2f(s[cc + 2 * k + 1]));
-                        mt = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
+                            for (int e = 0; e < 32; ++e)
+                                mx[e & 1] = fmaxf(mx[e & 1], (wq32 >> e) & 1u ? u2f(s[e]) : -INFINITY);
+                            mt = fmax3(mt, mx[0], mx[1]);
+                        }
                     }
                     const float m_new = fmaxf(mrow, mt);
                     // a row that has seen no key yet takes its weights, all 0, against 0
@@ -710,7 +709,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                             break;
                         tc_fence_after();
                         __syncwarp();
-#pragma unroll
+#pragma unroll 1
                         for (int q = 0; q < D / 32; ++q) {
                             uint32_t o[32];
                             tmem_ld32(tO + 32 * q, o);
@@ -724,13 +723,22 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                     const float2 c2 = make_float2(c, c);
                     const float2 nmc2 = make_float2(-m_use * c, -m_use * c);
                     float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
+                    // P (16 columns of pairs) overwrites scores that have been read
+#pragma unroll 1
                     for (int q = 0; q < 4; ++q) {
+                        uint32_t s[32];
+                        tmem_ld32(tS + 32 * q, s);
+                        tmem_ld_wait(s);
+                        if (!whole) {
+                            const uint32_t wq32 = q == 0 ? w[0] : q == 1 ? w[1] : q == 2 ? w[2] : w[3];
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (!((wq32 >> e) & 1u)) s[e] = __float_as_uint(-INFINITY);
+                        }
                         uint32_t pk[16];
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
-                            const int cc = 32 * q + 2 * e;
-                            float2 x = ffma2(make_float2(u2f(s[cc]), u2f(s[cc + 1])), c2, nmc2);
+                            float2 x = ffma2(make_float2(u2f(s[2 * e]), u2f(s[2 * e + 1])), c2, nmc2);
                             x.x = ex2_approx(x.x);
                             x.y = ex2_approx(x.y);
                             acc[e & 1] = fadd2(acc[e & 1], x);
@@ -768,7 +776,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                     const size_t prow = (static_cast<size_t>(blockIdx.x) * 2 + (u.piece > 0 ? 1 : 0)) * kBM + r;
                     float *part = p.part_o + prow * D;
                     const bool whole = u.piece < 0;
-#pragma unroll
+#pragma unroll 1
                     for (int q = 0; q < D / 32; ++q) {
                         uint32_t o[32];
                         tmem_ld32(tO + 32 * q, o);
@@ -846,8 +854,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 // deepseek.csdn.net/6a3201f8..., section "在线softmax", across CTAs).  One warp per output
 // row; a row whose unit lay in one share has been written already.  Where a row's pieces lie
 // follows from the offsets and lengths, which are read before the wait for the kernel before,
-// so that after it one round trip brings the log-sum-exps (32 at once) and the first rows;
-// blocks of two warps fit beside that kernel's blocks in the register file.
+// so that after it one round trip brings the log-sum-exps (lane j: piece j) and the rows of
+// the first 8 pieces.
 template <int D, bool kBF16>
 __global__ void __launch_bounds__(kMergeThreads) attn_tree_merge_kernel(const __grid_constant__ TreeParams p) {
     grid_launch_dependents();
@@ -862,84 +870,79 @@ __global__ void __launch_bounds__(kMergeThreads) attn_tree_merge_kernel(const __
         if (__ldg(p.cu + mid) <= tok) lo = mid; else hi = mid;
     }
     const TreeSeq q = tree_seq(p, lo);
-    const int nt = tree_key_tiles(q.L), mt = tree_row_tiles(p, q.T);
+    int total = 0, before = 0;  // weights of all sequences, and of those before this one
+    for (int s0 = 0; s0 < p.n_seqs; s0 += 32) {
+        const int s = s0 + lane;
+        const TreeSeq x = s < p.n_seqs ? tree_seq(p, s) : TreeSeq{0, 0, 0, 0, false};
+        const int w = s < p.n_seqs ? tree_seq_weight(p, x.T, x.L) : 0;
+        total += __reduce_add_sync(0xffffffffu, w);
+        before += __reduce_add_sync(0xffffffffu, s < lo ? w : 0);
+    }
+    const int share = tree_share(p, total);
+    const int nt = tree_key_tiles(q.L), mt = tree_row_tiles(p, q.T), uw = tree_unit_weight(nt);
     const int t = tok - q.q0, m = t / p.rt;
     const int prow = (t - m * p.rt) * p.group + head % p.group;  // row within the tile
+    // the weight past the unit's last tile, and the CTAs of its first and last one
+    const int end = before + ((head / p.group) * mt + m + 1) * uw;
+    const int c0 = (end - nt) / share, c1 = (end - 1) / share;
     grid_dependency_wait();
-    if (!in || t < 0 || t >= q.T) return;
-    const int share = p.plan[0];
-    // the weights of the unit's first and last tile
-    const int uw = tree_unit_weight(nt), u1 = p.plan[1 + lo] + ((head / p.group) * mt + m + 1) * uw - 1;
-    const int c0 = (u1 - nt + 1) / share, c1 = u1 / share;
-    if (c0 == c1) return;
+    if (!in || t < 0 || t >= q.T || c0 == c1) return;
     constexpr int kPer = D / 32;
-    uint8_t *dst = static_cast<uint8_t *>(p.o) + tok * p.o_row + head * p.o_head + lane * kPer * 2;
-    auto store = [&](const uint32_t (&w)[kPer / 2]) {
-        if constexpr (kPer == 4)
-            *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
-        else
-            *reinterpret_cast<uint32_t *>(dst) = w[0];
-    };
-    float *lse_out = p.lse == nullptr ? nullptr : p.lse + static_cast<size_t>(head) * p.total_q + tok;
-    if (*reinterpret_cast<volatile unsigned int *>(&g_abort_seq) == p.seq) {
-        // the kernel before gave up on a wait: its pieces may be stale
-        uint32_t w[kPer / 2];
-#pragma unroll
-        for (int i = 0; i < kPer / 2; ++i) w[i] = kBF16 ? 0x7FC07FC0u : 0x7E007E00u;
-        store(w);
-        if (lse_out != nullptr && lane == 0) *lse_out = __int_as_float(0x7FC00000);
-        return;
-    }
+    // where the kernel before gave up on a wait, its pieces may be stale: NaN
+    const bool gave_up = *reinterpret_cast<volatile unsigned int *>(&g_abort_seq) == p.seq;
     // CTA c0's piece begins at the unit's start (slot 1), the others in mid-unit (slot 0)
     auto row_of = [&](int c) { return (static_cast<size_t>(c) * 2 + (c == c0 ? 1 : 0)) * kBM + prow; };
-    constexpr int kBatch = 4;
     float acc[kPer];
 #pragma unroll
     for (int d = 0; d < kPer; ++d) acc[d] = 0.f;
     float mx = -INFINITY, sum = 0.f;
-    for (int s0 = c0; s0 <= c1; s0 += 32) {
-        const int n = c1 + 1 - s0 < 32 ? c1 + 1 - s0 : 32;
-        const float ls = lane < n ? p.part_lse[row_of(s0 + lane)] : -INFINITY;
+#pragma unroll 1
+    for (int s0 = c0; s0 <= c1; s0 += 8) {
+        const float ls = lane < 8 && s0 + lane <= c1 ? p.part_lse[row_of(s0 + lane)] : -INFINITY;
+        float v[8][kPer];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float *src = p.part_o + row_of(s0 + j <= c1 ? s0 + j : c1) * D + lane * kPer;
+            if constexpr (kPer == 4)
+                *reinterpret_cast<float4 *>(v[j]) = *reinterpret_cast<const float4 *>(src);
+            else
+                *reinterpret_cast<float2 *>(v[j]) = *reinterpret_cast<const float2 *>(src);
+        }
         float bm = ls;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, o));
+        for (int o = 4; o > 0; o >>= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, o));
+        bm = __shfl_sync(0xffffffffu, bm, 0);
         const float m_new = fmaxf(mx, bm);
         const float old = mx == -INFINITY ? 0.f : expf(mx - m_new);
+        const float wl = ls == -INFINITY ? 0.f : expf(ls - m_new);
+        sum = sum * old + wl;  // of this lane's pieces
+        mx = m_new;
 #pragma unroll
         for (int d = 0; d < kPer; ++d) acc[d] *= old;
-        sum *= old;
-        mx = m_new;
-        const float wl = ls == -INFINITY ? 0.f : expf(ls - mx);
-        sum += wl;
-        for (int i0 = 0; i0 < n; i0 += kBatch) {
-            float v[kBatch][kPer];
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                const float *src = p.part_o + row_of(i0 + i < n ? s0 + i0 + i : s0) * D + lane * kPer;
-                if constexpr (kPer == 4)
-                    *reinterpret_cast<float4 *>(v[i]) = *reinterpret_cast<const float4 *>(src);
-                else
-                    *reinterpret_cast<float2 *>(v[i]) = *reinterpret_cast<const float2 *>(src);
-            }
+        for (int j = 0; j < 8; ++j) {
+            const float w = __shfl_sync(0xffffffffu, wl, j);
+            if (s0 + j <= c1 && w != 0.f) {
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                const float w = __shfl_sync(0xffffffffu, wl, (i0 + i) & 31);
-                if (i0 + i < n && w != 0.f) {
-#pragma unroll
-                    for (int d = 0; d < kPer; ++d) acc[d] += w * v[i][d];
-                }
+                for (int d = 0; d < kPer; ++d) acc[d] += w * v[j][d];
             }
         }
     }
-    // every lane holds its own pieces' weights in `sum`
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;  // 0: the row saw no key
+    for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    sum = __shfl_sync(0xffffffffu, sum, 0);
+    const float inv = gave_up ? __int_as_float(0x7FC00000) : (sum == 0.f ? 0.f : 1.f / sum);  // 0: the row saw no key
+    uint8_t *dst = static_cast<uint8_t *>(p.o) + tok * p.o_row + head * p.o_head + lane * kPer * 2;
     uint32_t w[kPer / 2];
 #pragma unroll
     for (int i = 0; i < kPer / 2; ++i) w[i] = pack2<kBF16>(acc[2 * i] * inv, acc[2 * i + 1] * inv);
-    store(w);
-    if (lse_out != nullptr && lane == 0) *lse_out = sum == 0.f ? -INFINITY : mx + logf(sum);
+    if constexpr (kPer == 4)
+        *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
+    else
+        *reinterpret_cast<uint32_t *>(dst) = w[0];
+    if (p.lse != nullptr && lane == 0)
+        p.lse[static_cast<size_t>(head) * p.total_q + tok] =
+            gave_up ? __int_as_float(0x7FC00000) : (sum == 0.f ? -INFINITY : mx + logf(sum));
 }
 
 }  // namespace gqa

@@ -116,7 +116,8 @@ attn_status_t launch_tree(int dev, int kid, const CUtensorMap &tq, const CUtenso
     auto kern = gqa::attn_fwd_tree_kernel<D, BF16>;
     constexpr int smem = gqa::TreeLayout<D>::kAlloc;
     if (attn_status_t st = set_smem_limit(dev, 32 + kid, kern, smem); st != ATTN_OK) return st;
-    if (attn_status_t st = launch_dependent(kern, grid, gqa::kTreeThreads, smem, s, tq, tk, tv, prm); st != ATTN_OK)
+    if (attn_status_t st = launch_dependent(kern, grid, gqa::kTreeThreads, smem, s, tq, tk, tv, prm);
+        st != ATTN_OK)
         return st;
     const long long rows = static_cast<long long>(prm.total_q) * prm.Hq;
     constexpr int per = gqa::kMergeThreads / 32;
@@ -124,8 +125,8 @@ attn_status_t launch_tree(int dev, int kid, const CUtensorMap &tq, const CUtenso
                             gqa::kMergeThreads, 0, s, prm);
 }
 
-// Least key tiles per CTA of the tree kernel.
-constexpr int kTreeMinShare = 1;
+// Least weight of a CTA's share in the tree kernel (a unit of one key tile weighs two).
+constexpr int kTreeMinShare = 2;
 
 int log2_of(int x) {
     int n = 0;
@@ -261,15 +262,14 @@ attn_status_t attn_fwd_varlen(const void *q, const void *k, const void *v, void 
     }
 }
 
-attn_status_t attn_fwd_tree_workspace(int n_seqs, int D, size_t *bytes) {
+attn_status_t attn_fwd_tree_workspace(int D, size_t *bytes) {
     if (bytes == nullptr) return ATTN_ERR_NULL;
     *bytes = 0;
-    if (n_seqs < 0) return ATTN_ERR_SHAPE;
     if (D != 64 && D != 128) return ATTN_ERR_HEADDIM;
     int dev = 0;
     if (attn_status_t st = check_device(&dev); st != ATTN_OK) return st;
     const size_t rows = static_cast<size_t>(g_dev_sms[dev]) * 2 * gqa::kBM;
-    *bytes = rows * (D + 1) * sizeof(float) + (static_cast<size_t>(n_seqs) + 1) * sizeof(int);
+    *bytes = rows * (D + 1) * sizeof(float);
     return ATTN_OK;
 }
 
@@ -301,7 +301,7 @@ attn_status_t attn_fwd_tree(const void *q, const attn_kv_cache_t *cache, int lay
     int dev = 0;
     if (attn_status_t e = check_device(&dev); e != ATTN_OK) return e;
     size_t need = 0;
-    if (attn_status_t e = attn_fwd_tree_workspace(n_seqs, D, &need); e != ATTN_OK) return e;
+    if (attn_status_t e = attn_fwd_tree_workspace(D, &need); e != ATTN_OK) return e;
     if (workspace_bytes < need) return ATTN_ERR_SCRATCH;
     common_params(prm, o, lse, Hq, Hkv, scale);
     const size_t layer_bytes = static_cast<size_t>(cache->n_pages) * Hkv * cache->page * D * 2;
@@ -328,7 +328,6 @@ attn_status_t attn_fwd_tree(const void *q, const attn_kv_cache_t *cache, int lay
     const int sms = g_dev_sms[dev];
     prm.part_o = static_cast<float *>(workspace);
     prm.part_lse = prm.part_o + static_cast<size_t>(sms) * 2 * gqa::kBM * D;
-    prm.plan = reinterpret_cast<int *>(prm.part_lse + static_cast<size_t>(sms) * 2 * gqa::kBM);
     const bool bf16 = cache->dtype == ATTN_BF16;
     CUtensorMap tq, tk, tv;
     int head_y = 0;
@@ -338,6 +337,7 @@ attn_status_t attn_fwd_tree(const void *q, const attn_kv_cache_t *cache, int lay
         return no_map();
     const long long most = row_tiles * Hkv * (key_tiles + 1);
     const unsigned grid = static_cast<unsigned>(most < sms ? most : sms);
+    prm.grid = static_cast<int>(grid);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int kid = (D == 128 ? 2 : 0) + (bf16 ? 1 : 0);
     switch (kid) {

@@ -394,7 +394,7 @@ attn_status_t attn_kv_compact(const attn_kv_cache_t *cache, int *live, void *str
  * the sequence's positions and bad offsets or sequences (ATTN_ERR_SHAPE), whose rows are then
  * undefined, and missing pages (ATTN_ERR_PAGE), which read as zeros.
  */
-attn_status_t attn_fwd_tree_workspace(int n_seqs, int D, size_t *bytes);
+attn_status_t attn_fwd_tree_workspace(int D, size_t *bytes);
 attn_status_t attn_fwd_tree(const void *q, const attn_kv_cache_t *cache, int layer, void *o,
                             float *lse, const int *cu, const int *seqs, const int *parents,
                             int n_seqs, int total_q, int Hq, const long long *strides,

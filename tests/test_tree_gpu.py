@@ -228,7 +228,7 @@ def test_captured_call_replays_on_new_lengths_trees_and_pages():
     p = i32([x for t in trees(T, 0) for x in t])
     cu = offsets(T)
     o, lse = torch.zeros_like(q), torch.zeros((8, 18), device="cuda")
-    n = binding.attn_fwd_tree_workspace(3, 128)[1]
+    n = binding.attn_fwd_tree_workspace(128)[1]
     ws = torch.empty(n, dtype=torch.uint8, device="cuda")
     binding.attention_tree(q, cache, cu, parents=p, out=o, lse_out=lse, workspace=ws)
     torch.cuda.synchronize()
