@@ -698,11 +698,21 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                             mt = fmax3(mt, mx[0], mx[1]);
                         }
                     }
-                    const float m_new = fmaxf(mrow, mt);
+                    // The weights are taken against a stale max (mrow) until the true one is 2^8 above
+                    // it: a rescale waits for the P V before, and on fresh rows the max grows in most
+                    // of the first tiles.  Rows without a token ask for none.
+                    float alpha = 1.f;
+                    bool rescale = false;
+                    if (mrow == -INFINITY) {
+                        mrow = mt;  // nothing seen so far: the accumulator holds zeros at most
+                    } else if (valid && (mt - mrow) * c > kRescaleLog2) {
+                        alpha = ex2_approx((mrow - mt) * c);
+                        mrow = mt;
+                        rescale = true;
+                    }
                     // a row that has seen no key yet takes its weights, all 0, against 0
-                    const float m_use = m_new == -INFINITY ? 0.f : m_new;
-                    const float alpha = ex2_approx((mrow - m_use) * c);
-                    if (kt > k0 && __any_sync(0xffffffffu, m_new > mrow)) {
+                    const float m_use = mrow == -INFINITY ? 0.f : mrow;
+                    if (__any_sync(0xffffffffu, rescale)) {
                         // rescale O: the P V before must have finished writing it
                         if (!__all_sync(0xffffffffu,
                                         wait_bar(o_done((jj - 1) & 1u), ((jj - 1) >> 1) & 1u, p, abort_flag)))
@@ -719,7 +729,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                             tmem_st32(tO + 32 * q, o);
                         }
                     }
-                    mrow = m_new;
                     const float2 c2 = make_float2(c, c);
                     const float2 nmc2 = make_float2(-m_use * c, -m_use * c);
                     float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
