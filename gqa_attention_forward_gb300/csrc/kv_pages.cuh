@@ -177,13 +177,13 @@ __global__ void __launch_bounds__(kPlanThreads) kv_extend_kernel(const KvPool c,
     }
 }
 
-// Children take the full pages of their parents (one reference more each) and a free page
-// for the last one that is not full; pairs lists what kv_move_kernel then copies.
+// Children take the lengths of their parents and a free page for the last page that is not
+// full; pairs lists what kv_move_kernel<kMoveFork> then copies, beside the table entries of the
+// full pages and their references, which one block would take too long over.
 __global__ void __launch_bounds__(kPlanThreads) kv_fork_kernel(const KvPool c, const int *parents, const int *children, int n) {
     __shared__ int sm[33];
     grid_launch_dependents();
     grid_dependency_wait();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     auto in = [&](int s) { return s >= 0 && s < c.n_rows; };
     for (int i = threadIdx.x; i < n; i += kPlanThreads) {
         const int a = parents[i], b = children[i];
@@ -218,34 +218,23 @@ __global__ void __launch_bounds__(kPlanThreads) kv_fork_kernel(const KvPool c, c
     const int have = kv_list<true>(c.refs, 0, c.n_pages, want < c.n_pages ? want : c.n_pages, c.list, sm);
     __syncthreads();
     if (have < want && threadIdx.x == 0) kv_error(ATTN_ERR_POOL);
-    for (int i = warp; i < n; i += kPlanThreads / 32) {
+    for (int i = threadIdx.x; i < n; i += kPlanThreads) {
         const int off = c.need[i], past = i + 1 < n ? c.need[i + 1] : want;
-        if (c.pairs[3 * i] == -2 || past > have) {
-            __syncwarp();
-            if (lane == 0) c.pairs[3 * i] = -1;
+        if (c.pairs[3 * i] == -2) continue;
+        if (past > have) {
+            c.pairs[3 * i] = -2;
             continue;
         }
         const int a = parents[i], b = children[i], len = c.lens[a];
-        const int full = len >> c.page_shift;
-        for (int j = lane; j < full; j += 32) {
-            const int p = kv_row(c, a)[j];
-            if (p >= 0 && p < c.n_pages)
-                atomicAdd(&c.refs[p], 1);
-            else
-                kv_error(ATTN_ERR_PAGE);
-            kv_row(c, b)[j] = p;
+        if (past > off) {
+            const int p = c.list[off], full = len >> c.page_shift;
+            c.pairs[3 * i] = kv_row(c, a)[full];
+            c.pairs[3 * i + 1] = p;
+            c.pairs[3 * i + 2] = len & (c.page - 1);
+            kv_row(c, b)[full] = p;
+            c.refs[p] = 1;
         }
-        if (lane == 0) {
-            if (past > off) {
-                const int p = c.list[off];
-                c.pairs[3 * i + 1] = p;
-                c.pairs[3 * i + 2] = len & (c.page - 1);
-                c.pairs[3 * i] = kv_row(c, a)[full];
-                kv_row(c, b)[full] = p;
-                c.refs[p] = 1;
-            }
-            c.lens[b] = len;
-        }
+        c.lens[b] = len;
     }
 }
 
@@ -308,11 +297,30 @@ __device__ __forceinline__ void kv_rename(const KvPool &c, long long first, long
     }
 }
 
+// The full pages of forked sequences: one reference more each.
+__device__ __forceinline__ void kv_share(const KvPool &c, const int *parents, const int *children, int n,
+                                         long long first, long long step) {
+    const long long entries = static_cast<long long>(n) * c.table_w;
+    for (long long t = first; t < entries; t += step) {
+        const int i = static_cast<int>(t / c.table_w), j = static_cast<int>(t - static_cast<long long>(i) * c.table_w);
+        if (c.pairs[3 * i] == -2) continue;  // refused
+        const int b = children[i];
+        if (j >= c.lens[b] >> c.page_shift) continue;
+        const int p = kv_row(c, parents[i])[j];
+        if (p >= 0 && p < c.n_pages)
+            atomicAdd(&c.refs[p], 1);
+        else
+            kv_error(ATTN_ERR_PAGE);
+        kv_row(c, b)[j] = p;
+    }
+}
+
 enum KvMove { kMoveCopy, kMoveFork, kMoveCompact };
 
 // Copies rows of pages in every layer, K and V: a warp moves up to 4 KB of one head of one
-// page at a time.  kMoveCopy: pages src[i] -> dst[i]; kMoveFork: the pairs of kv_fork_kernel;
-// kMoveCompact: the movers and holes of kv_compact_kernel, and the table entries renamed.
+// page at a time.  kMoveCopy: pages src[i] -> dst[i]; kMoveFork: the pairs of kv_fork_kernel
+// for parents src, children dst, and their tables; kMoveCompact: the movers and holes of
+// kv_compact_kernel, and the table entries renamed.
 template <KvMove kMove>
 __global__ void __launch_bounds__(256) kv_move_kernel(const KvPool c, const int *src, const int *dst, int n) {
     grid_launch_dependents();
@@ -323,6 +331,8 @@ __global__ void __launch_bounds__(256) kv_move_kernel(const KvPool c, const int 
         n = c.count[0];
         kv_rename(c, static_cast<long long>(blockIdx.x) * 256 + threadIdx.x, 256ll * gridDim.x);
     }
+    if (kMove == kMoveFork)
+        kv_share(c, src, dst, n, static_cast<long long>(blockIdx.x) * 256 + threadIdx.x, 256ll * gridDim.x);
     const int head16 = c.page * c.row16;         // 16-byte chunks of one head of a page
     const int segs = (head16 + 255) >> 8;        // of 4 KB
     const unsigned per = static_cast<unsigned>(c.n_layers) * 2u * c.Hkv * segs;  // segments per page
@@ -368,75 +378,71 @@ __global__ void __launch_bounds__(256) kv_move_kernel(const KvPool c, const int 
 }
 
 // Rows of new tokens into their pages: sequence s's tokens [cu[s], cu[s+1]) are its last
-// positions.  A block takes kAppendTokens tokens: one thread per token finds its page row,
-// then all threads copy 16-byte chunks (of all heads, K and V).
-constexpr int kAppendTokens = 16;
+// positions.  A warp per token: it asks for the token's rows (all heads, K and V, 16 bytes a
+// lane) and looks for their place, a chain of dependent loads, while they are on their way.
 struct KvAppend {
     const uint4 *k, *v;                        // of the layer's new rows
     long long k_row, k_head, v_row, v_head;    // strides in 16-byte chunks
     const int *cu, *seqs;
     int n, total, layer;
 };
+// Where token t's rows go: page * Hkv * page rows + row within the page, or -1 (behind the last
+// sequence, or refused).
+__device__ __forceinline__ long long append_place(const KvPool &c, const KvAppend &x, int t) {
+    int lo = 0, hi = x.n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (__ldg(x.cu + mid) <= t) lo = mid; else hi = mid;
+    }
+    const int a = __ldg(x.cu + lo), b = __ldg(x.cu + lo + 1);
+    if (t < a || t >= b) return -1;
+    const int s = x.seqs != nullptr ? __ldg(x.seqs + lo) : lo;
+    if (s < 0 || s >= c.n_rows) {
+        kv_error(ATTN_ERR_SHAPE);
+        return -1;
+    }
+    const int len = c.lens[s], pos = len - (b - t);
+    // none of a sequence's rows where it has fewer positions than new tokens
+    if (static_cast<long long>(b) - a > len || (pos >> c.page_shift) >= c.table_w) {
+        kv_error(ATTN_ERR_SHAPE);
+        return -1;
+    }
+    const int p = kv_row(c, s)[pos >> c.page_shift];
+    if (p < 0 || p >= c.n_pages || c.refs[p] != 1) {
+        kv_error(ATTN_ERR_PAGE);  // no page, or one that another sequence shares
+        return -1;
+    }
+    return static_cast<long long>(p) * c.Hkv * c.page + (pos & (c.page - 1));
+}
+
 __global__ void __launch_bounds__(256) kv_append_kernel(const KvPool c, const KvAppend x) {
-    __shared__ long long place[kAppendTokens];  // page * Hkv * page rows + row within the page, or -1
     grid_launch_dependents();
     grid_dependency_wait();
-    const int tok0 = blockIdx.x * kAppendTokens;
-    if (threadIdx.x < kAppendTokens) {
-        const int t = tok0 + threadIdx.x;
-        long long at = -1;
-        if (t < x.total) {
-            int lo = 0, hi = x.n;
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (__ldg(x.cu + mid) <= t) lo = mid; else hi = mid;
-            }
-            const int a = __ldg(x.cu + lo), b = __ldg(x.cu + lo + 1);
-            if (t >= a && t < b) {  // else: behind the last sequence
-                const int s = x.seqs != nullptr ? __ldg(x.seqs + lo) : lo;
-                if (s < 0 || s >= c.n_rows) {
-                    kv_error(ATTN_ERR_SHAPE);
-                } else {
-                    const int len = c.lens[s], pos = len - (b - t);
-                    // none of a sequence's rows where it has fewer positions than new tokens
-                    if (static_cast<long long>(b) - a > len || (pos >> c.page_shift) >= c.table_w) {
-                        kv_error(ATTN_ERR_SHAPE);
-                    } else {
-                        const int p = kv_row(c, s)[pos >> c.page_shift];
-                        if (p < 0 || p >= c.n_pages || c.refs[p] != 1)
-                            kv_error(ATTN_ERR_PAGE);  // no page, or one that another sequence shares
-                        else
-                            at = static_cast<long long>(p) * c.Hkv * c.page + (pos & (c.page - 1));
-                    }
-                }
-            }
-        }
-        place[threadIdx.x] = at;
-    }
-    __syncthreads();
+    const int t = static_cast<int>(blockIdx.x) * 8 + static_cast<int>(threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (t >= x.total) return;
     const unsigned row = static_cast<unsigned>(c.Hkv) * c.row16;  // chunks of a token, K or V
-    const unsigned chunks = kAppendTokens * 2u * row;
     const size_t layer16 = static_cast<size_t>(x.layer) * c.n_pages * c.Hkv * c.page * c.row16;
-    for (unsigned i0 = threadIdx.x; i0 < chunks; i0 += 256u * 8u) {
+    long long at = 0;
+    for (unsigned i0 = lane; i0 < 2u * row + lane; i0 += 32u * 8u) {
         uint4 r[8];
-        uint4 *to[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const unsigned i = i0 + 256u * e;
-            to[e] = nullptr;
-            if (i >= chunks) continue;
-            const unsigned tk = i / row, y = i - tk * row;  // (token, K or V), chunk
-            const unsigned t = tk >> 1, head = y / c.row16, ch = y - head * c.row16;
-            const long long at = place[t];
-            if (at < 0) continue;
-            const bool v = tk & 1u;
-            const uint4 *from = v ? x.v + (tok0 + t) * x.v_row + head * x.v_head : x.k + (tok0 + t) * x.k_row + head * x.k_head;
-            r[e] = __ldg(from + ch);
-            to[e] = (v ? c.v : c.k) + layer16 + (at + static_cast<long long>(head) * c.page) * c.row16 + ch;
+            const unsigned i = i0 + 32u * e;
+            if (i >= 2u * row) continue;
+            const bool v = i >= row;
+            const unsigned y = v ? i - row : i, head = y / c.row16, ch = y - head * c.row16;
+            r[e] = __ldg((v ? x.v + t * x.v_row + head * x.v_head : x.k + t * x.k_row + head * x.k_head) + ch);
         }
+        if (i0 == static_cast<unsigned>(lane)) at = append_place(c, x, t);  // the rows are on their way
+        if (at < 0) return;
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (to[e] != nullptr) *to[e] = r[e];
+        for (int e = 0; e < 8; ++e) {
+            const unsigned i = i0 + 32u * e;
+            if (i >= 2u * row) continue;
+            const bool v = i >= row;
+            const unsigned y = v ? i - row : i, head = y / c.row16, ch = y - head * c.row16;
+            (v ? c.v : c.k)[layer16 + (at + static_cast<long long>(head) * c.page) * c.row16 + ch] = r[e];
+        }
     }
 }
 
