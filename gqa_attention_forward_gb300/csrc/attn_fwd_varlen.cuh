@@ -795,67 +795,84 @@ __global__ void __launch_bounds__(kWsThreads, 1)
                 ++scount;
                 tc_fence_after();
                 __syncwarp();
-                uint32_t s[128];
+                float alpha = 1.f;
+                bool rescale = false;
+                float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                const float2 c2 = make_float2(c, c);
+                // takes the tile's max (in m_top) into the reference; what the weights are taken against
+                auto reference = [&]() -> float2 {
+                    if (m_ref == -INFINITY) {
+                        m_ref = m_top;  // nothing seen so far: the accumulator holds zeros at most
+                    } else if ((m_top - m_ref) * c > kRescaleLog2) {
+                        alpha = ex2_approx((m_ref - m_top) * c);
+                        m_ref = m_top;
+                        rescale = true;
+                    }
+                    // a row that has seen no key yet takes its weights, all 0, against 0
+                    const float mr = m_ref == -INFINITY ? 0.f : m_ref;
+                    return make_float2(-mr * c, -mr * c);
+                };
                 if (j < first_masked) {
+                    uint32_t s[128];
                     float mq[4];
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
                         tmem_ld32_max(tS + 32 * q, *reinterpret_cast<uint32_t(*)[32]>(&s[32 * q]), mq[q]);
                     tmem_ld_wait(s, mq);
                     m_top = fmaxf(m_top, fmax3(mq[0], mq[1], fmaxf(mq[2], mq[3])));
+                    const float2 nmc2 = reference();
+#pragma unroll
+                    for (int cc = 0; cc < 128; cc += 2) {
+                        float2 e = ffma2(make_float2(u2f(s[cc]), u2f(s[cc + 1])), c2, nmc2);
+                        e.x = ex2_approx(e.x);
+                        e.y = ex2_approx(e.y);
+                        acc[(cc >> 1) & 1] = fadd2(acc[(cc >> 1) & 1], e);
+                        s[cc] = __float_as_uint(e.x);
+                        s[cc + 1] = __float_as_uint(e.y);
+                    }
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            pk[e] = pack2<kBF16>(u2f(s[32 * q + 2 * e]), u2f(s[32 * q + 2 * e + 1]));
+                        tmem_st16(tS + 16 * q, pk);
+                    }
                 } else {
+                    // A masked tile, once or twice per unit: 32 columns at a time, in two passes over
+                    // TMEM, which is few instructions to fetch each time (P, 16 columns of pairs,
+                    // overwrites scores that have been read).
+                    const int lim = lim0 - j * kBN;  // this row keeps the columns up to lim
+#pragma unroll 1
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t s[32];
+                        tmem_ld32(tS + 32 * q, s);
+                        tmem_ld_wait(s);
+                        float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        tmem_ld32(tS + 32 * q, *reinterpret_cast<uint32_t(*)[32]>(&s[32 * q]));
-                    tmem_ld_wait(s);
-                    const int lim = lim0 - j * kBN;
+                        for (int e = 0; e < 32; ++e)
+                            mx[e & 1] = fmaxf(mx[e & 1], e <= lim - 32 * q ? u2f(s[e]) : -INFINITY);
+                        m_top = fmax3(m_top, mx[0], mx[1]);
+                    }
+                    const float2 nmc2 = reference();
+#pragma unroll 1
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t s[32], pk[16];
+                        tmem_ld32(tS + 32 * q, s);
+                        tmem_ld_wait(s);
 #pragma unroll
-                    for (int cc = 0; cc < 128; ++cc)
-                        if (cc > lim) s[cc] = __float_as_uint(-INFINITY);
-                    float mx[8];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) mx[k] = fmaxf(u2f(s[2 * k]), u2f(s[2 * k + 1]));
-#pragma unroll
-                    for (int cc = 16; cc < 128; cc += 16)
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            mx[k] = fmax3(mx[k], u2f(s[cc + 2 * k]), u2f(s[cc + 2 * k + 1]));
-                    m_top = fmaxf(m_top, fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]),
-                                               fmaxf(mx[6], mx[7])));
-                }
-                float alpha = 1.f;
-                bool rescale = false;
-                if (m_ref == -INFINITY) {
-                    m_ref = m_top;  // nothing seen so far: the accumulator holds zeros at most
-                } else if ((m_top - m_ref) * c > kRescaleLog2) {
-                    alpha = ex2_approx((m_ref - m_top) * c);
-                    m_ref = m_top;
-                    rescale = true;
-                }
-                // a row that has seen no key yet takes its weights, all 0, against 0
-                const float mr = m_ref == -INFINITY ? 0.f : m_ref;
-                const float2 c2 = make_float2(c, c);
-                const float2 nmc2 = make_float2(-mr * c, -mr * c);
-                float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-                for (int cc = 0; cc < 128; cc += 2) {
-                    float2 e = ffma2(make_float2(u2f(s[cc]), u2f(s[cc + 1])), c2, nmc2);
-                    e.x = ex2_approx(e.x);
-                    e.y = ex2_approx(e.y);
-                    acc[(cc >> 1) & 1] = fadd2(acc[(cc >> 1) & 1], e);
-                    s[cc] = __float_as_uint(e.x);
-                    s[cc + 1] = __float_as_uint(e.y);
+                        for (int e = 0; e < 16; ++e) {
+                            float2 x = ffma2(make_float2(u2f(s[2 * e]), u2f(s[2 * e + 1])), c2, nmc2);
+                            x.x = 2 * e <= lim - 32 * q ? ex2_approx(x.x) : 0.f;
+                            x.y = 2 * e + 1 <= lim - 32 * q ? ex2_approx(x.y) : 0.f;
+                            acc[e & 1] = fadd2(acc[e & 1], x);
+                            pk[e] = pack2<kBF16>(x.x, x.y);
+                        }
+                        tmem_st16(tS + 16 * q, pk);
+                    }
                 }
                 const float2 sum2 = fadd2(acc[0], acc[1]);
                 l = l * alpha + (sum2.x + sum2.y);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        pk[e] = pack2<kBF16>(u2f(s[32 * q + 2 * e]), u2f(s[32 * q + 2 * e + 1]));
-                    tmem_st16(tS + 16 * q, pk);
-                }
                 if (__any_sync(0xffffffffu, rescale)) {
                     // O_i holds P_i V_{j-1} already (covered by the S_i(j) commit).
                     __syncwarp();
