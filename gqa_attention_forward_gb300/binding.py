@@ -76,7 +76,7 @@ def load(path: str | None = None):
         lib.attn_fwd_varlen.argtypes = [vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, vp,
                                         ctypes.c_float, i, i, vp]
         lib.attn_fwd_varlen.restype = i
-        lib.attn_fwd_tree_workspace.argtypes = [i, ctypes.POINTER(sz)]
+        lib.attn_fwd_tree_workspace.argtypes = [i, i, ctypes.POINTER(sz)]
         lib.attn_fwd_tree_workspace.restype = i
         lib.attn_fwd_tree.argtypes = [vp, pc, i, vp, vp, vp, vp, vp, i, i, i, vp, ctypes.c_float, vp,
                                       sz, vp]
@@ -407,7 +407,7 @@ def _run(what, dev, stream, entry, *args):
 
 def _new(q, shape, dtype, stream):
     """A new tensor beside q; memory of the current stream that ``stream`` uses is kept until then."""
-    t = q.new_empty(shape, dtype=dtype)
+    t = _torch().empty(shape, dtype=dtype, device=q.device)
     if stream is not None and not isinstance(stream, int):
         t.record_stream(stream)
     return t
@@ -568,10 +568,10 @@ def attn_kv_compact(cache, live, stream=None) -> int:
     return load().attn_kv_compact(_c(cache), _ptr(live), _stream_handle(stream))
 
 
-def attn_fwd_tree_workspace(D):
+def attn_fwd_tree_workspace(n_seqs, D):
     """(status, bytes) of the C entry point with the same name."""
     n = ctypes.c_size_t(0)
-    st = load().attn_fwd_tree_workspace(int(D), ctypes.byref(n))
+    st = load().attn_fwd_tree_workspace(int(n_seqs), int(D), ctypes.byref(n))
     return st, n.value
 
 
@@ -660,7 +660,7 @@ def kv_compact(cache, live=None, stream=None):
     return live
 
 
-_tree_bytes = {}  # (device number, D) -> bytes of attn_fwd_tree_workspace
+_tree_bytes = {}  # (device number, sequences, D) -> bytes of attn_fwd_tree_workspace
 
 
 def attention_tree(q, cache, cu, seqs=None, parents=None, layer: int = 0, scale: float | None = None,
@@ -685,13 +685,13 @@ def attention_tree(q, cache, cu, seqs=None, parents=None, layer: int = 0, scale:
     if so[2] != 1:
         raise ValueError("out must have its last axis contiguous")
     if workspace is None:
-        nbytes = _tree_bytes.get((dev, D))
+        nbytes = _tree_bytes.get((dev, n, D))
         if nbytes is None:
             with torch.cuda.device(dev):
-                st, nbytes = attn_fwd_tree_workspace(D)
+                st, nbytes = attn_fwd_tree_workspace(n, D)
             if st != ATTN_OK:
                 raise AttnError(st, "attn_fwd_tree_workspace")
-            _tree_bytes[dev, D] = nbytes
+            _tree_bytes[dev, n, D] = nbytes
         workspace = _new(q, (nbytes,), torch.uint8, stream)
     else:
         nbytes = workspace.numel()

@@ -47,14 +47,15 @@ namespace gqa {
 constexpr int kTreeThreads = 256;
 constexpr int kTreeSlots = 4;
 constexpr int kTreeMax = 128;      // tokens of one tree
-constexpr int kTreeSeqCache = 512; // sequences whose lengths are kept in shared memory
+constexpr int kTreeSeqs = 2048;    // most sequences of one launch (their lengths lie in shared memory)
 constexpr int kMergeThreads = 32;
 constexpr int kTreeBadTiles = 2;   // the tree's positions lie in at most two key tiles
 
 struct TreeParams : Params {
     const int *cu, *table, *lens, *seqs, *parents;
     const uint8_t *v_ptr;
-    int n_seqs, total_q, Hq, Hkv, n_rows;  // n_rows: rows of the page table
+    int n_seqs, total_q, Hq, Hkv, n_rows;  // n_seqs <= kTreeSeqs; n_rows: rows of the page table
+    int seq0;                  // row of the first sequence where seqs is NULL
     int page, page_shift, n_pages, table_w;
     int rt;                    // tokens per row tile: 128 / group
     int min_share;             // least number of key tiles per CTA
@@ -62,6 +63,7 @@ struct TreeParams : Params {
     float *part_o;             // [2 * CTAs][128][D]
     float *part_lse;           // [2 * CTAs][128]
     int grid;                  // CTAs of the first kernel
+    int *plan;                 // [0]: share, [1 + s]: weights before sequence s
 };
 
 struct TreeUnit {
@@ -94,7 +96,7 @@ struct TreeLayout {
     static constexpr int kUnits = (kAbort + 4 + 15) & ~15;
     static constexpr int kPar = kUnits + kTreeSlots * static_cast<int>(sizeof(TreeUnit));
     static constexpr int kSeqs = (kPar + 2 * kTreeMax * 4 + 15) & ~15;
-    static constexpr int kUsed = kSeqs + kTreeSeqCache * 16;
+    static constexpr int kUsed = kSeqs + kTreeSeqs * 8;
     // more than half of an SM's shared memory: one CTA (all 512 TMEM columns) per SM
     static constexpr int kAlloc = (kUsed + 1024) > 118 * 1024 ? (kUsed + 1024) : 118 * 1024;
 };
@@ -107,7 +109,7 @@ struct TreeSeq {
 };
 __device__ __forceinline__ TreeSeq tree_seq(const TreeParams &p, int s) {
     const VlSpan q = vl_span(p.cu, s, p.total_q);
-    int row = p.seqs != nullptr ? __ldg(p.seqs + s) : s;
+    const int row = p.seqs != nullptr ? __ldg(p.seqs + s) : p.seq0 + s;
     TreeSeq r{q.a, q.b - q.a, 0, row, q.bad};
     if (row < 0 || row >= p.n_rows) {
         r.row = -1;
@@ -203,7 +205,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(smem + L::kTmemSlot);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kAbort);
     TreeUnit *units = reinterpret_cast<TreeUnit *>(smem + L::kUnits);
-    int4 *seqs = reinterpret_cast<int4 *>(smem + L::kSeqs);  // (T, L, q0, row)
+    int2 *seqs = reinterpret_cast<int2 *>(smem + L::kSeqs);  // (T, L)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 64) {
@@ -242,9 +244,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     // lengths) was written before this kernel.
     grid_dependency_wait();
     grid_launch_dependents();
-    for (int s = threadIdx.x; s < p.n_seqs && s < kTreeSeqCache; s += kTreeThreads) {
+    for (int s = threadIdx.x; s < p.n_seqs; s += kTreeThreads) {
         const TreeSeq q = tree_seq(p, s);
-        seqs[s] = make_int4(q.T, q.L, q.q0, q.row);
+        seqs[s] = make_int2(q.T, q.L);
     }
     tc_fence_before();
     __syncthreads();
@@ -253,16 +255,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 
     if (warp == 3) {
         // -------------------------------------------------------- scheduler, and Q
-        auto seq_of = [&](int s) -> int4 {
-            if (s < kTreeSeqCache) return seqs[s];
-            const TreeSeq q = tree_seq(p, s);
-            return make_int4(q.T, q.L, q.q0, q.row);
-        };
-        auto weight_of = [&](int s) -> int {
-            if (s >= p.n_seqs) return 0;
-            const int4 q = seq_of(s);
-            return tree_seq_weight(p, q.x, q.y);
-        };
+        auto weight_of = [&](int s) -> int { return s < p.n_seqs ? tree_seq_weight(p, seqs[s].x, seqs[s].y) : 0; };
         auto scan = [&](int x) {  // inclusive prefix sum over the lanes
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -273,9 +266,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         };
         int total = 0;
         for (int s0 = 0; s0 < p.n_seqs; s0 += 32) {
-            total += __reduce_add_sync(0xffffffffu, weight_of(s0 + lane));
+            const int w = weight_of(s0 + lane);
+            if (blockIdx.x == 0) {
+                const int incl = scan(w);
+                if (s0 + lane < p.n_seqs) p.plan[1 + s0 + lane] = total + incl - w;
+            }
+            total += __reduce_add_sync(0xffffffffu, w);
         }
         const int share = tree_share(p, total);
+        if (blockIdx.x == 0 && lane == 0) p.plan[0] = share;
         // 64-bit: the last CTAs' first tiles may lie past the end
         const long long first = static_cast<long long>(blockIdx.x) * share;
         int at = first < total ? static_cast<int>(first) : total;
@@ -295,9 +294,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 while (at < end && k0 == k1) {
                     int in_seq = 0;
                     for (;; s0 += 32) {
-                        const int w = weight_of(s0 + lane), incl = scan(w);
-                        const int all = __shfl_sync(0xffffffffu, incl, 31);
+                        const int w = weight_of(s0 + lane), all = __reduce_add_sync(0xffffffffu, w);
                         if (at < before + all) {
+                            const int incl = scan(w);
                             const int src = __ffs(__ballot_sync(0xffffffffu, before + incl > at)) - 1;
                             seq = s0 + src;
                             in_seq = at - before - __shfl_sync(0xffffffffu, incl - w, src);
@@ -305,7 +304,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                         }
                         before += all;
                     }
-                    nt = tree_key_tiles(seq_of(seq).y);
+                    nt = tree_key_tiles(seqs[seq].y);
                     const int uw = tree_unit_weight(nt);
                     unit = in_seq / uw;  // kv head * row tiles + row tile
                     // weights [0, uw - nt) of a unit are its change, then come its tiles; a share that
@@ -319,23 +318,23 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 if (!(ok = __all_sync(0xffffffffu, wait_bar(unit_empty(slot), phase ^ 1u, p, abort_flag)))) break;
                 TreeUnit &u = units[slot];
                 if (more) {
-                    const int4 q = seq_of(seq);  // (T, L, q0, row)
-                    const int mt = tree_row_tiles(p, q.x), t0 = (unit % mt) * p.rt;
+                    const TreeSeq q = tree_seq(p, seq);
+                    const int mt = tree_row_tiles(p, q.T), t0 = (unit % mt) * p.rt;
                     if (lane < kTreeBadTiles * 4) u.bad_rows[lane >> 2][lane & 3] = 0;
                     if (lane == 0) {
                         u.valid = 1;
                         u.t0 = t0;
-                        u.q0 = q.z + t0;
-                        u.ntok = q.x - t0 < p.rt ? q.x - t0 : p.rt;
-                        u.T = q.x;
-                        u.L = q.y;
-                        u.base = q.y > q.x ? q.y - q.x : 0;
-                        u.row = q.w;
+                        u.q0 = q.q0 + t0;
+                        u.ntok = q.T - t0 < p.rt ? q.T - t0 : p.rt;
+                        u.T = q.T;
+                        u.L = q.L;
+                        u.base = q.L > q.T ? q.L - q.T : 0;
+                        u.row = q.row;
                         u.kvh = unit / mt;
                         u.k0 = k0;
                         u.k1 = k1;
                         u.piece = (k0 == 0 && k1 == nt) ? -1 : (k0 > 0 ? 0 : 1);
-                        u.first = q.z;
+                        u.first = q.q0;
                         u.bad = 0;
                     }
                     ++emitted;
@@ -861,10 +860,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 // Merges the pieces of the units that were cut: lse = log sum_s exp(lse_s) and
 // O = sum_s exp(lse_s - lse) O_s (the online-softmax update of page "从零开始写Qwen3",
 // deepseek.csdn.net/6a3201f8..., section "在线softmax", across CTAs).  One warp per output
-// row; a row whose unit lay in one share has been written already.  Where a row's pieces lie
-// follows from the offsets and lengths, which are read before the wait for the kernel before,
-// so that after it one round trip brings the log-sum-exps (lane j: piece j) and the rows of
-// the first 8 pieces.
+// row; a row whose unit lay in one share has been written already.  The row's sequence is looked
+// for before the wait for the kernel before; after it come the plan, and then in one round trip
+// the log-sum-exps (lane j: piece j) and the rows of 8 pieces.  (Adding the plan up here before
+// the wait, too, saves 0.3 us of 11 with one sequence and nothing with 16.)
 template <int D, bool kBF16>
 __global__ void __launch_bounds__(kMergeThreads) attn_tree_merge_kernel(const __grid_constant__ TreeParams p) {
     grid_launch_dependents();
@@ -879,23 +878,16 @@ __global__ void __launch_bounds__(kMergeThreads) attn_tree_merge_kernel(const __
         if (__ldg(p.cu + mid) <= tok) lo = mid; else hi = mid;
     }
     const TreeSeq q = tree_seq(p, lo);
-    int total = 0, before = 0;  // weights of all sequences, and of those before this one
-    for (int s0 = 0; s0 < p.n_seqs; s0 += 32) {
-        const int s = s0 + lane;
-        const TreeSeq x = s < p.n_seqs ? tree_seq(p, s) : TreeSeq{0, 0, 0, 0, false};
-        const int w = s < p.n_seqs ? tree_seq_weight(p, x.T, x.L) : 0;
-        total += __reduce_add_sync(0xffffffffu, w);
-        before += __reduce_add_sync(0xffffffffu, s < lo ? w : 0);
-    }
-    const int share = tree_share(p, total);
     const int nt = tree_key_tiles(q.L), mt = tree_row_tiles(p, q.T), uw = tree_unit_weight(nt);
     const int t = tok - q.q0, m = t / p.rt;
     const int prow = (t - m * p.rt) * p.group + head % p.group;  // row within the tile
+    grid_dependency_wait();
+    if (!in || t < 0 || t >= q.T) return;
+    const int share = p.plan[0], before = p.plan[1 + lo];
     // the weight past the unit's last tile, and the CTAs of its first and last one
     const int end = before + ((head / p.group) * mt + m + 1) * uw;
     const int c0 = (end - nt) / share, c1 = (end - 1) / share;
-    grid_dependency_wait();
-    if (!in || t < 0 || t >= q.T || c0 == c1) return;
+    if (c0 == c1) return;
     constexpr int kPer = D / 32;
     // where the kernel before gave up on a wait, its pieces may be stale: NaN
     const bool gave_up = *reinterpret_cast<volatile unsigned int *>(&g_abort_seq) == p.seq;

@@ -54,13 +54,13 @@
 namespace gqa {
 
 constexpr int kVlSlots = 4;       // unit descriptors in flight
-constexpr int kVlSeqCache = 2048; // sequences whose block counts are kept in shared memory
+constexpr int kVlSeqs = 2048;     // most sequences of one launch (their block counts lie in shared memory)
 constexpr int kVlBadTiles = 4;    // key tiles of a unit that the guard may look at
 
 struct VarlenParams : Params {
     const int *cu_q, *cu_k;  // device [n_seqs + 1]
     const uint8_t *v_ptr;    // V in global memory (the rare non-finite rows are read again)
-    int n_seqs, total_q, total_k;
+    int n_seqs, total_q, total_k;  // n_seqs <= kVlSeqs
     int pair;                // 1: the tiles are two heads of a group; 0: two row tiles of a head
     int block_rows;          // query rows of a unit: 128 (pair) or 256
     int head_units;          // units per block of rows: Hq / 2 (pair) or Hq
@@ -96,7 +96,7 @@ struct VlLayout {
     static constexpr int kAbort = kTmemSlot + 4;
     static constexpr int kUnits = (kAbort + 4 + 15) & ~15;
     static constexpr int kSeqs = kUnits + kVlSlots * static_cast<int>(sizeof(VlUnit));
-    static constexpr int kUsed = kSeqs + kVlSeqCache * 4;
+    static constexpr int kUsed = kSeqs + kVlSeqs * 4;
     static constexpr int kAlloc = (kUsed + 1024) > 118 * 1024 ? (kUsed + 1024) : 118 * 1024;
 };
 static_assert(VlLayout<128>::kAlloc <= 227 * 1024, "shared memory of one CTA");
@@ -151,14 +151,11 @@ __device__ __forceinline__ uint32_t vl_blocks(const VarlenParams &p, int s) {
 template <bool kCausal>
 struct VlWalk {
     const VarlenParams &p;
-    const uint32_t *cache;
+    const uint32_t *blocks;  // vl_blocks of every sequence
     int lane;
     int level = INT_MAX;  // current level; blocks [base, base + count) lie on it
     int base = 0, count = 0;
 
-    __device__ __forceinline__ uint32_t info(int s) const {
-        return s < kVlSeqCache ? cache[s] : vl_blocks(p, s);
-    }
     // blocks of a sequence on a level
     __device__ __forceinline__ int on_level(uint32_t x, int lev) const {
         const int nqb = static_cast<int>(x >> 16), H = static_cast<int>(x & 0xFFFFu);
@@ -168,7 +165,7 @@ struct VlWalk {
     __device__ __forceinline__ bool next_level() {
         int best = INT_MIN;
         for (int s = lane; s < p.n_seqs; s += 32) {
-            const uint32_t x = info(s);
+            const uint32_t x = blocks[s];
             const int nqb = static_cast<int>(x >> 16), H = static_cast<int>(x & 0xFFFFu);
             if (nqb == 0) continue;
             const int cand = H < level ? H : level - 1;
@@ -179,7 +176,7 @@ struct VlWalk {
         base += count;
         level = best;
         int n = 0;
-        for (int s = lane; s < p.n_seqs; s += 32) n += on_level(info(s), level);
+        for (int s = lane; s < p.n_seqs; s += 32) n += on_level(blocks[s], level);
         count = __reduce_add_sync(0xffffffffu, n);
         return true;
     }
@@ -190,7 +187,7 @@ struct VlWalk {
         int r = b - base;
         for (int s0 = 0; s0 < p.n_seqs; s0 += 32) {
             const int s = s0 + lane;
-            const uint32_t x = s < p.n_seqs ? info(s) : 0u;
+            const uint32_t x = s < p.n_seqs ? blocks[s] : 0u;
             const int c = s < p.n_seqs ? on_level(x, level) : 0;
             int incl = c;  // blocks of sequences up to this lane
 #pragma unroll
@@ -421,7 +418,7 @@ __global__ void __launch_bounds__(kWsThreads, 1)
     }
     // the set-up above overlaps the kernel before this one; its results are read from here on
     grid_dependency_wait();
-    for (int s = threadIdx.x; s < p.n_seqs && s < kVlSeqCache; s += kWsThreads) seqs[s] = vl_blocks(p, s);
+    for (int s = threadIdx.x; s < p.n_seqs; s += kWsThreads) seqs[s] = vl_blocks(p, s);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();

@@ -228,10 +228,7 @@ attn_status_t attn_fwd_varlen(const void *q, const void *k, const void *v, void 
     int dev = 0;
     if (attn_status_t e = check_device(&dev); e != ATTN_OK) return e;
     common_params(prm, o, lse, Hq, Hkv, scale);
-    prm.cu_q = cu_q;
-    prm.cu_k = cu_k ? cu_k : cu_q;
     prm.v_ptr = static_cast<const uint8_t *>(v);
-    prm.n_seqs = n_seqs;
     prm.total_q = total_q;
     prm.total_k = total_k;
     prm.v_row = st[4] * 2;
@@ -251,26 +248,38 @@ attn_status_t attn_fwd_varlen(const void *q, const void *k, const void *v, void 
     const unsigned grid = static_cast<unsigned>(units < g_dev_sms[dev] ? units : g_dev_sms[dev]);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int kid = (D == 128 ? 4 : 0) + (bf16 ? 2 : 0) + (causal ? 1 : 0);
-    switch (kid) {
-        case 0: return launch_varlen<64, false, false>(dev, kid, tq, tk, tv, prm, grid, s);
-        case 1: return launch_varlen<64, false, true>(dev, kid, tq, tk, tv, prm, grid, s);
-        case 2: return launch_varlen<64, true, false>(dev, kid, tq, tk, tv, prm, grid, s);
-        case 3: return launch_varlen<64, true, true>(dev, kid, tq, tk, tv, prm, grid, s);
-        case 4: return launch_varlen<128, false, false>(dev, kid, tq, tk, tv, prm, grid, s);
-        case 5: return launch_varlen<128, false, true>(dev, kid, tq, tk, tv, prm, grid, s);
-        case 6: return launch_varlen<128, true, false>(dev, kid, tq, tk, tv, prm, grid, s);
-        default: return launch_varlen<128, true, true>(dev, kid, tq, tk, tv, prm, grid, s);
+    auto launch = [&]() {
+        switch (kid) {
+            case 0: return launch_varlen<64, false, false>(dev, kid, tq, tk, tv, prm, grid, s);
+            case 1: return launch_varlen<64, false, true>(dev, kid, tq, tk, tv, prm, grid, s);
+            case 2: return launch_varlen<64, true, false>(dev, kid, tq, tk, tv, prm, grid, s);
+            case 3: return launch_varlen<64, true, true>(dev, kid, tq, tk, tv, prm, grid, s);
+            case 4: return launch_varlen<128, false, false>(dev, kid, tq, tk, tv, prm, grid, s);
+            case 5: return launch_varlen<128, false, true>(dev, kid, tq, tk, tv, prm, grid, s);
+            case 6: return launch_varlen<128, true, false>(dev, kid, tq, tk, tv, prm, grid, s);
+            default: return launch_varlen<128, true, true>(dev, kid, tq, tk, tv, prm, grid, s);
+        }
+    };
+    // at most kVlSeqs sequences per launch; a launch leaves the rows of the others alone
+    for (int s0 = 0; s0 < n_seqs; s0 += gqa::kVlSeqs) {
+        prm.cu_q = cu_q + s0;
+        prm.cu_k = (cu_k ? cu_k : cu_q) + s0;
+        prm.n_seqs = n_seqs - s0 < gqa::kVlSeqs ? n_seqs - s0 : gqa::kVlSeqs;
+        if (attn_status_t e = launch(); e != ATTN_OK) return e;
     }
+    return ATTN_OK;
 }
 
-attn_status_t attn_fwd_tree_workspace(int D, size_t *bytes) {
+attn_status_t attn_fwd_tree_workspace(int n_seqs, int D, size_t *bytes) {
     if (bytes == nullptr) return ATTN_ERR_NULL;
     *bytes = 0;
+    if (n_seqs < 0) return ATTN_ERR_SHAPE;
     if (D != 64 && D != 128) return ATTN_ERR_HEADDIM;
     int dev = 0;
     if (attn_status_t st = check_device(&dev); st != ATTN_OK) return st;
     const size_t rows = static_cast<size_t>(g_dev_sms[dev]) * 2 * gqa::kBM;
-    *bytes = rows * (D + 1) * sizeof(float);
+    const int launch_seqs = n_seqs < gqa::kTreeSeqs ? n_seqs : gqa::kTreeSeqs;
+    *bytes = rows * (D + 1) * sizeof(float) + (static_cast<size_t>(launch_seqs) + 1) * sizeof(int);
     return ATTN_OK;
 }
 
@@ -298,23 +307,20 @@ attn_status_t attn_fwd_tree(const void *q, const attn_kv_cache_t *cache, int lay
     prm.rt = 128 / (Hq / Hkv);
     const long long row_tiles = static_cast<long long>(total_q) / prm.rt + n_seqs;
     const long long key_tiles = (static_cast<long long>(cache->table_width) * cache->page + 127) / 128;
-    if (row_tiles * Hkv > INT_MAX / 2 / (key_tiles + 1) || static_cast<long long>(total_q) * Hq > INT_MAX) return ATTN_ERR_SHAPE;
+    if (row_tiles * Hkv > INT_MAX / 2 / (key_tiles + 2) || static_cast<long long>(total_q) * Hq > INT_MAX) return ATTN_ERR_SHAPE;
     int dev = 0;
     if (attn_status_t e = check_device(&dev); e != ATTN_OK) return e;
     size_t need = 0;
-    if (attn_status_t e = attn_fwd_tree_workspace(D, &need); e != ATTN_OK) return e;
+    if (attn_status_t e = attn_fwd_tree_workspace(n_seqs, D, &need); e != ATTN_OK) return e;
     if (workspace_bytes < need) return ATTN_ERR_SCRATCH;
     common_params(prm, o, lse, Hq, Hkv, scale);
     const size_t layer_bytes = static_cast<size_t>(cache->n_pages) * Hkv * cache->page * D * 2;
     const uint8_t *kp = static_cast<const uint8_t *>(cache->k) + layer * layer_bytes;
     const uint8_t *vp = static_cast<const uint8_t *>(cache->v) + layer * layer_bytes;
-    prm.cu = cu;
     prm.table = cache->table;
     prm.lens = cache->lens;
-    prm.seqs = seqs;
     prm.parents = parents;
     prm.v_ptr = vp;
-    prm.n_seqs = n_seqs;
     prm.total_q = total_q;
     prm.Hq = Hq;
     prm.Hkv = Hkv;
@@ -329,6 +335,7 @@ attn_status_t attn_fwd_tree(const void *q, const attn_kv_cache_t *cache, int lay
     const int sms = g_dev_sms[dev];
     prm.part_o = static_cast<float *>(workspace);
     prm.part_lse = prm.part_o + static_cast<size_t>(sms) * 2 * gqa::kBM * D;
+    prm.plan = reinterpret_cast<int *>(prm.part_lse + static_cast<size_t>(sms) * 2 * gqa::kBM);
     const bool bf16 = cache->dtype == ATTN_BF16;
     CUtensorMap tq, tk, tv;
     int head_y = 0;
@@ -336,17 +343,28 @@ attn_status_t attn_fwd_tree(const void *q, const attn_kv_cache_t *cache, int lay
     if (!encode_packed_map(&tq, q, bf16, D, total_q, Hq, st[0], st[1], prm.rt, prm.group, &head_y) || head_y != 1 ||
         !encode_pool_map(&tk, kp, bf16, D, cache->page, slices) || !encode_pool_map(&tv, vp, bf16, D, cache->page, slices))
         return no_map();
-    const long long most = row_tiles * Hkv * (key_tiles + 1);
+    const long long most = row_tiles * Hkv * (key_tiles + 2);
     const unsigned grid = static_cast<unsigned>(most < sms ? most : sms);
     prm.grid = static_cast<int>(grid);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int kid = (D == 128 ? 2 : 0) + (bf16 ? 1 : 0);
-    switch (kid) {
-        case 0: return launch_tree<64, false>(dev, kid, tq, tk, tv, prm, grid, s);
-        case 1: return launch_tree<64, true>(dev, kid, tq, tk, tv, prm, grid, s);
-        case 2: return launch_tree<128, false>(dev, kid, tq, tk, tv, prm, grid, s);
-        default: return launch_tree<128, true>(dev, kid, tq, tk, tv, prm, grid, s);
+    auto launch = [&]() {
+        switch (kid) {
+            case 0: return launch_tree<64, false>(dev, kid, tq, tk, tv, prm, grid, s);
+            case 1: return launch_tree<64, true>(dev, kid, tq, tk, tv, prm, grid, s);
+            case 2: return launch_tree<128, false>(dev, kid, tq, tk, tv, prm, grid, s);
+            default: return launch_tree<128, true>(dev, kid, tq, tk, tv, prm, grid, s);
+        }
+    };
+    // at most kTreeSeqs sequences per launch; a launch leaves the tokens of the others alone
+    for (int s0 = 0; s0 < n_seqs; s0 += gqa::kTreeSeqs) {
+        prm.cu = cu + s0;
+        prm.seqs = seqs != nullptr ? seqs + s0 : nullptr;
+        prm.seq0 = s0;
+        prm.n_seqs = n_seqs - s0 < gqa::kTreeSeqs ? n_seqs - s0 : gqa::kTreeSeqs;
+        if (attn_status_t e = launch(); e != ATTN_OK) return e;
     }
+    return ATTN_OK;
 }
 
 attn_status_t attn_kv_scratch(int n_pages, int n_rows, size_t *bytes) {

@@ -273,6 +273,8 @@ __global__ void __launch_bounds__(kPlanThreads) kv_compact_kernel(const KvPool c
     const int half = c.n_pages >> 1;  // holes, and movers, are at most half of the pages
     const int m = kv_list<true>(c.refs, 0, live, half, c.list, sm);
     kv_list<false>(c.refs, live, c.n_pages, half, movers, sm);
+    // an entry that names a free page, which no table should, stays what it is
+    for (int p = live + static_cast<int>(threadIdx.x); p < c.n_pages; p += kPlanThreads) c.map[p] = p;
     __syncthreads();
     for (int k = threadIdx.x; k < m; k += kPlanThreads) {
         const int from = movers[k], to = c.list[k];

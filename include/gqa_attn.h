@@ -255,7 +255,7 @@ attn_status_t attn_fwd_host(const void *q_h, const void *k_h, const void *v_h, v
 
 /*
  * attn_fwd_varlen -- attention over packed sequences of different lengths (the
- * prompts of a batch, without padding), one kernel launch.
+ * prompts of a batch, without padding).
  *
  * Sequence s owns query rows [cu_q[s], cu_q[s+1]) of q, o and lse and rows
  * [cu_k[s], cu_k[s+1]) of k and v.  Each of its rows attends over its keys
@@ -281,7 +281,7 @@ attn_status_t attn_fwd_host(const void *q_h, const void *k_h, const void *v_h, v
  * Errors: as attn_fwd_kv (no error for Nq_s > Nk_s); ATTN_ERR_SHAPE for strides.
  *         Offsets that descend or leave the tensors are clamped, and
  *         attn_last_device_error reports ATTN_ERR_SHAPE.
- * Graphs, streams and ownership: as attn_fwd; no workspace.
+ * Graphs, streams and ownership: as attn_fwd, one launch per 2048 sequences; no workspace.
  */
 attn_status_t attn_fwd_varlen(const void *q, const void *k, const void *v, void *o, float *lse,
                               const int *cu_q, const int *cu_k, int n_seqs, int total_q,
@@ -394,7 +394,7 @@ attn_status_t attn_kv_compact(const attn_kv_cache_t *cache, int *live, void *str
  * the sequence's positions and bad offsets or sequences (ATTN_ERR_SHAPE), whose rows are then
  * undefined, and missing pages (ATTN_ERR_PAGE), which read as zeros.
  */
-attn_status_t attn_fwd_tree_workspace(int D, size_t *bytes);
+attn_status_t attn_fwd_tree_workspace(int n_seqs, int D, size_t *bytes);
 attn_status_t attn_fwd_tree(const void *q, const attn_kv_cache_t *cache, int layer, void *o,
                             float *lse, const int *cu, const int *seqs, const int *parents,
                             int n_seqs, int total_q, int Hq, const long long *strides,

@@ -163,9 +163,10 @@ def test_size_queries():
     st, n = binding.attn_kv_scratch(10, 4)
     assert st == OK and n >= 4 * (2 * 10 + 5 * 4)
     assert binding.attn_kv_scratch(0, 4) == (SHAPE, 0)
-    assert binding.attn_fwd_tree_workspace(80) == (HEADDIM, 0)
+    assert binding.attn_fwd_tree_workspace(-1, 128) == (SHAPE, 0)
+    assert binding.attn_fwd_tree_workspace(3, 80) == (HEADDIM, 0)
     assert binding.load().attn_kv_scratch(1, 1, None) == NULL
-    assert binding.load().attn_fwd_tree_workspace(64, None) == NULL
+    assert binding.load().attn_fwd_tree_workspace(1, 64, None) == NULL
     assert ctypes.sizeof(binding.KVCache) == 6 * 8 + 8 * 4
 
 

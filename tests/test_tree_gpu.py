@@ -75,6 +75,7 @@ CASES = [
     ([1500, 900], [5, 4], 3, 3, 128, "bf16", 1024),
     ([30 + 17 * i for i in range(70)], [1 + i % 4 for i in range(70)], 2, 1, 64, "bf16", 16),
     ([(7 * i) % 50 for i in range(700)], [1] * 700, 2, 2, 64, "f16", 16),
+    ([(7 * i) % 20 for i in range(2300)], [1 + (i % 7 == 0) for i in range(2300)], 2, 1, 64, "f16", 16),
 ]
 
 
@@ -228,7 +229,7 @@ def test_captured_call_replays_on_new_lengths_trees_and_pages():
     p = i32([x for t in trees(T, 0) for x in t])
     cu = offsets(T)
     o, lse = torch.zeros_like(q), torch.zeros((8, 18), device="cuda")
-    n = binding.attn_fwd_tree_workspace(128)[1]
+    n = binding.attn_fwd_tree_workspace(3, 128)[1]
     ws = torch.empty(n, dtype=torch.uint8, device="cuda")
     binding.attention_tree(q, cache, cu, parents=p, out=o, lse_out=lse, workspace=ws)
     torch.cuda.synchronize()
