@@ -840,28 +840,50 @@ __global__ void __launch_bounds__(kWsThreads, 1)
                     // TMEM, which is few instructions to fetch each time (P, 16 columns of pairs,
                     // overwrites scores that have been read).
                     const int lim = lim0 - j * kBN;  // this row keeps the columns up to lim
+                    // Of columns 32 q .. every row of the warp sees all for q < q_all and none for
+                    // q >= q_none: on a causal diagonal all but one of the four steps need no selects.
+                    const int lo = __reduce_min_sync(0xffffffffu, lim), hi = __reduce_max_sync(0xffffffffu, lim);
+                    const int q_all = lo < 31 ? 0 : (lo + 1) >> 5, q_none = hi < 0 ? 0 : (hi >> 5) + 1;
 #pragma unroll 1
-                    for (int q = 0; q < 4; ++q) {
+                    for (int q = 0; q < 4 && q < q_none; ++q) {
                         uint32_t s[32];
-                        tmem_ld32(tS + 32 * q, s);
-                        tmem_ld_wait(s);
-                        float mx[2] = {-INFINITY, -INFINITY};
+                        if (q < q_all) {
+                            float mq[1];
+                            tmem_ld32_max(tS + 32 * q, s, mq[0]);
+                            tmem_ld_wait(s, mq);
+                            m_top = fmaxf(m_top, mq[0]);
+                        } else {
+                            tmem_ld32(tS + 32 * q, s);
+                            tmem_ld_wait(s);
+                            float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            mx[e & 1] = fmaxf(mx[e & 1], e <= lim - 32 * q ? u2f(s[e]) : -INFINITY);
-                        m_top = fmax3(m_top, mx[0], mx[1]);
+                            for (int e = 0; e < 32; ++e)
+                                mx[e & 1] = fmaxf(mx[e & 1], e <= lim - 32 * q ? u2f(s[e]) : -INFINITY);
+                            m_top = fmax3(m_top, mx[0], mx[1]);
+                        }
                     }
                     const float2 nmc2 = reference();
 #pragma unroll 1
                     for (int q = 0; q < 4; ++q) {
                         uint32_t s[32], pk[16];
+                        if (q >= q_none) {
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) pk[e] = 0u;
+                            tmem_st16(tS + 16 * q, pk);
+                            continue;
+                        }
                         tmem_ld32(tS + 32 * q, s);
                         tmem_ld_wait(s);
+                        if (q >= q_all) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (e > lim - 32 * q) s[e] = __float_as_uint(-INFINITY);
+                        }
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
                             float2 x = ffma2(make_float2(u2f(s[2 * e]), u2f(s[2 * e + 1])), c2, nmc2);
-                            x.x = 2 * e <= lim - 32 * q ? ex2_approx(x.x) : 0.f;
-                            x.y = 2 * e + 1 <= lim - 32 * q ? ex2_approx(x.y) : 0.f;
+                            x.x = ex2_approx(x.x);
+                            x.y = ex2_approx(x.y);
                             acc[e & 1] = fadd2(acc[e & 1], x);
                             pk[e] = pack2<kBF16>(x.x, x.y);
                         }
