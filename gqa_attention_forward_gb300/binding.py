@@ -395,6 +395,8 @@ def _same(t, name, dtype, dev):
 def _run(what, dev, stream, entry, *args):
     """entry(*args, stream handle) with device ``dev`` current; raises AttnError unless it succeeds."""
     torch = _torch()
+    if dev < 0:
+        raise ValueError(f"{what}: the tensors must be on a CUDA device")
     handle = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream_handle(stream)
     if torch._C._cuda_getDevice() == dev:
         st = entry(*args, handle)
@@ -406,10 +408,16 @@ def _run(what, dev, stream, entry, *args):
 
 
 def _new(q, shape, dtype, stream):
-    """A new tensor beside q; memory of the current stream that ``stream`` uses is kept until then."""
-    t = _torch().empty(shape, dtype=dtype, device=q.device)
-    if stream is not None and not isinstance(stream, int):
-        t.record_stream(stream)
+    """A new tensor beside q, in memory of ``stream`` (None: the current one), which nothing
+    earlier still uses there; it is kept, too, for what the current stream does with it."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=q.device)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=q.device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=q.device)
+    t.record_stream(torch.cuda.current_stream(q.device))
     return t
 
 

@@ -887,7 +887,8 @@ __global__ void __launch_bounds__(kMergeThreads) attn_tree_merge_kernel(const __
     // the weight past the unit's last tile, and the CTAs of its first and last one
     const int end = before + ((head / p.group) * mt + m + 1) * uw;
     const int c0 = (end - nt) / share, c1 = (end - 1) / share;
-    if (c0 == c1) return;
+    // (lengths that changed since the kernel before, against the rules, must not lead outside)
+    if (c0 >= c1 || c0 < 0 || c1 >= p.grid) return;
     constexpr int kPer = D / 32;
     // where the kernel before gave up on a wait, its pieces may be stale: NaN
     const bool gave_up = *reinterpret_cast<volatile unsigned int *>(&g_abort_seq) == p.seq;

@@ -404,8 +404,9 @@ __device__ __forceinline__ long long append_place(const KvPool &c, const KvAppen
         return -1;
     }
     const int len = c.lens[s], pos = len - (b - t);
-    // none of a sequence's rows where it has fewer positions than new tokens
-    if (static_cast<long long>(b) - a > len || (pos >> c.page_shift) >= c.table_w) {
+    // none of a sequence's rows where it has fewer positions than new tokens, or where its
+    // offsets leave the new rows
+    if (a < 0 || b > x.total || static_cast<long long>(b) - a > len || (pos >> c.page_shift) >= c.table_w) {
         kv_error(ATTN_ERR_SHAPE);
         return -1;
     }

@@ -220,6 +220,9 @@ def test_python_calls_check_their_tensors():
         lambda: binding.attention_tree(q.half(), c, cu),
         lambda: binding.attention_tree(q, c, cu, parents=lens),
         lambda: binding.attention_tree(q, c, cu, seqs=lens),
+        lambda: binding.kv_extend(c, lens),  # everything fits, but nothing is on a GPU
+        lambda: binding.kv_append(c, k, k, cu),
+        lambda: binding.attention_varlen(q, k, k, cu),
     ):
         with pytest.raises(ValueError):
             bad()

@@ -158,6 +158,8 @@ BAD = [
     ("copy", binding.ATTN_ERR_PAGE, lambda c: binding.kv_copy(c, i32([-2]), i32([0]))),
     ("append", binding.ATTN_ERR_SHAPE, lambda c: binding.kv_append(c, *new(c, 500), i32([0, 500]), i32([0]))),
     ("append", binding.ATTN_ERR_SHAPE, lambda c: binding.kv_append(c, *new(c, 2), i32([0, 2]), i32([-1]))),
+    ("append", binding.ATTN_ERR_SHAPE, lambda c: binding.kv_append(c, *new(c, 2), i32([0, 5]), i32([0]))),
+    ("append", binding.ATTN_ERR_SHAPE, lambda c: binding.kv_append(c, *new(c, 2), i32([-3, 2]), i32([0]))),
     ("accept", binding.ATTN_ERR_SHAPE, lambda c: binding.kv_accept(c, i32([0, 4]), i32([[1, 1]]), i32([2]))),
     ("accept", binding.ATTN_ERR_SHAPE, lambda c: binding.kv_accept(c, i32([0, 4]), i32([[1, 4]]), i32([2]))),
     ("accept", binding.ATTN_ERR_SHAPE, lambda c: binding.kv_accept(c, i32([0, 4]), i32([[1]]), i32([2]))),

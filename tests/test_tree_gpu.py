@@ -264,6 +264,61 @@ def test_another_stream_and_same_bits():
     assert torch.equal(o1, o2) and torch.equal(l1, l2)
 
 
+def test_calls_at_once_on_two_streams():
+    """Tree and packed calls on two streams over one cache, each with outputs (and a workspace) of
+    its own: the bits of the calls one after another."""
+    cache = build([9000, 300, 4000], 64, 2, 128, "bf16", seed=27)
+    par = trees([20, 3, 9], 6)
+    p = i32([x for t in par for x in t])
+    cu, lens = offsets([20, 3, 9]), offsets([700, 40, 300])
+    qs = [queries(32, 8, 128, "bf16", 28 + i) for i in range(2)]
+    x = [queries(1040, 8, 128, "bf16", 38 + i) for i in range(2)]
+    want = [binding.attention_tree(q, cache, cu, parents=p) for q in qs]
+    packed = [binding.attention_varlen(y, y[:, :2], y[:, 2:4], lens) for y in x]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            got[i].append(binding.attention_tree(qs[i], cache, cu, parents=p, stream=s) +
+                          binding.attention_varlen(x[i], x[i][:, :2], x[i][:, 2:4], lens,
+                                                   stream=s.cuda_stream if i else s))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for o, l, po, pl in got[i]:
+            assert torch.equal(o, want[i][0]) and torch.equal(l, want[i][1])
+            assert torch.equal(po, packed[i][0]) and torch.equal(pl, packed[i][1])
+    assert status() == binding.ATTN_OK
+
+
+def test_two_captured_steps_replayed_at_once():
+    """Two graphs over one cache, captured with workspaces of their own and replayed on two streams."""
+    cache = build([5000, 900], 32, 2, 128, "bf16", seed=29)
+    q = [queries(9, 8, 128, "bf16", 30 + i) for i in range(2)]
+    cu = offsets([8, 1])
+    want = [binding.attention_tree(x, cache, cu) for x in q]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for x in q:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(binding.attention_tree(x, cache, cu))
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(4):
+        for o, l in outs:
+            o.zero_()
+            l.zero_()
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for (o, l), (wo, wl) in zip(outs, want):
+            assert torch.equal(o, wo) and torch.equal(l, wl)
+    assert status() == binding.ATTN_OK
+
+
 def test_cache_past_32_bits():
     """A sequence whose pages lie past 2^31 elements of the pool."""
     page, Hkv, D = 128, 8, 128
