@@ -388,7 +388,7 @@ struct KvAppend {
     const int *cu, *seqs;
     int n, total, layer;
 };
-// Where token t's rows go: page * Hkv * page rows + row within the page, or -1 (behind the last
+// Where token t's rows go (one warp): page * Hkv * page rows + row within the page, or -1 (behind the last
 // sequence, or refused).
 __device__ __forceinline__ long long append_place(const KvPool &c, const KvAppend &x, int t) {
     int lo = 0, hi = x.n;
@@ -399,7 +399,12 @@ __device__ __forceinline__ long long append_place(const KvPool &c, const KvAppen
     const int a = __ldg(x.cu + lo), b = __ldg(x.cu + lo + 1);
     if (t < a || t >= b) return -1;
     const int s = x.seqs != nullptr ? __ldg(x.seqs + lo) : lo;
-    if (s < 0 || s >= c.n_rows) {
+    bool again = false;  // named before in the list
+    if (x.seqs != nullptr) {
+        for (int j = threadIdx.x & 31; j < lo; j += 32) again |= __ldg(x.seqs + j) == s;
+        again = __any_sync(0xffffffffu, again);
+    }
+    if (s < 0 || s >= c.n_rows || again) {
         kv_error(ATTN_ERR_SHAPE);
         return -1;
     }
@@ -469,9 +474,13 @@ __global__ void __cluster_dims__(kAcceptCtas, 1, 1) __launch_bounds__(256)
         moves = 0;
         bad = 0;
     }
-    __syncthreads();
+    // a sequence named before in the list is refused: its length may be changing by now
+    int again = 0;
+    if (seqs != nullptr)
+        for (int j = threadIdx.x; j < i; j += 256) again |= seqs[j] == s ? 1 : 0;
+    again = __syncthreads_or(again);
     int base = 0;
-    bool fine = s >= 0 && s < c.n_rows && T >= 0 && T <= kAcceptMost && m >= 0 && m <= T && m <= path_w;
+    bool fine = again == 0 && s >= 0 && s < c.n_rows && T >= 0 && T <= kAcceptMost && m >= 0 && m <= T && m <= path_w;
     if (fine) {
         base = c.lens[s] - T;
         fine = base >= 0 && ((base + T + c.page - 1) >> c.page_shift) <= c.table_w;

@@ -197,6 +197,40 @@ def test_the_same_sequence_twice():
     assert status() == binding.ATTN_ERR_SHAPE
 
 
+def test_the_same_sequence_twice_in_append_accept_and_free():
+    """The first entry of a list stands; the others are refused (or, freeing, do nothing more)."""
+    c = build([40, 33], 16, 2, 64, "f16", n_rows=6)
+    x = torch.randn(9, 2, 64, device="cuda").to(DT["f16"])
+    m = Model(c)
+    seqs, cu = [0, 1, 0, 1], [0, 3, 5, 8, 9]
+    binding.kv_append(c, x, x, i32(cu), i32(seqs))
+    m.append(0, seqs[:2], x, x, [3, 2])
+    assert status() == binding.ATTN_ERR_SHAPE
+    m.same(c)
+    path = [[1, 2, 3], [0, 2, 3], [0, 1, 2], [2, 3, 3]]
+    cu = [0, 5, 9, 14, 18]
+    binding.kv_accept(c, i32(cu), i32(path), i32([3, 3, 3, 2]), i32(seqs))
+    m.accept(seqs[:2], [5, 4], path[:2])
+    assert status() == binding.ATTN_ERR_SHAPE
+    m.same(c)
+    binding.kv_free(c, i32([1, 0, 1]))
+    m.free([1, 0])
+    assert status() == binding.ATTN_OK
+    m.same(c)
+
+
+def test_one_token_of_any_row_stride():
+    """The row stride of a single token, and the head stride of a single head, are not looked at."""
+    c = build([33], 16, 1, 64, "f16", n_rows=2)
+    m = Model(c)
+    x = torch.randn(64, device="cuda").to(DT["f16"])
+    one = x.as_strided((1, 1, 64), (3, 5, 1))
+    binding.kv_append(c, one, one, i32([0, 1]), i32([0]))
+    m.append(0, [0], one, one, [1])
+    assert status() == binding.ATTN_OK
+    m.same(c)
+
+
 def test_shared_and_missing_pages_are_not_written():
     page = 16
     c = build([2 * page, 5], page, 1, 64, "f16", 1, n_rows=6)
