@@ -413,8 +413,9 @@ def _new(q, shape, dtype, stream):
     torch = _torch()
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=q.device)
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=q.device)
+    if isinstance(stream, int):  # 0 to 2: the default stream's handles
+        stream = (torch.cuda.default_stream(q.device) if stream < 3
+                  else torch.cuda.ExternalStream(stream, device=q.device))
     with torch.cuda.stream(stream):
         t = torch.empty(shape, dtype=dtype, device=q.device)
     t.record_stream(torch.cuda.current_stream(q.device))

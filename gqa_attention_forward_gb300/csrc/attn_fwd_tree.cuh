@@ -45,7 +45,7 @@
 namespace gqa {
 
 constexpr int kTreeThreads = 256;
-constexpr int kTreeSlots = 8;  // unit descriptors in flight (256 sequences of 1000: 189 us with 4, 177 with 8)
+constexpr int kTreeSlots = 8;      // unit descriptors in flight (256 sequences of 1000: 189 us with 4, 177 with 8)
 constexpr int kTreeMax = 128;      // tokens of one tree
 constexpr int kTreeSeqs = 2048;    // most sequences of one launch (their lengths lie in shared memory)
 constexpr int kMergeThreads = 32;
@@ -58,7 +58,7 @@ struct TreeParams : Params {
     int seq0;                  // row of the first sequence where seqs is NULL
     int page, page_shift, n_pages, table_w;
     int rt;                    // tokens per row tile: 128 / group
-    int min_share;             // least number of key tiles per CTA
+    int min_share;             // least weight of a CTA's share
     long long o_row, o_head;   // strides in bytes
     float *part_o;             // [2 * CTAs][128][D]
     float *part_lse;           // [2 * CTAs][128]
@@ -120,7 +120,9 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeParams &p, int s) {
     const long long cap = static_cast<long long>(p.table_w) << p.page_shift;
     if (r.L < 0) r.L = 0, r.bad = true;
     if (r.L > cap) r.L = static_cast<int>(cap), r.bad = true;
-    if (r.T > kTreeMax || r.T > r.L) r.bad |= r.T > 0;
+    // (a tree that is too long is cut, so that no offsets make the sum of the weights pass 32 bits)
+    if (r.T > kTreeMax) r.T = kTreeMax, r.bad = true;
+    if (r.T > r.L) r.bad = true;
     return r;
 }
 __device__ __forceinline__ int tree_row_tiles(const TreeParams &p, int T) { return (T + p.rt - 1) / p.rt; }

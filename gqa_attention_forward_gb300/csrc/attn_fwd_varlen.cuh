@@ -64,6 +64,7 @@ struct VarlenParams : Params {
     int pair;                // 1: the tiles are two heads of a group; 0: two row tiles of a head
     int block_rows;          // query rows of a unit: 128 (pair) or 256
     int head_units;          // units per block of rows: Hq / 2 (pair) or Hq
+    int most_blocks;         // blocks of rows that ascending offsets can have
     int q_head_y, k_head_y, v_head_y;  // tensor map order: 1 = (D, heads, rows), 0 = (D, rows, heads)
     long long o_row, o_head, v_row, v_head;  // strides in bytes
 };
@@ -180,8 +181,11 @@ struct VlWalk {
         count = __reduce_add_sync(0xffffffffu, n);
         return true;
     }
-    // Block b (b never decreases from call to call): its sequence and place, or false.
+    // Block b (b never decreases from call to call): its sequence and place, or false.  Offsets
+    // that descend can overlap, up to n_seqs times the rows: the walk ends at what ascending ones
+    // can have.
     __device__ __forceinline__ bool find(int b, int &seq, int &qb) {
+        if (b >= p.most_blocks) return false;
         while (b >= base + count)
             if (!next_level()) return false;
         int r = b - base;
@@ -210,18 +214,6 @@ struct VlWalk {
         return false;
     }
 };
-
-// 16 consecutive 32-bit TMEM columns of this thread's lane (warp-collective).
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-          "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr)
-        : "memory");
-}
 
 // The two products of a key tile, with the matrix descriptors of sdesc_sw128 put together in
 // the instruction's own block: the upper word is a constant, the lower one (start address and

@@ -125,7 +125,7 @@ attn_status_t launch_tree(int dev, int kid, const CUtensorMap &tq, const CUtenso
                             gqa::kMergeThreads, 0, s, prm);
 }
 
-// Least weight of a CTA's share in the tree kernel (a unit of one key tile weighs two).
+// Least weight of a CTA's share in the tree kernel (a unit weighs its key tiles and two more).
 constexpr int kTreeMinShare = 2;
 
 int log2_of(int x) {
@@ -138,6 +138,7 @@ attn_status_t check_cache(const attn_kv_cache_t *c) {
     if (c == nullptr) return ATTN_ERR_NULL;
     if (c->n_layers < 1 || c->n_pages < 1 || c->Hkv < 1 || c->n_rows < 1 || c->table_width < 1) return ATTN_ERR_SHAPE;
     if (c->page < 16 || c->page > 4096 || (c->page & (c->page - 1)) != 0) return ATTN_ERR_SHAPE;
+    if (c->n_rows > (1 << 26)) return ATTN_ERR_SHAPE;  // lists of sequences: grids and 32-bit indexes
     if (c->D != 64 && c->D != 128) return ATTN_ERR_HEADDIM;
     if (c->dtype != ATTN_F16 && c->dtype != ATTN_BF16) return ATTN_ERR_DTYPE;
     // 32-bit tile coordinates, positions and row numbers
@@ -265,6 +266,7 @@ attn_status_t attn_fwd_varlen(const void *q, const void *k, const void *v, void 
         prm.cu_q = cu_q + s0;
         prm.cu_k = (cu_k ? cu_k : cu_q) + s0;
         prm.n_seqs = n_seqs - s0 < gqa::kVlSeqs ? n_seqs - s0 : gqa::kVlSeqs;
+        prm.most_blocks = total_q / prm.block_rows + prm.n_seqs;
         if (attn_status_t e = launch(); e != ATTN_OK) return e;
     }
     return ATTN_OK;
@@ -305,9 +307,10 @@ attn_status_t attn_fwd_tree(const void *q, const attn_kv_cache_t *cache, int lay
     if (total_q > 1 && Hq > 1 && st[0] < st[1]) return ATTN_ERR_SHAPE;
     gqa::TreeParams prm = {};
     prm.rt = 128 / (Hq / Hkv);
-    const long long row_tiles = static_cast<long long>(total_q) / prm.rt + n_seqs;
+    // weight of the longest sequence with the largest tree in the kernel's list
     const long long key_tiles = (static_cast<long long>(cache->table_width) * cache->page + 127) / 128;
-    if (row_tiles * Hkv > INT_MAX / 2 / (key_tiles + 2) || static_cast<long long>(total_q) * Hq > INT_MAX) return ATTN_ERR_SHAPE;
+    const long long seq_weight = (gqa::kTreeMax + prm.rt - 1) / prm.rt * (key_tiles + 2) * Hkv;
+    if (seq_weight > INT_MAX / 2 || static_cast<long long>(total_q) * Hq > INT_MAX) return ATTN_ERR_SHAPE;
     int dev = 0;
     if (attn_status_t e = check_device(&dev); e != ATTN_OK) return e;
     size_t need = 0;
@@ -343,7 +346,7 @@ attn_status_t attn_fwd_tree(const void *q, const attn_kv_cache_t *cache, int lay
     if (!encode_packed_map(&tq, q, bf16, D, total_q, Hq, st[0], st[1], prm.rt, prm.group, &head_y) || head_y != 1 ||
         !encode_pool_map(&tk, kp, bf16, D, cache->page, slices) || !encode_pool_map(&tv, vp, bf16, D, cache->page, slices))
         return no_map();
-    const long long most = row_tiles * Hkv * (key_tiles + 2);
+    const long long most = (static_cast<long long>(total_q) / prm.rt + n_seqs) * Hkv * (key_tiles + 2);
     const unsigned grid = static_cast<unsigned>(most < sms ? most : sms);
     prm.grid = static_cast<int>(grid);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -356,12 +359,14 @@ attn_status_t attn_fwd_tree(const void *q, const attn_kv_cache_t *cache, int lay
             default: return launch_tree<128, true>(dev, kid, tq, tk, tv, prm, grid, s);
         }
     };
-    // at most kTreeSeqs sequences per launch; a launch leaves the tokens of the others alone
-    for (int s0 = 0; s0 < n_seqs; s0 += gqa::kTreeSeqs) {
+    // at most kTreeSeqs sequences per launch, and no more than the list's 32-bit weights hold
+    // whatever the device offsets are; a launch leaves the tokens of the others alone
+    const int step = static_cast<int>(seq_weight * gqa::kTreeSeqs > INT_MAX / 2 ? INT_MAX / 2 / seq_weight : gqa::kTreeSeqs);
+    for (int s0 = 0; s0 < n_seqs; s0 += step) {
         prm.cu = cu + s0;
         prm.seqs = seqs != nullptr ? seqs + s0 : nullptr;
         prm.seq0 = s0;
-        prm.n_seqs = n_seqs - s0 < gqa::kTreeSeqs ? n_seqs - s0 : gqa::kTreeSeqs;
+        prm.n_seqs = n_seqs - s0 < step ? n_seqs - s0 : step;
         if (attn_status_t e = launch(); e != ATTN_OK) return e;
     }
     return ATTN_OK;
@@ -399,12 +404,15 @@ attn_status_t attn_kv_append(const attn_kv_cache_t *cache, int layer, const void
     const long long D = cache->D, row = cache->Hkv * D;
     const long long st[4] = {strides ? strides[0] : row, strides ? strides[1] : D, strides ? strides[2] : row,
                              strides ? strides[3] : D};
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 4; ++i) {
+        if ((i % 2 == 0 ? total : cache->Hkv) == 1) continue;  // the stride of an axis of one entry
         if (st[i] < 0 || st[i] % 8 != 0 || st[i] >= (1ll << 36)) return ATTN_ERR_SHAPE;
+    }
     if (attn_status_t e = check_device(&dev); e != ATTN_OK) return e;
     const gqa::KvAppend x = {static_cast<const uint4 *>(k_new), static_cast<const uint4 *>(v_new), st[0] / 8, st[1] / 8,
                              st[2] / 8, st[3] / 8, cu, seqs, n, total, layer};
-    return launch_dependent(gqa::kv_append_kernel, static_cast<unsigned>((static_cast<long long>(total) + 7) / 8), 256, 0, static_cast<cudaStream_t>(stream), pool_of(cache), x);
+    return launch_dependent(gqa::kv_append_kernel, static_cast<unsigned>((static_cast<long long>(total) + 7) / 8), 256, 0,
+                            static_cast<cudaStream_t>(stream), pool_of(cache), x);
 }
 
 attn_status_t attn_kv_accept(const attn_kv_cache_t *cache, const int *cu, const int *seqs, const int *path, int path_width,

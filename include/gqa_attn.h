@@ -279,8 +279,8 @@ attn_status_t attn_fwd_host(const void *q_h, const void *k_h, const void *v_h, v
  *         overlapping ([heads, rows, D], or heads cut from one projection's output)
  * Limits: total_q and total_k at most 65535 * 128.
  * Errors: as attn_fwd_kv (no error for Nq_s > Nk_s); ATTN_ERR_SHAPE for strides.
- *         Offsets that descend or leave the tensors are clamped, and
- *         attn_last_device_error reports ATTN_ERR_SHAPE.
+ *         Offsets that descend or leave the tensors are clamped, with no more work done
+ *         than ascending ones can be, and attn_last_device_error reports ATTN_ERR_SHAPE.
  * Graphs, streams and ownership: as attn_fwd, one launch per 2048 sequences; no workspace.
  */
 attn_status_t attn_fwd_varlen(const void *q, const void *k, const void *v, void *o, float *lse,
@@ -330,7 +330,8 @@ attn_status_t attn_kv_extend(const attn_kv_cache_t *cache, const int *seqs, cons
  * [cu[i], cu[i+1]) of k_new, v_new [total, Hkv, D] are the last positions of sequence
  * seqs[i] (i, when NULL), whose lens already counts them (attn_kv_extend).  strides: NULL,
  * or 4 element strides {k row, k head, v row, v head}, multiples of 8.  A page that
- * another sequence shares is not written (ATTN_ERR_PAGE). */
+ * another sequence shares is not written (ATTN_ERR_PAGE), nor the rows of a sequence that
+ * was named before in the list (ATTN_ERR_SHAPE). */
 attn_status_t attn_kv_append(const attn_kv_cache_t *cache, int layer, const void *k_new,
                              const void *v_new, const long long *strides, const int *cu,
                              const int *seqs, int n, int total, void *stream);
@@ -339,7 +340,8 @@ attn_status_t attn_kv_append(const attn_kv_cache_t *cache, int layer, const void
  * T = cu[i+1] - cu[i] <= 128 positions of sequence seqs[i] (i, when NULL) are its tree's
  * tokens; path[i][0 .. taken[i]) are the accepted ones, ascending.  Their rows move to the
  * positions right behind those before the tree, and the sequence ends there; its pages
- * stay with it.  path is [n, path_width]. */
+ * stay with it.  path is [n, path_width].  A sequence named again stays as its first entry
+ * leaves it (ATTN_ERR_SHAPE). */
 attn_status_t attn_kv_accept(const attn_kv_cache_t *cache, const int *cu, const int *seqs,
                              const int *path, int path_width, const int *taken, int n,
                              void *stream);

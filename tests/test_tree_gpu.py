@@ -222,6 +222,21 @@ def test_bad_state_is_reported_and_stays_inside():
     check(q, cache, o, lse, [0, 1, 2], par, "f16", 1 / 8)
 
 
+def test_overlapping_offsets_and_trees_past_the_largest():
+    """Offsets that go back and forth over the queries, and one tree of 300 tokens: reported, and
+    the next call is right."""
+    T = [100]
+    cache = build([1000] * 8, 32, 2, 64, "f16", seed=41)
+    q = queries(100, 8, 64, "f16", 42)
+    binding.attention_tree(q, cache, i32([0, 100, 0, 100, 0, 100, 0, 100, 0]))
+    assert status() == binding.ATTN_ERR_SHAPE
+    binding.attention_tree(queries(300, 8, 64, "f16", 45), cache, offsets([300]))
+    assert status() == binding.ATTN_ERR_SHAPE
+    o, lse = binding.attention_tree(q, cache, offsets(T))
+    assert status() == binding.ATTN_OK
+    check(q, cache, o, lse, [0], [list(range(-1, 99))], "f16", 1 / 8)
+
+
 def test_captured_call_replays_on_new_lengths_trees_and_pages():
     cache = build([600, 600, 600], 32, 2, 128, "bf16", seed=20)
     T = [6, 6, 6]
@@ -288,6 +303,20 @@ def test_calls_at_once_on_two_streams():
         for o, l, po, pl in got[i]:
             assert torch.equal(o, want[i][0]) and torch.equal(l, want[i][1])
             assert torch.equal(po, packed[i][0]) and torch.equal(pl, packed[i][1])
+    assert status() == binding.ATTN_OK
+
+
+def test_stream_handles():
+    """The same bits with the stream as an object, as its handle and as the default stream's."""
+    cache = build([3000], 64, 2, 128, "bf16", seed=43)
+    q, cu = queries(4, 8, 128, "bf16", 44), offsets([4])
+    want = binding.attention_tree(q, cache, cu)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for s in (side, side.cuda_stream, torch.cuda.default_stream(), 0):
+        o, l = binding.attention_tree(q, cache, cu, stream=s)
+        torch.cuda.synchronize()
+        assert torch.equal(o, want[0]) and torch.equal(l, want[1])
     assert status() == binding.ATTN_OK
 
 

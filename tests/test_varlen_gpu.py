@@ -219,6 +219,20 @@ def test_bad_offsets_are_clamped_and_reported():
     check(q, k, v, o, lse, [100, 200], [100, 200], "bf16", 1 / math.sqrt(128), True)
 
 
+@pytest.mark.parametrize("Hq,Hkv", [(4, 2), (3, 1)])
+def test_overlapping_offsets_do_no_more_work_than_ascending_ones(Hq, Hkv):
+    """Offsets that go back and forth over the rows ask for more blocks than the tensors hold:
+    clamped, cut and reported, and the next call is right."""
+    q, k, v = make(300, Hq, Hkv, 64, "f16", seed=27)
+    s = torch.cuda.current_stream()
+    cu = torch.tensor([0, 300] * 40, dtype=torch.int32, device="cuda")
+    binding.attention_varlen(q, k, v, cu)
+    assert binding.attn_last_device_error(s) == binding.ATTN_ERR_SHAPE
+    o, lse = binding.attention_varlen(q, k, v, offsets([100, 200]))
+    assert binding.attn_last_device_error(s) == binding.ATTN_OK
+    check(q, k, v, o, lse, [100, 200], [100, 200], "f16", 1 / 8, True)
+
+
 def test_timeout_is_reported_and_the_next_call_works():
     lib = binding.load()
     q, k, v = make(300, 4, 2, 128, "bf16", seed=26)
