@@ -93,6 +93,17 @@ def test_trees(case, chain):
     check(q, cache, o, lse, range(len(ctx)), par, dtype, 1 / math.sqrt(D), heads=None if len(ctx) < 50 else [0])
 
 
+def test_wide_table_of_few_positions():
+    """A table for 8 million positions and 128 row tiles a tree: the call goes in launches of few
+    sequences, whose weights fit in 32 bits whatever the lengths are."""
+    cache = build([5, 130, 64, 200], 64, 1, 64, "f16", width=1 << 17, seed=46)
+    rows = [(3 * i) % 4 for i in range(300)]
+    q = queries(300, 128, 64, "f16", 47)
+    o, lse = binding.attention_tree(q, cache, offsets([1] * 300), seqs=i32(rows))
+    assert status() == binding.ATTN_OK
+    check(q, cache, o, lse, rows, [[-1]] * 300, "f16", 1 / 8, heads=[0, 127])
+
+
 def test_large_scores_layers_chosen_rows_and_strides():
     """Rows close to one-hot, the second layer, rows of the table in another order and one of
     them twice, queries cut from a projection, an output with strides of its own."""
