@@ -48,7 +48,13 @@ constexpr int kTreeThreads = 256;
 constexpr int kTreeSlots = 8;      // unit descriptors in flight (256 sequences of 1000: 189 us with 4, 177 with 8)
 constexpr int kTreeMax = 128;      // tokens of one tree
 constexpr int kTreeSeqs = 2048;    // most sequences of one launch (their lengths lie in shared memory)
-constexpr int kMergeThreads = 32;
+// The merge takes a warp (and block) per output row up to kMergeRows of them, and then blocks of
+// 4 warps over 8 rows of each CTA's slot 1.  The first finds its row's pieces before it has to
+// wait, but is bound by the blocks that are resident, as most wait for loads; in the second most
+// blocks may have no row.  us per call, first / second: 128 rows 10.6 / 11.7, 1024 rows of 20
+// pieces 27.9 / 32.1, 2048 rows 39.6 / 41.0, 5120 rows 35.8 / 36.3, 8192 rows 57.9 / 55.0 and
+// 182.5 / 178.7, 12288 rows 46.2 / 41.8, 16384 rows 28.3 / 15.6, 32768 rows 88.7 / 66.4.
+constexpr int kMergeRows = 6144, kMergeCtaThreads = 128, kMergeCtaRows = 8;
 constexpr int kTreeBadTiles = 2;   // the tree's positions lie in at most two key tiles
 
 struct TreeParams : Params {
@@ -63,7 +69,10 @@ struct TreeParams : Params {
     float *part_o;             // [2 * CTAs][128][D]
     float *part_lse;           // [2 * CTAs][128]
     int grid;                  // CTAs of the first kernel
-    int *plan;                 // [0]: share, [1 + s]: weights before sequence s
+    // for the merge, one of the two: of each CTA's slot 1 the first packed row, kv head << 8 | tokens
+    // (0: unused), key tiles behind this CTA and share; or [0]: share, [1 + s]: weights before sequence s
+    int4 *starts;
+    int *plan;
 };
 
 struct TreeUnit {
@@ -95,7 +104,7 @@ struct TreeLayout {
     static constexpr int kAbort = kTmemSlot + 4;
     static constexpr int kUnits = (kAbort + 4 + 15) & ~15;
     static constexpr int kPar = kUnits + kTreeSlots * static_cast<int>(sizeof(TreeUnit));
-    static constexpr int kSeqs = (kPar + 2 * kTreeMax * 4 + 15) & ~15;
+    static constexpr int kSeqs = (kPar + 4 * kTreeMax * 4 + 15) & ~15;
     static constexpr int kUsed = kSeqs + kTreeSeqs * 8;
     // more than half of an SM's shared memory: one CTA (all 512 TMEM columns) per SM
     static constexpr int kAlloc = (kUsed + 1024) > 118 * 1024 ? (kUsed + 1024) : 118 * 1024;
@@ -269,14 +278,19 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         int total = 0;
         for (int s0 = 0; s0 < p.n_seqs; s0 += 32) {
             const int w = weight_of(s0 + lane);
-            if (blockIdx.x == 0) {
+            if (p.plan != nullptr && blockIdx.x == 0) {
                 const int incl = scan(w);
                 if (s0 + lane < p.n_seqs) p.plan[1 + s0 + lane] = total + incl - w;
             }
             total += __reduce_add_sync(0xffffffffu, w);
         }
         const int share = tree_share(p, total);
-        if (blockIdx.x == 0 && lane == 0) p.plan[0] = share;
+        if (lane == 0) {
+            if (p.plan == nullptr)
+                p.starts[blockIdx.x] = make_int4(0, 0, 0, 0);
+            else if (blockIdx.x == 0)
+                p.plan[0] = share;
+        }
         // 64-bit: the last CTAs' first tiles may lie past the end
         const long long first = static_cast<long long>(blockIdx.x) * share;
         int at = first < total ? static_cast<int>(first) : total;
@@ -338,6 +352,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                         u.piece = (k0 == 0 && k1 == nt) ? -1 : (k0 > 0 ? 0 : 1);
                         u.first = q.q0;
                         u.bad = 0;
+                        // a unit that begins here and goes on in the next CTAs is merged
+                        if (u.piece > 0 && p.plan == nullptr)
+                            p.starts[blockIdx.x] = make_int4(u.q0, u.kvh << 8 | u.ntok, nt - k1, share);
                     }
                     ++emitted;
                 } else if (lane == 0) {
@@ -615,7 +632,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
         const float c = p.scale_log2;
         const int tok = r / p.group;  // token within the row tile
-        int *par0 = reinterpret_cast<int *>(smem + L::kPar);
+        int *par = reinterpret_cast<int *>(smem + L::kPar) + wq * kTreeMax;
         int slot = -1, done_slot = -1;  // the unit at work, and the one whose O is still to be stored
         uint32_t uphase = 1, jj = 0, un = 0;  // tiles and units so far
         int kt = 0, k0 = 0, k1 = 0, tree0 = 0;
@@ -643,10 +660,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                     anc.lo = 1ull;
                     anc.hi = 0ull;
                     if (u.T > 1) {
-                        // the tree's parents (without: a chain), one per thread
-                        int *par = par0 + (un & 1u) * kTreeMax;
-                        par[r] = p.parents != nullptr && r < u.T ? __ldg(p.parents + u.first + r) : r - 1;
-                        asm volatile("bar.sync 1, 128;" ::: "memory");
+                        // the tree's parents (without: a chain), a copy for each warp
+#pragma unroll 1
+                        for (int t = lane; t < u.T && t < kTreeMax; t += 32)
+                            par[t] = p.parents != nullptr ? __ldg(p.parents + u.first + t) : t - 1;
+                        __syncwarp();
                         if (valid) anc = tree_ancestors(u.t0 + tok, [&](int t) { return par[t]; });
                     }
                     ++un;
@@ -859,38 +877,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     }
 }
 
-// Merges the pieces of the units that were cut: lse = log sum_s exp(lse_s) and
-// O = sum_s exp(lse_s - lse) O_s (the online-softmax update of page "从零开始写Qwen3",
-// deepseek.csdn.net/6a3201f8..., section "在线softmax", across CTAs).  One warp per output
-// row; a row whose unit lay in one share has been written already.  The row's sequence is looked
-// for before the wait for the kernel before; after it come the plan, and then in one round trip
-// the log-sum-exps (lane j: piece j) and the rows of 8 pieces.  (Adding the plan up here before
-// the wait, too, saves 0.3 us of 11 with one sequence and nothing with 16.)
+// Merges the pieces of row prow of a unit that begins in slot 1 of CTA c0 and ends in slot 0 of
+// CTA c1: lse = log sum_s exp(lse_s) and O = sum_s exp(lse_s - lse) O_s (the online-softmax update
+// of page "从零开始写Qwen3", deepseek.csdn.net/6a3201f8..., section "在线softmax", across CTAs).
+// One round trip brings the log-sum-exps (lane j: piece j) and the rows of 8 pieces.
 template <int D, bool kBF16>
-__global__ void __launch_bounds__(kMergeThreads) attn_tree_merge_kernel(const __grid_constant__ TreeParams p) {
-    grid_launch_dependents();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const long long R = static_cast<long long>(blockIdx.x) * (kMergeThreads / 32) + warp;
-    const bool in = R < static_cast<long long>(p.total_q) * p.Hq;
-    const int tok = static_cast<int>(R / p.Hq), head = static_cast<int>(R - static_cast<long long>(tok) * p.Hq);
-    // the sequence of this token: the last one that starts at or before it
-    int lo = 0, hi = p.n_seqs;  // cu[lo] <= tok < cu[hi], where the offsets ascend
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (__ldg(p.cu + mid) <= tok) lo = mid; else hi = mid;
-    }
-    const TreeSeq q = tree_seq(p, lo);
-    const int nt = tree_key_tiles(q.L), mt = tree_row_tiles(p, q.T), uw = tree_unit_weight(nt);
-    const int t = tok - q.q0, m = t / p.rt;
-    const int prow = (t - m * p.rt) * p.group + head % p.group;  // row within the tile
-    grid_dependency_wait();
-    if (!in || t < 0 || t >= q.T) return;
-    const int share = p.plan[0], before = p.plan[1 + lo];
-    // the weight past the unit's last tile, and the CTAs of its first and last one
-    const int end = before + ((head / p.group) * mt + m + 1) * uw;
-    const int c0 = (end - nt) / share, c1 = (end - 1) / share;
-    // (lengths that changed since the kernel before, against the rules, must not lead outside)
-    if (c0 >= c1 || c0 < 0 || c1 >= p.grid) return;
+__device__ __forceinline__ void tree_merge_row(const TreeParams &p, int c0, int c1, int prow, int tok, int head, int lane) {
     constexpr int kPer = D / 32;
     // where the kernel before gave up on a wait, its pieces may be stale: NaN
     const bool gave_up = *reinterpret_cast<volatile unsigned int *>(&g_abort_seq) == p.seq;
@@ -947,6 +939,55 @@ __global__ void __launch_bounds__(kMergeThreads) attn_tree_merge_kernel(const __
     if (p.lse != nullptr && lane == 0)
         p.lse[static_cast<size_t>(head) * p.total_q + tok] =
             gave_up ? __int_as_float(0x7FC00000) : (sum == 0.f ? -INFINITY : mx + logf(sum));
+}
+
+// The cut units, a warp per output row: a row whose unit lay in one share has been written already.
+// The row's sequence is looked for before the wait for the kernel before; after it comes the plan.
+// (Adding the plan up here before the wait, too, saves 0.3 us of 11 with one sequence and nothing
+// with 16.)
+template <int D, bool kBF16>
+__global__ void __launch_bounds__(32) attn_tree_merge_kernel(const __grid_constant__ TreeParams p) {
+    grid_launch_dependents();
+    const int lane = threadIdx.x & 31, R = static_cast<int>(blockIdx.x);
+    const int tok = R / p.Hq, head = R - tok * p.Hq;
+    // the sequence of this token: the last one that starts at or before it
+    int lo = 0, hi = p.n_seqs;  // cu[lo] <= tok < cu[hi], where the offsets ascend
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (__ldg(p.cu + mid) <= tok) lo = mid; else hi = mid;
+    }
+    const TreeSeq q = tree_seq(p, lo);
+    const int nt = tree_key_tiles(q.L), mt = tree_row_tiles(p, q.T), uw = tree_unit_weight(nt);
+    const int t = tok - q.q0, m = t / p.rt;
+    const int prow = (t - m * p.rt) * p.group + head % p.group;  // row within the tile
+    grid_dependency_wait();
+    if (t < 0 || t >= q.T) return;
+    const int share = p.plan[0], before = p.plan[1 + lo];
+    // the weight past the unit's last tile, and the CTAs of its first and last one
+    const int end = before + ((head / p.group) * mt + m + 1) * uw;
+    const int c0 = (end - nt) / share, c1 = (end - 1) / share;
+    // (lengths that changed since the kernel before, against the rules, must not lead outside)
+    if (c0 >= c1 || c0 < 0 || c1 >= p.grid) return;
+    tree_merge_row<D, kBF16>(p, c0, c1, prow, tok, head, lane);
+}
+
+// The same by CTAs, of which each has left what its slot 1 holds; the blocks of one CTA go to
+// different SMs.
+template <int D, bool kBF16>
+__global__ void __launch_bounds__(kMergeCtaThreads) attn_tree_merge_ctas_kernel(const __grid_constant__ TreeParams p) {
+    grid_launch_dependents();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = static_cast<int>(blockIdx.x) / p.grid, c0 = (static_cast<int>(blockIdx.x) + 37 * g) % p.grid;
+    grid_dependency_wait();
+    const int4 unit = p.starts[c0];
+    const int row0 = g * kMergeCtaRows, rows = (unit.y & 255) * p.group, kvh = unit.y >> 8;
+    if (row0 >= rows) return;
+    const int c1 = c0 + 1 + (unit.z - 1) / unit.w;
+#pragma unroll 1
+    for (int r = row0 + warp; r < row0 + kMergeCtaRows && r < rows; r += kMergeCtaThreads / 32) {
+        const int t = r / p.group;
+        tree_merge_row<D, kBF16>(p, c0, c1, r, unit.x + t, kvh * p.group + (r - t * p.group), lane);
+    }
 }
 
 }  // namespace gqa

@@ -119,10 +119,11 @@ attn_status_t launch_tree(int dev, int kid, const CUtensorMap &tq, const CUtenso
     if (attn_status_t st = launch_dependent(kern, grid, gqa::kTreeThreads, smem, s, tq, tk, tv, prm);
         st != ATTN_OK)
         return st;
-    const long long rows = static_cast<long long>(prm.total_q) * prm.Hq;
-    constexpr int per = gqa::kMergeThreads / 32;
-    return launch_dependent(gqa::attn_tree_merge_kernel<D, BF16>, static_cast<unsigned>((rows + per - 1) / per),
-                            gqa::kMergeThreads, 0, s, prm);
+    if (prm.plan != nullptr)
+        return launch_dependent(gqa::attn_tree_merge_kernel<D, BF16>, static_cast<unsigned>(prm.total_q) * prm.Hq, 32, 0,
+                                s, prm);
+    constexpr unsigned per_cta = gqa::kBM / gqa::kMergeCtaRows;
+    return launch_dependent(gqa::attn_tree_merge_ctas_kernel<D, BF16>, grid * per_cta, gqa::kMergeCtaThreads, 0, s, prm);
 }
 
 // Least weight of a CTA's share in the tree kernel (a unit weighs its key tiles and two more).
@@ -281,7 +282,8 @@ attn_status_t attn_fwd_tree_workspace(int n_seqs, int D, size_t *bytes) {
     if (attn_status_t st = check_device(&dev); st != ATTN_OK) return st;
     const size_t rows = static_cast<size_t>(g_dev_sms[dev]) * 2 * gqa::kBM;
     const int launch_seqs = n_seqs < gqa::kTreeSeqs ? n_seqs : gqa::kTreeSeqs;
-    *bytes = rows * (D + 1) * sizeof(float) + (static_cast<size_t>(launch_seqs) + 1) * sizeof(int);
+    const size_t plan = (static_cast<size_t>(launch_seqs) + 1) * sizeof(int), starts = g_dev_sms[dev] * sizeof(int4);
+    *bytes = rows * (D + 1) * sizeof(float) + (plan > starts ? plan : starts);
     return ATTN_OK;
 }
 
@@ -338,7 +340,11 @@ attn_status_t attn_fwd_tree(const void *q, const attn_kv_cache_t *cache, int lay
     const int sms = g_dev_sms[dev];
     prm.part_o = static_cast<float *>(workspace);
     prm.part_lse = prm.part_o + static_cast<size_t>(sms) * 2 * gqa::kBM * D;
-    prm.plan = reinterpret_cast<int *>(prm.part_lse + static_cast<size_t>(sms) * 2 * gqa::kBM);
+    void *plan = prm.part_lse + static_cast<size_t>(sms) * 2 * gqa::kBM;
+    if (total_q * Hq <= gqa::kMergeRows)
+        prm.plan = static_cast<int *>(plan);
+    else
+        prm.starts = static_cast<int4 *>(plan);
     const bool bf16 = cache->dtype == ATTN_BF16;
     CUtensorMap tq, tk, tv;
     int head_y = 0;

@@ -93,6 +93,21 @@ def test_trees(case, chain):
     check(q, cache, o, lse, range(len(ctx)), par, dtype, 1 / math.sqrt(D), heads=None if len(ctx) < 50 else [0])
 
 
+@pytest.mark.parametrize("Hq,Hkv,D,dtype,T", [(32, 8, 128, "bf16", [128, 100, 0, 37, 1]), (24, 8, 64, "f16", [90, 128, 1, 64, 0]),
+                                              (32, 1, 128, "f16", [128, 64, 2, 7, 1])])
+def test_many_cut_rows(Hq, Hkv, D, dtype, T):
+    """More output rows than the merge takes one by one: it goes over the CTAs' pieces."""
+    ctx = [3000, 9001, 500, 0, 7777]
+    cache = build([a + b for a, b in zip(ctx, T)], 64, Hkv, D, dtype, seed=48)
+    par = trees(T, 49)
+    q = queries(sum(T) + 3, Hq, D, dtype, 50)
+    out = torch.full_like(q, 7)
+    o, lse = binding.attention_tree(q, cache, offsets(T), parents=i32([x for p in par for x in p] + [-1] * 3), out=out)
+    assert status() == binding.ATTN_OK
+    check(q, cache, o, lse, range(5), par, dtype, 1 / math.sqrt(D), heads=[0, Hq // 2, Hq - 1])
+    assert bool((o[-3:] == 7).all())
+
+
 def test_wide_table_of_few_positions():
     """A table for 8 million positions and 128 row tiles a tree: the call goes in launches of few
     sequences, whose weights fit in 32 bits whatever the lengths are."""
