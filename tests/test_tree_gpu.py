@@ -108,6 +108,22 @@ def test_many_cut_rows(Hq, Hkv, D, dtype, T):
     assert bool((o[-3:] == 7).all())
 
 
+@pytest.mark.parametrize("Hq,Hkv,D,dtype,ctx,T", [
+    (16, 8, 128, "bf16", [20000, 300], [128, 60]),
+    (32, 8, 128, "bf16", [20001, 9000, 40], [128, 90, 33]),
+    (32, 4, 64, "f16", [70000, 1000], [50, 128]),
+    (24, 8, 128, "f16", [30000, 0, 12345], [43, 0, 100]),
+    (64, 1, 128, "bf16", [20010], [30])])
+def test_trees_of_several_row_tiles_over_long_contexts(Hq, Hkv, D, dtype, ctx, T):
+    """Several row tiles, each cut over many CTAs, merged by rows and by CTAs."""
+    cache = build([a + b for a, b in zip(ctx, T)], 64, Hkv, D, dtype, seed=51)
+    par = trees(T, 52)
+    q = queries(sum(T), Hq, D, dtype, 53)
+    o, lse = binding.attention_tree(q, cache, offsets(T), parents=i32([x for p in par for x in p]))
+    assert status() == binding.ATTN_OK
+    check(q, cache, o, lse, range(len(T)), par, dtype, 1 / math.sqrt(D), heads=[0, Hq // 2 + 1, Hq - 1])
+
+
 def test_wide_table_of_few_positions():
     """A table for 8 million positions and 128 row tiles a tree: the call goes in launches of few
     sequences, whose weights fit in 32 bits whatever the lengths are."""
