@@ -489,7 +489,9 @@ __global__ void __cluster_dims__(kAcceptCtas, 1, 1) __launch_bounds__(256)
         const int j = threadIdx.x;
         const int at = path[static_cast<size_t>(i) * path_w + j];
         const int prev = j > 0 ? path[static_cast<size_t>(i) * path_w + j - 1] : -1;
-        if (at <= prev || at >= T) {
+        // (each entry on its own, before it is an index: one that ascends from a negative one is
+        // negative, too, and lies before the tree)
+        if (at < 0 || at <= prev || at >= T) {
             atomicExch(&bad, 1);  // not an ascending path within the tree
         } else {
             const int ps = base + at, pd = base + j;
