@@ -456,7 +456,7 @@ attn_status_t attn_kv_fork(const attn_kv_cache_t *cache, const int *parents, con
     if (attn_status_t st = check_device(&dev); st != ATTN_OK) return st;
     const gqa::KvPool p = pool_of(cache);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (attn_status_t st = launch_dependent(gqa::kv_fork_kernel, 1, gqa::kPlanThreads, 0, s, p, parents, children, n);
+    if (attn_status_t st = launch_dependent(gqa::kv_fork_kernel, gqa::kForkCtas, gqa::kPlanThreads, 0, s, p, parents, children, n);
         st != ATTN_OK)
         return st;
     return launch_dependent(gqa::kv_move_kernel<gqa::kMoveFork>, move_grid(p, n, g_dev_sms[dev]), 256, 0, s, p, parents,

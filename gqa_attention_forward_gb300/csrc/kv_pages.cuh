@@ -179,12 +179,42 @@ __global__ void __launch_bounds__(kPlanThreads) kv_extend_kernel(const KvPool c,
 
 // Children take the lengths of their parents and a free page for the last page that is not
 // full; pairs lists what kv_move_kernel<kMoveFork> then copies, beside the table entries of the
-// full pages and their references, which one block would take too long over.
-__global__ void __launch_bounds__(kPlanThreads) kv_fork_kernel(const KvPool c, const int *parents, const int *children, int n) {
+// full pages and their references, which one block would take too long over.  A request is
+// refused as a whole before anything is written: all pages of its parent are looked at first,
+// a warp per request (4 entries per lane in flight) of a cluster of kForkCtas blocks, as a long
+// context has thousands of them; the first block then plans alone.
+constexpr int kForkCtas = 8;
+__global__ void __cluster_dims__(kForkCtas, 1, 1) __launch_bounds__(kPlanThreads)
+    kv_fork_kernel(const KvPool c, const int *parents, const int *children, int n) {
     __shared__ int sm[33];
     grid_launch_dependents();
     grid_dependency_wait();
     auto in = [&](int s) { return s >= 0 && s < c.n_rows; };
+    constexpr int kFine = -1, kRefused = -2, kNoPage = -3;  // in pairs[3 i]
+    const int lane = threadIdx.x & 31;
+    for (int i = blockIdx.x * (kPlanThreads / 32) + (threadIdx.x >> 5); i < n; i += kForkCtas * (kPlanThreads / 32)) {
+        const int a = parents[i];
+        int verdict = kRefused;
+        if (in(a)) {
+            const int len = c.lens[a];
+            if (len >= 0 && len <= (static_cast<long long>(c.table_w) << c.page_shift)) {
+                const int pages = static_cast<int>((static_cast<long long>(len) + c.page - 1) >> c.page_shift);
+                const int *row = kv_row(c, a);
+                bool hole = false;
+                for (int j = lane; j < pages; j += 128) {
+                    int p[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) p[e] = j + 32 * e < pages ? row[j + 32 * e] : 0;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) hole |= p[e] < 0 || p[e] >= c.n_pages;
+                }
+                verdict = __any_sync(0xffffffffu, hole) ? kNoPage : kFine;
+            }
+        }
+        if (lane == 0) c.pairs[3 * i] = verdict;
+    }
+    cooperative_groups::this_cluster().sync();
+    if (blockIdx.x != 0) return;
     for (int i = threadIdx.x; i < n; i += kPlanThreads) {
         const int a = parents[i], b = children[i];
         if (in(a)) c.claim[a] = INT_MAX;
@@ -202,16 +232,12 @@ __global__ void __launch_bounds__(kPlanThreads) kv_fork_kernel(const KvPool c, c
     };
     for (int i = threadIdx.x; i < n; i += kPlanThreads) {
         int a, b;
-        bool ok = fine(i, a, b) && c.lens[b] == 0 && kv_row(c, b)[0] < 0;
-        const int len = ok ? c.lens[a] : 0;
-        ok = ok && len >= 0 && len <= (static_cast<long long>(c.table_w) << c.page_shift);
-        if (ok && (len & (c.page - 1)) != 0) {
-            const int p = kv_row(c, a)[len >> c.page_shift];
-            ok = p >= 0 && p < c.n_pages;
-        }
-        c.need[i] = ok && (len & (c.page - 1)) != 0 ? 1 : 0;
-        c.pairs[3 * i] = ok ? -1 : -2;  // -2: refused
-        if (!ok) kv_error(ATTN_ERR_SHAPE);
+        const int verdict = c.pairs[3 * i];
+        const bool right = fine(i, a, b) && c.lens[b] == 0 && kv_row(c, b)[0] < 0 && verdict != kRefused;
+        const bool ok = right && verdict == kFine;
+        c.need[i] = ok && (c.lens[a] & (c.page - 1)) != 0 ? 1 : 0;
+        c.pairs[3 * i] = ok ? kFine : kRefused;
+        if (!ok) kv_error(right ? ATTN_ERR_PAGE : ATTN_ERR_SHAPE);
     }
     __syncthreads();
     const int want = kv_offsets(c.need, n, sm);
@@ -220,9 +246,9 @@ __global__ void __launch_bounds__(kPlanThreads) kv_fork_kernel(const KvPool c, c
     if (have < want && threadIdx.x == 0) kv_error(ATTN_ERR_POOL);
     for (int i = threadIdx.x; i < n; i += kPlanThreads) {
         const int off = c.need[i], past = i + 1 < n ? c.need[i + 1] : want;
-        if (c.pairs[3 * i] == -2) continue;
+        if (c.pairs[3 * i] == kRefused) continue;
         if (past > have) {
-            c.pairs[3 * i] = -2;
+            c.pairs[3 * i] = kRefused;
             continue;
         }
         const int a = parents[i], b = children[i], len = c.lens[a];
@@ -309,10 +335,8 @@ __device__ __forceinline__ void kv_share(const KvPool &c, const int *parents, co
         const int b = children[i];
         if (j >= c.lens[b] >> c.page_shift) continue;
         const int p = kv_row(c, parents[i])[j];
-        if (p >= 0 && p < c.n_pages)
-            atomicAdd(&c.refs[p], 1);
-        else
-            kv_error(ATTN_ERR_PAGE);
+        if (p < 0 || p >= c.n_pages) continue;  // (changed since it was looked at, against the rules)
+        atomicAdd(&c.refs[p], 1);
         kv_row(c, b)[j] = p;
     }
 }

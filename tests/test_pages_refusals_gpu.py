@@ -36,3 +36,50 @@ def test_paths_of_no_tree(path):
     assert status() == binding.ATTN_ERR_SHAPE
     m.accept([0, 2], [5, 3], [[1, 4], [0, 2]])
     m.same(c)
+
+
+@pytest.mark.parametrize("page,length", [(16, 64), (16, 70), (32, 32 * 300 + 5), (128, 1)])
+@pytest.mark.parametrize("entry", [-1, LOWEST, 10 ** 6, "n_pages"])
+def test_fork_of_a_parent_with_a_bad_page(page, length, entry):
+    """A page that is missing or out of range, full or not, first, middle or last: the request is
+    refused as a whole and the others of the list are served, in their order."""
+    pages = -(-length // page)
+    for j in sorted({0, pages // 2, pages - 1}):
+        c = build([length, 2 * page + 3, page], page, 2, 64, "f16", 1, extra_pages=5, n_rows=9)
+        c.table[0, j] = c.n_pages if entry == "n_pages" else entry
+        m = Model(c)
+        binding.kv_fork(c, i32([0]), i32([4]))
+        assert status() == binding.ATTN_ERR_PAGE
+        m.same(c)
+        binding.kv_fork(c, i32([1, 0, 2, 0, 1]), i32([5, 4, 6, 3, 7]))
+        assert status() == binding.ATTN_ERR_PAGE
+        m.fork([1, 2, 1], [5, 6, 7])
+        m.same(c)
+
+
+def test_fork_of_many_parents_of_which_some_are_bad():
+    """More requests than the cluster has warps."""
+    page, n = 16, 700
+    lens = [(37 * i) % 100 for i in range(n)]
+    c = build(lens, page, 1, 64, "bf16", extra_pages=n, seed=6, n_rows=2 * n)
+    bad = [i for i in range(n) if lens[i] > page and i % 5 == 0]
+    for i in bad:
+        c.table[i, 0] = -1 if i % 2 else c.n_pages + i
+    m = Model(c)
+    binding.kv_fork(c, i32(list(range(n))), i32([n + i for i in range(n)]))
+    assert status() == binding.ATTN_ERR_PAGE
+    good = [i for i in range(n) if i not in bad]
+    m.fork(good, [n + i for i in good])
+    m.same(c)
+
+
+def test_fork_of_a_length_past_the_table():
+    c = build([40, 20], 16, 2, 64, "f16", n_rows=6)
+    for length in (-1, 10 ** 6, 2 ** 31 - 1):
+        c.lens[0] = length
+        m = Model(c)
+        binding.kv_fork(c, i32([0, 1]), i32([4, 5]))
+        assert status() == binding.ATTN_ERR_SHAPE
+        m.fork([1], [5])
+        m.same(c)
+        binding.kv_free(c, i32([5]))
