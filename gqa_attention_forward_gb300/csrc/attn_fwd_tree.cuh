@@ -116,15 +116,16 @@ struct TreeSeq {
     int q0, T, L, row;
     bool bad;
 };
+template <bool kAhead = false>
 __device__ __forceinline__ TreeSeq tree_seq(const TreeParams &p, int s) {
-    const VlSpan q = vl_span(p.cu, s, p.total_q);
-    const int row = p.seqs != nullptr ? __ldg(p.seqs + s) : p.seq0 + s;
+    const VlSpan q = vl_span<kAhead>(p.cu, s, p.total_q);
+    const int row = p.seqs != nullptr ? ld_state<kAhead>(p.seqs + s) : p.seq0 + s;
     TreeSeq r{q.a, q.b - q.a, 0, row, q.bad};
     if (row < 0 || row >= p.n_rows) {
         r.row = -1;
         r.bad = true;
     } else {
-        r.L = __ldg(p.lens + row);
+        r.L = ld_state<kAhead>(p.lens + row);
     }
     const long long cap = static_cast<long long>(p.table_w) << p.page_shift;
     if (r.L < 0) r.L = 0, r.bad = true;
@@ -406,7 +407,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         int slot = 0;
         uint32_t uphase = 0;
         auto entry = [&](const Cur &c, int i) -> int {
-            return c.row >= 0 && i < c.pages ? __ldg(p.table + static_cast<long long>(c.row) * p.table_w + i) : -1;
+            return c.row >= 0 && i < c.pages ? p.table[static_cast<long long>(c.row) * p.table_w + i] : -1;
         };
         auto take = [&](Cur &c) {  // the descriptor in the slot has arrived
             const TreeUnit &u = units[slot];
@@ -663,7 +664,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                         // the tree's parents (without: a chain), a copy for each warp
 #pragma unroll 1
                         for (int t = lane; t < u.T && t < kTreeMax; t += 32)
-                            par[t] = p.parents != nullptr ? __ldg(p.parents + u.first + t) : t - 1;
+                            par[t] = p.parents != nullptr ? p.parents[u.first + t] : t - 1;
                         __syncwarp();
                         if (valid) anc = tree_ancestors(u.t0 + tok, [&](int t) { return par[t]; });
                     }
@@ -835,7 +836,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                             // added to the stored row, whose other values they do not change
                             const Bits128 seen = u.T > 1
                                 ? tree_ancestors(u.t0 + tok, [&](int t) {
-                                      return p.parents != nullptr && t < u.T ? __ldg(p.parents + u.first + t) : t - 1;
+                                      return p.parents != nullptr && t < u.T ? p.parents[u.first + t] : t - 1;
                                   })
                                 : Bits128{1ull, 0ull};
 #pragma unroll 1
@@ -845,8 +846,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                                     const int key = u.base / kBN * kBN + 32 * g + __ffs(bits) - 1, node = key - u.base;
                                     if (node >= 0 && !((node < 64 ? seen.lo >> node : seen.hi >> (node - 64)) & 1ull))
                                         continue;
-                                    const int pg = __ldg(p.table + static_cast<long long>(u.row) * p.table_w +
-                                                         (key >> p.page_shift));
+                                    const int pg = p.table[static_cast<long long>(u.row) * p.table_w + (key >> p.page_shift)];
                                     const uint8_t *vr = p.v_ptr + ((static_cast<size_t>(pg) * p.Hkv + u.kvh) * p.page +
                                                                    (key & (p.page - 1))) * (D * 2);
                                     if (whole)
@@ -954,9 +954,9 @@ __global__ void __launch_bounds__(32) attn_tree_merge_kernel(const __grid_consta
     int lo = 0, hi = p.n_seqs;  // cu[lo] <= tok < cu[hi], where the offsets ascend
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (__ldg(p.cu + mid) <= tok) lo = mid; else hi = mid;
+        if (ld_ahead_of_wait(p.cu + mid) <= tok) lo = mid; else hi = mid;
     }
-    const TreeSeq q = tree_seq(p, lo);
+    const TreeSeq q = tree_seq<true>(p, lo);
     const int nt = tree_key_tiles(q.L), mt = tree_row_tiles(p, q.T), uw = tree_unit_weight(nt);
     const int t = tok - q.q0, m = t / p.rt;
     const int prow = (t - m * p.rt) * p.group + head % p.group;  // row within the tile

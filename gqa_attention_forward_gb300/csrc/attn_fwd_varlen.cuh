@@ -147,8 +147,9 @@ struct VlSpan {
     int a, b;
     bool bad;
 };
+template <bool kAhead = false>  // read ahead of grid_dependency_wait
 __device__ __forceinline__ VlSpan vl_span(const int *cu, int s, int total) {
-    const int a0 = __ldg(cu + s), b0 = __ldg(cu + s + 1);
+    const int a0 = ld_state<kAhead>(cu + s), b0 = ld_state<kAhead>(cu + s + 1);
     const int a = a0 < 0 ? 0 : (a0 > total ? total : a0);
     const int b = b0 < a ? a : (b0 > total ? total : b0);
     return {a, b, a != a0 || b != b0};

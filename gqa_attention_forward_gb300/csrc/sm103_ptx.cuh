@@ -272,6 +272,21 @@ __device__ __forceinline__ void grid_dependency_wait() {
 __device__ __forceinline__ void grid_launch_dependents() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
+// What a call reads and an earlier one may write (offsets, lists, lengths, tables, new rows) can
+// change while this kernel's blocks are already resident, waiting.  It is read with plain loads
+// behind grid_dependency_wait, never by the read-only path (__ldg), which needs data that is
+// constant for the kernel's whole life; ahead of the wait, where its writer has ended all the
+// same, with this load, which goes to L2 whatever an SM's L1 still holds.
+__device__ __forceinline__ int ld_ahead_of_wait(const int *p) {
+    int x;
+    asm volatile("ld.relaxed.gpu.global.s32 %0, [%1];" : "=r"(x) : "l"(p) : "memory");
+    return x;
+}
+template <bool kAhead>
+__device__ __forceinline__ int ld_state(const int *p) {
+    if constexpr (kAhead) return ld_ahead_of_wait(p);
+    return *p;
+}
 
 // ---------------------------------------------------------------- math
 __device__ __forceinline__ float ex2_approx(float x) {
