@@ -27,11 +27,12 @@
 // block of a level is found with a ballot over the sequences.  A CTA's units only ever
 // move down the levels.
 //
-// Units without keys come last (a second walk, taken only where a CTA has any).  The producer,
-// the issuer and the guard look one unit ahead, and the unit at work keeps its descriptor slot
-// until its last V tile, which the producer loads after that look: a look past any number of
-// units without keys would wait for slots that wait for it.  So the first unit without keys
-// ends these three roles, and the softmax warps store the zeros of it and of those behind it.
+// Units without keys are not handed out: the scheduler warp stores their zeros itself.  The
+// producer, the issuer and the guard look one unit ahead, and the unit at work keeps its
+// descriptor slot until its last V tile, which the producer loads after that look: a look past
+// any number of units without keys would wait for slots that wait for it.  (Handing them out
+// behind the others, to the softmax warps alone, takes a second walk and 58.6 us instead of 40.6
+// for 8192 queries over 512 keys, Hq 32, D 128.)
 //
 // Roles (384 threads): warp 0 MMA issuer, warp 1 value guard (and TMEM), warp 2 TMA
 // producer, warp 3 scheduler, warps 4-7 and 8-11 the softmax of tile 0 and 1.  Shared memory,
@@ -62,7 +63,6 @@ namespace gqa {
 constexpr int kVlSlots = 4;       // unit descriptors in flight
 constexpr int kVlSeqs = 2048;     // most sequences of one launch (their block counts lie in shared memory)
 constexpr int kVlBadTiles = 4;    // key tiles of a unit that the guard may look at
-constexpr int kVlKeyRoles = 3;    // producer, issuer and guard: they have nothing to do without keys
 
 struct VarlenParams : Params {
     const int *cu_q, *cu_k;  // device [n_seqs + 1]
@@ -133,6 +133,21 @@ __device__ __forceinline__ VlTile vl_tile(const VarlenParams &p, const VlUnit &u
 template <bool kCausal>
 __device__ __forceinline__ bool vl_has_keys(const VarlenParams &p, int rows, int nk, int rel) {
     return nk > 0 && (!kCausal || rel + (rows < p.block_rows ? rows : p.block_rows) > 0);
+}
+// Rows [q0, q0 + rows) of a unit without keys (one warp): O = 0, LSE = -inf.  Not inlined: the
+// kernel's code does not stay in the instruction cache, and these lines in the scheduler's loop
+// cost calls that never come here (12 mixed prompts 226 us instead of 223, two long ones 1785
+// instead of 1768).
+template <int D>
+__device__ __noinline__ void vl_store_blind(const VarlenParams &p, int head, int q0, int rows, int lane) {
+#pragma unroll 1
+    for (int h = head; h <= head + p.pair; ++h) {
+        uint8_t *o = static_cast<uint8_t *>(p.o) + h * p.o_head + q0 * p.o_row + lane % (D / 8) * 16;
+#pragma unroll 4
+        for (int r = lane / (D / 8); r < rows; r += 32 / (D / 8)) st_global_v4(o + r * p.o_row, 0u, 0u, 0u, 0u);
+        if (p.lse != nullptr)
+            for (int r = lane; r < rows; r += 32) p.lse[static_cast<size_t>(h) * p.total_q + q0 + r] = -INFINITY;
+    }
 }
 // First key tile that some row of the tile does not see whole.
 template <bool kCausal>
@@ -414,7 +429,7 @@ __global__ void __launch_bounds__(kWsThreads, 1)
         mbar_init(mma_done, 1);
         for (int s = 0; s < kVlSlots; ++s) {
             mbar_init(unit_full(s), 1);
-            mbar_init(unit_empty(s), kVlKeyRoles + 8);  // and 8 softmax warps
+            mbar_init(unit_empty(s), 11);  // producer, MMA issuer, guard, 8 softmax warps
         }
         fence_mbar_init();
     }
@@ -434,53 +449,47 @@ __global__ void __launch_bounds__(kWsThreads, 1)
         regs_dec<kRegsLow>();
         if (warp == 3) {
             // ---------------------------------------------------- scheduler
+            VlWalk<kCausal> walk{p, seqs, lane};
             int slot = 0;
             uint32_t phase = 0;
-            bool ok = true, keyless = false;  // keyless: some unit of this CTA has no keys
-            auto handed = [&]() {
-                if (lane == 0) mbar_arrive(unit_full(slot));
+            for (unsigned r = 0;; ++r) {
+                const unsigned c = (r & 1u) ? (gridDim.x - 1u - blockIdx.x) : blockIdx.x;
+                const unsigned t = r * gridDim.x + c;
+                int seq = 0, qb = 0;
+                const bool more =
+                    walk.find(static_cast<int>(t / static_cast<unsigned>(p.head_units)), seq, qb);
+                const int head = static_cast<int>(t % static_cast<unsigned>(p.head_units)) * (p.pair ? 2 : 1);
+                int q0 = 0, rows = 0, k0 = 0, nk = 0;
+                if (more) {
+                    const VlSpan q = vl_span(p.cu_q, seq, p.total_q), k = vl_span(p.cu_k, seq, p.total_k);
+                    q0 = q.a + qb * p.block_rows;
+                    rows = q.b - q0;
+                    k0 = k.a;
+                    nk = k.b - k.a;
+                    if (!vl_has_keys<kCausal>(p, rows, nk, nk - rows)) {
+                        vl_store_blind<D>(p, head, q0, rows < p.block_rows ? rows : p.block_rows, lane);
+                        continue;
+                    }
+                }
+                if (!__all_sync(0xffffffffu, wait_bar(unit_empty(slot), phase ^ 1u, p, abort_flag))) break;
+                if (lane == 0) {
+                    VlUnit &u = units[slot];
+                    u.valid = more ? 1 : 0;
+                    u.head = head;
+                    u.q0 = q0;
+                    u.rows = rows;
+                    u.k0 = k0;
+                    u.nk = nk;
+                    u.rel = nk - rows;
+                    u.bad = 0;
+                    mbar_arrive(unit_full(slot));
+                }
                 __syncwarp();
+                if (!more) break;
                 if (++slot == kVlSlots) {
                     slot = 0;
                     phase ^= 1u;
                 }
-            };
-#pragma unroll 1
-            for (int pass = 0; ok && (pass == 0 || (pass == 1 && keyless)); ++pass) {
-                VlWalk<kCausal> walk{p, seqs, lane};
-                bool ended = false;  // a unit without keys has been handed out
-                for (unsigned r = 0;; ++r) {
-                    const unsigned c = (r & 1u) ? (gridDim.x - 1u - blockIdx.x) : blockIdx.x;
-                    const unsigned t = r * gridDim.x + c;
-                    int seq = 0, qb = 0;
-                    if (!walk.find(static_cast<int>(t / static_cast<unsigned>(p.head_units)), seq, qb)) break;
-                    const VlSpan q = vl_span(p.cu_q, seq, p.total_q), k = vl_span(p.cu_k, seq, p.total_k);
-                    const int row0 = qb * p.block_rows, rows = q.b - q.a - row0, Nk = k.b - k.a;
-                    const int rel = Nk - rows;
-                    const bool keys = vl_has_keys<kCausal>(p, rows, Nk, rel);
-                    keyless |= !keys;
-                    if (keys != (pass == 0)) continue;
-                    if (!(ok = __all_sync(0xffffffffu, wait_bar(unit_empty(slot), phase ^ 1u, p, abort_flag)))) break;
-                    if (lane == 0) {
-                        VlUnit &u = units[slot];
-                        u.valid = 1;
-                        u.head = static_cast<int>(t % static_cast<unsigned>(p.head_units)) * (p.pair ? 2 : 1);
-                        u.q0 = q.a + row0;
-                        u.rows = rows;
-                        u.k0 = k.a;
-                        u.nk = Nk;
-                        u.rel = rel;
-                        u.bad = 0;
-                        if (ended)  // in place of the roles that have ended
-                            for (int e = 0; e < kVlKeyRoles; ++e) mbar_arrive(unit_empty(slot));
-                    }
-                    ended = pass == 1;
-                    handed();
-                }
-            }
-            if (ok && __all_sync(0xffffffffu, wait_bar(unit_empty(slot), phase ^ 1u, p, abort_flag))) {
-                if (lane == 0) units[slot].valid = 0;
-                handed();
             }
             // offsets that do not ascend within the tensors were read as clamped: say so
             if (blockIdx.x == 0) {
@@ -507,7 +516,7 @@ __global__ void __launch_bounds__(kWsThreads, 1)
                 for (int a = 0; a < D / 64; ++a)
                     tma_load_3d(dst + a * kAtomBytes, tm, 64 * a, head_y ? head : row, head_y ? row : head, bar);
             };
-            // the next unit (valid 0: no more units with keys)
+            // the next unit (valid 0: none); it has keys, as every unit that is handed out
             auto fetch = [&](Cur &c) -> bool {
                 if (!wait_bar(unit_full(slot), uphase, p, abort_flag)) return false;
                 const VlUnit &u = units[slot];
@@ -517,7 +526,6 @@ __global__ void __launch_bounds__(kWsThreads, 1)
                     c.n0 = t0.n;
                     c.n1 = t1.n;
                     c.n = t0.n > t1.n ? t0.n : t1.n;
-                    c.valid = c.n > 0;
                     c.q0 = u.q0;
                     c.q1 = u.q0 + t1.row0;
                     c.head = u.head;
@@ -615,7 +623,6 @@ __global__ void __launch_bounds__(kWsThreads, 1)
                     c.n0 = t0.n;
                     c.n1 = t1.n;
                     c.n = t0.n > t1.n ? t0.n : t1.n;
-                    c.valid = c.n > 0;
                     c.g0 = vl_first_masked<kCausal>(u, t0);
                 } else {
                     c.n0 = c.n1 = 0;
@@ -759,7 +766,6 @@ __global__ void __launch_bounds__(kWsThreads, 1)
                     slot = 0;
                     uphase ^= 1u;
                 }
-                if (n == 0) break;  // no more units with keys
             }
         }
         __syncwarp();

@@ -7,7 +7,6 @@ kernel's, it passes on that phase's parity alone, and the model checks that it w
 """
 
 SLOTS, STAGES = 4, 4  # kVlSlots, kStagesWs
-ROLES_WITH_KEYS = 3   # producer, MMA issuer, guard: they leave at the first unit without keys
 
 
 class Barrier:
@@ -70,11 +69,12 @@ def units_of_ctas(lens_q, lens_k, Hq, Hkv, causal, ctas):
 
 
 class Cta:
-    """Units (n0, n1, g0): key tiles of the two query tiles, first guarded key tile."""
+    """Units (n0, n1, g0): key tiles of the two query tiles, first guarded key tile.  With
+    ``hand_out_all`` those without keys go through the slots, too."""
 
-    def __init__(self, units, keys_first=True):
-        self.units = sorted(units, key=lambda u: max(u[:2]) == 0) if keys_first else list(units)
-        self.keys_first = keys_first
+    def __init__(self, units, hand_out_all=False):
+        self.blind = [] if hand_out_all else [u for u in units if max(u[:2]) == 0]  # stored by the scheduler
+        self.units = [u for u in units if hand_out_all or max(u[:2]) > 0]
         two = range(2)
         self.q_full = [Barrier(1) for _ in two]
         self.kv_full = [Barrier(1) for _ in range(STAGES)]
@@ -92,15 +92,10 @@ class Cta:
         self.scores = [[], []]          # (unit, key tile) of each score product
 
     def scheduler(self):
-        ended = False
         for t, u in enumerate(self.units + [0]):
             s = t % SLOTS
             yield self.unit_empty[s], t // SLOTS - 1
             self.slot[s] = 0 if u == 0 else (t, *u)
-            if u and max(u[:2]) == 0:
-                if ended:  # the roles that need keys have left
-                    self.unit_empty[s].arrive(ROLES_WITH_KEYS)
-                ended = self.keys_first
             self.unit_full[s].arrive()
 
     def fetch(self, at):
@@ -111,10 +106,8 @@ class Cta:
             u = self.slot[s]
             self.unit_empty[s].arrive()
             at += 1
-            if u == 0 or max(u[1:3]) > 0:
+            if u == 0 or max(u[1:3]) > 0:  # (always, where only units with keys are handed out)
                 return u, at
-            if self.keys_first:
-                return 0, at
 
     def producer(self):
         ring, at, scores = 0, 0, [0, 0]
@@ -220,8 +213,6 @@ class Cta:
                 tiles += 1
             self.unit_empty[s].arrive()
             at += 1
-            if self.keys_first and max(u[1:3]) == 0:
-                return
 
     def softmax(self, i):
         at, sn, on, j, n, cur, done = -1, 0, 0, 0, 0, None, None

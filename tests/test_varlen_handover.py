@@ -1,6 +1,6 @@
 """The hand-over of units in attn_fwd_varlen_kernel, on a model of its barriers: every role comes
-to its end whatever mix of units with and without keys a CTA gets, as it does not where a unit
-without keys may lie before one with keys."""
+to its end whatever mix of units with and without keys a CTA gets, as it does not where units
+without keys are handed out like the others."""
 import itertools
 import os
 import random
@@ -15,12 +15,13 @@ from handover_model import Cta, blocks_in_order, units_of_ctas
 KINDS = [(0, 0, 0), (1, 1, 0), (2, 2, 1), (0, 1, 0), (1, 0, 0), (2, 3, 1), (3, 3, 3)]
 
 
-def finishes(units, keys_first=True):
-    c = Cta(units, keys_first)
+def finishes(units, hand_out_all=False):
+    c = Cta(units, hand_out_all)
     done = c.run()
-    if done:  # every unit stored once by either tile, in the order of the list
+    if done:  # every unit stored once by either tile, in the order of the list, or by the scheduler
+        assert len(c.units) + len(c.blind) == len(units)
         for i in range(2):
-            assert [t for x, t in c.stored if x == i] == list(range(len(units)))
+            assert [t for x, t in c.stored if x == i] == list(range(len(c.units)))
             assert c.scores[i] == [(t, j) for t, u in enumerate(c.units) for j in range(u[i])]
     return done
 
@@ -30,8 +31,7 @@ def test_the_model_has_the_kernels_numbers():
         text = f.read()
     with open(os.path.join(build.CSRC, "attn_fwd_ws.cuh")) as f:
         text += f.read()
-    for name, value in (("kVlSlots", handover_model.SLOTS), ("kStagesWs", handover_model.STAGES),
-                        ("kVlKeyRoles", handover_model.ROLES_WITH_KEYS)):
+    for name, value in (("kVlSlots", handover_model.SLOTS), ("kStagesWs", handover_model.STAGES)):
         assert int(re.search(rf"constexpr int {name} = (\d+);", text).group(1)) == value
 
 
@@ -51,10 +51,10 @@ def test_long_lists_finish():
 
 @pytest.mark.parametrize("tiles,ends", [([3, 0, 0], True), ([3, 0, 0, 0], False), ([3, 2, 1, 0, 0, 0, 0], False),
                                         ([0, 0, 0, 0, 0, 0], True), ([1, 0, 0, 0, 1], False)])
-def test_the_order_matters(tiles, ends):
-    """A look ahead past units without keys, in the order of the levels, waits for its own slot."""
+def test_a_look_past_units_without_keys_does_not_end(tiles, ends):
+    """Handed out like the others, three of them behind a unit with keys make it wait for its own slot."""
     units = [(n, n, max(0, n - 1)) for n in tiles]
-    assert finishes(units, keys_first=False) == ends
+    assert finishes(units, hand_out_all=True) == ends
     assert finishes(units)
 
 
@@ -72,9 +72,9 @@ def test_calls_with_units_without_keys_finish(lens_q, lens_k, causal, Hq, Hkv):
     assert all(finishes(x) for x in lists)
 
 
-def test_the_order_of_levels_would_not_finish_them():
+def test_handing_out_all_units_would_not_finish_them():
     lists = units_of_ctas([8192], [512], 32, 8, True, 152)
-    assert sum(not finishes(x, keys_first=False) for x in lists) == 64
+    assert sum(not finishes(x, hand_out_all=True) for x in lists) == 64
 
 
 @pytest.mark.parametrize("causal", [True, False])
