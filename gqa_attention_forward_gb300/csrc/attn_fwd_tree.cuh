@@ -913,14 +913,21 @@ __device__ __forceinline__ void tree_merge_row(const TreeParams &p, int c0, int 
         const float wl = ls == -INFINITY ? 0.f : expf(ls - m_new);
         sum = sum * old + wl;  // of this lane's pieces
         mx = m_new;
+        // A weight (and a rebasing factor) that underflows to 0 drops the finite values of its piece
+        // only: an infinity or NaN there is one of a key that the row sees, and stays.
 #pragma unroll
-        for (int d = 0; d < kPer; ++d) acc[d] *= old;
+        for (int d = 0; d < kPer; ++d) acc[d] = old != 0.f || isfinite(acc[d]) ? acc[d] * old : acc[d];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const float w = __shfl_sync(0xffffffffu, wl, j);
-            if (s0 + j <= c1 && w != 0.f) {
+            if (s0 + j > c1) continue;
+            if (w != 0.f) {
 #pragma unroll
                 for (int d = 0; d < kPer; ++d) acc[d] += w * v[j][d];
+            } else {
+#pragma unroll
+                for (int d = 0; d < kPer; ++d)
+                    if (!isfinite(v[j][d])) acc[d] += v[j][d];
             }
         }
     }
