@@ -143,12 +143,19 @@ __global__ void __launch_bounds__(kPlanThreads) kv_extend_kernel(const KvPool c,
     for (int i = warp; i < n; i += kPlanThreads / 32) {
         int s, len, j0, j1, miss = 0;
         const bool fine = columns(i, s, len, j0, j1);
+        bool past = false;  // a page that the sequence has kept is none of the pool
         if (fine)
-            for (int j = j0 + lane; j < j1; j += 32) miss += kv_row(c, s)[j] < 0 ? 1 : 0;
+            for (int j = j0 + lane; j < j1; j += 32) {
+                const int p = kv_row(c, s)[j];
+                miss += p < 0 ? 1 : 0;
+                past |= p >= c.n_pages;
+            }
         miss = __reduce_add_sync(0xffffffffu, miss);
+        past = __any_sync(0xffffffffu, past);
         if (lane == 0) {
-            c.need[i] = miss;
-            if (!fine) kv_error(ATTN_ERR_SHAPE);
+            c.need[i] = past ? 0 : miss;
+            if (past) c.claim[s] = -1;  // refused: no request of the list
+            if (!fine || past) kv_error(fine ? ATTN_ERR_PAGE : ATTN_ERR_SHAPE);
         }
     }
     __syncthreads();

@@ -83,3 +83,27 @@ def test_fork_of_a_length_past_the_table():
         m.fork([1], [5])
         m.same(c)
         binding.kv_free(c, i32([5]))
+
+
+@pytest.mark.parametrize("seqs", [None, [0, 1, 2]])
+def test_extend_over_a_kept_page_out_of_range(seqs):
+    """A sequence ends before pages that it has kept (as after accepting a tree), one of which is
+    no page of the pool: refused, the others are served."""
+    page = 16
+    c = build([100, 20, 90], page, 2, 64, "f16", extra_pages=6, n_rows=5)
+    c.lens[0] = 30  # five pages of its seven are kept behind its end
+    s = None if seqs is None else i32(seqs)
+    for wrong in (c.n_pages, 10 ** 6, 2 ** 31 - 1):
+        good = int(c.table[0, 4])
+        c.table[0, 4] = wrong
+        m = Model(c)
+        binding.kv_extend(c, i32([60, 15, 7]), s)
+        assert status() == binding.ATTN_ERR_PAGE
+        m.extend([1, 2], [15, 7])
+        m.same(c)
+        binding.kv_extend(c, i32([34, 0, 0]), s)  # up to the page before it: served
+        m.extend([0], [34])
+        m.same(c)
+        assert status() == binding.ATTN_OK
+        c.table[0, 4] = good
+        c.lens[0] = 30
