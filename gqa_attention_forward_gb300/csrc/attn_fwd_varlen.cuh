@@ -31,8 +31,8 @@
 // producer, the issuer and the guard look one unit ahead, and the unit at work keeps its
 // descriptor slot until its last V tile, which the producer loads after that look: a look past
 // any number of units without keys would wait for slots that wait for it.  (Handing them out
-// behind the others, to the softmax warps alone, takes a second walk and 58.6 us instead of 40.6
-// for 8192 queries over 512 keys, Hq 32, D 128.)
+// behind the others, to the softmax warps alone, takes a second walk and 58.6 us instead of 37.7
+// for 8192 queries over 512 keys, Hq 32, D 128; not inlining the stores 67.1.)
 //
 // Roles (384 threads): warp 0 MMA issuer, warp 1 value guard (and TMEM), warp 2 TMA
 // producer, warp 3 scheduler, warps 4-7 and 8-11 the softmax of tile 0 and 1.  Shared memory,
@@ -134,20 +134,17 @@ template <bool kCausal>
 __device__ __forceinline__ bool vl_has_keys(const VarlenParams &p, int rows, int nk, int rel) {
     return nk > 0 && (!kCausal || rel + (rows < p.block_rows ? rows : p.block_rows) > 0);
 }
-// Rows [q0, q0 + rows) of a unit without keys (one warp): O = 0, LSE = -inf.  Not inlined: the
-// kernel's code does not stay in the instruction cache, and these lines in the scheduler's loop
-// cost calls that never come here (12 mixed prompts 226 us instead of 223, two long ones 1785
-// instead of 1768).
+// Rows of one head that see no key (one warp): O = 0, LSE = -inf.
 template <int D>
-__device__ __noinline__ void vl_store_blind(const VarlenParams &p, int head, int q0, int rows, int lane) {
-#pragma unroll 1
-    for (int h = head; h <= head + p.pair; ++h) {
-        uint8_t *o = static_cast<uint8_t *>(p.o) + h * p.o_head + q0 * p.o_row + lane % (D / 8) * 16;
+__device__ __forceinline__ void vl_store_blind(uint8_t *o, long long o_row, float *lse, int rows, int lane) {
+    o += lane / (D / 8) * o_row + lane % (D / 8) * 16;
 #pragma unroll 4
-        for (int r = lane / (D / 8); r < rows; r += 32 / (D / 8)) st_global_v4(o + r * p.o_row, 0u, 0u, 0u, 0u);
-        if (p.lse != nullptr)
-            for (int r = lane; r < rows; r += 32) p.lse[static_cast<size_t>(h) * p.total_q + q0 + r] = -INFINITY;
+    for (int r = lane / (D / 8); r < rows; r += 32 / (D / 8)) {
+        st_global_v4(o, 0u, 0u, 0u, 0u);
+        o += 32 / (D / 8) * o_row;
     }
+    if (lse != nullptr)
+        for (int r = lane; r < rows; r += 32) lse[r] = -INFINITY;
 }
 // First key tile that some row of the tile does not see whole.
 template <bool kCausal>
@@ -247,7 +244,8 @@ struct VlWalk {
 // The two products of a key tile, with the matrix descriptors of sdesc_sw128 put together in
 // the instruction's own block: the upper word is a constant, the lower one (start address and
 // leading offset, in 16-byte units) a base plus a constant, so that one register per operand is
-// live and nothing is hoisted out of the issuer's loop (hoisted descriptors spilled there).
+// live and no descriptors are hoisted out of the issuer's loop (there they spilled).  What the
+// kernel still spills is 12 bytes stored and 4 loaded at D = 128, 24 and 88 to 96 at D = 64, in all.
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // stride 1024 B, version 1, swizzle 128 B
 __device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo_bytes) {
     return ((saddr & 0x3FFFFu) >> 4) | ((lbo_bytes >> 4) << 16);
@@ -447,58 +445,7 @@ __global__ void __launch_bounds__(kWsThreads, 1)
 
     if (warp < 4) {
         regs_dec<kRegsLow>();
-        if (warp == 3) {
-            // ---------------------------------------------------- scheduler
-            VlWalk<kCausal> walk{p, seqs, lane};
-            int slot = 0;
-            uint32_t phase = 0;
-            for (unsigned r = 0;; ++r) {
-                const unsigned c = (r & 1u) ? (gridDim.x - 1u - blockIdx.x) : blockIdx.x;
-                const unsigned t = r * gridDim.x + c;
-                int seq = 0, qb = 0;
-                const bool more =
-                    walk.find(static_cast<int>(t / static_cast<unsigned>(p.head_units)), seq, qb);
-                const int head = static_cast<int>(t % static_cast<unsigned>(p.head_units)) * (p.pair ? 2 : 1);
-                int q0 = 0, rows = 0, k0 = 0, nk = 0;
-                if (more) {
-                    const VlSpan q = vl_span(p.cu_q, seq, p.total_q), k = vl_span(p.cu_k, seq, p.total_k);
-                    q0 = q.a + qb * p.block_rows;
-                    rows = q.b - q0;
-                    k0 = k.a;
-                    nk = k.b - k.a;
-                    if (!vl_has_keys<kCausal>(p, rows, nk, nk - rows)) {
-                        vl_store_blind<D>(p, head, q0, rows < p.block_rows ? rows : p.block_rows, lane);
-                        continue;
-                    }
-                }
-                if (!__all_sync(0xffffffffu, wait_bar(unit_empty(slot), phase ^ 1u, p, abort_flag))) break;
-                if (lane == 0) {
-                    VlUnit &u = units[slot];
-                    u.valid = more ? 1 : 0;
-                    u.head = head;
-                    u.q0 = q0;
-                    u.rows = rows;
-                    u.k0 = k0;
-                    u.nk = nk;
-                    u.rel = nk - rows;
-                    u.bad = 0;
-                    mbar_arrive(unit_full(slot));
-                }
-                __syncwarp();
-                if (!more) break;
-                if (++slot == kVlSlots) {
-                    slot = 0;
-                    phase ^= 1u;
-                }
-            }
-            // offsets that do not ascend within the tensors were read as clamped: say so
-            if (blockIdx.x == 0) {
-                bool bad = false;
-                for (int s = lane; s < p.n_seqs; s += 32)
-                    bad |= vl_span(p.cu_q, s, p.total_q).bad || vl_span(p.cu_k, s, p.total_k).bad;
-                if (bad) atomicCAS(&g_error_code, 0, static_cast<int>(ATTN_ERR_SHAPE));
-            }
-        } else if (warp == 2 && lane == 0) {
+        if (warp == 2 && lane == 0) {
             // ---------------------------------------------------- TMA producer
             // The ring holds K_0, then V_j and the K tile after it (K_{j+1}, or the next unit's
             // K_0) in pairs that complete V_j's barrier together, so that the issuer waits once
@@ -766,6 +713,60 @@ __global__ void __launch_bounds__(kWsThreads, 1)
                     slot = 0;
                     uphase ^= 1u;
                 }
+            }
+        } else if (warp == 3) {
+            // ---------------------------------------------------- scheduler
+            VlWalk<kCausal> walk{p, seqs, lane};
+            int slot = 0;
+            uint32_t phase = 0;
+            for (unsigned r = 0;; ++r) {
+                const unsigned c = (r & 1u) ? (gridDim.x - 1u - blockIdx.x) : blockIdx.x;
+                const unsigned t = r * gridDim.x + c;
+                int seq = 0, qb = 0;
+                const bool more =
+                    walk.find(static_cast<int>(t / static_cast<unsigned>(p.head_units)), seq, qb);
+                const int head = static_cast<int>(t % static_cast<unsigned>(p.head_units)) * (p.pair ? 2 : 1);
+                int q0 = 0, rows = 0, k0 = 0, nk = 0;
+                if (more) {
+                    const VlSpan q = vl_span(p.cu_q, seq, p.total_q), k = vl_span(p.cu_k, seq, p.total_k);
+                    q0 = q.a + qb * p.block_rows;
+                    rows = q.b - q0;
+                    k0 = k.a;
+                    nk = k.b - k.a;
+                    if (!vl_has_keys<kCausal>(p, rows, nk, nk - rows)) {
+                        for (int h = head; h <= head + p.pair; ++h)
+                            vl_store_blind<D>(static_cast<uint8_t *>(p.o) + h * p.o_head + q0 * p.o_row, p.o_row,
+                                              p.lse ? p.lse + static_cast<size_t>(h) * p.total_q + q0 : nullptr,
+                                              rows < p.block_rows ? rows : p.block_rows, lane);
+                        continue;
+                    }
+                }
+                if (!__all_sync(0xffffffffu, wait_bar(unit_empty(slot), phase ^ 1u, p, abort_flag))) break;
+                if (lane == 0) {
+                    VlUnit &u = units[slot];
+                    u.valid = more ? 1 : 0;
+                    u.head = head;
+                    u.q0 = q0;
+                    u.rows = rows;
+                    u.k0 = k0;
+                    u.nk = nk;
+                    u.rel = nk - rows;
+                    u.bad = 0;
+                    mbar_arrive(unit_full(slot));
+                }
+                __syncwarp();
+                if (!more) break;
+                if (++slot == kVlSlots) {
+                    slot = 0;
+                    phase ^= 1u;
+                }
+            }
+            // offsets that do not ascend within the tensors were read as clamped: say so
+            if (blockIdx.x == 0) {
+                bool bad = false;
+                for (int s = lane; s < p.n_seqs; s += 32)
+                    bad |= vl_span(p.cu_q, s, p.total_q).bad || vl_span(p.cu_k, s, p.total_k).bad;
+                if (bad) atomicCAS(&g_error_code, 0, static_cast<int>(ATTN_ERR_SHAPE));
             }
         }
         __syncwarp();
