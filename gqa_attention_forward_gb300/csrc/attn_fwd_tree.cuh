@@ -20,8 +20,9 @@
 //     more than it has, about what its change costs.  A unit cut by a share's border leaves
 //     at most two pieces per CTA (fp32 O and log-sum-exp), merged by a second, dependent
 //     launch; the others write O themselves.  (Merging in the CTA that brings the last piece
-//     saves the launch, but its round trips come one after another: one token over 4000
-//     positions 22.8 us instead of 16.5, 16 tokens over 32760 positions 86 instead of 47.);
+//     saves the launch, but its round trips come one after another: when it was tried, one token
+//     over 4000 positions took 22.8 us that way and about 16 in two launches, 16 tokens over 32760
+//     positions 86 and 47; the two launches, captured, take 12.9 and 33.5 by now.);
 //   * the load order runs on across the units of a share: the next unit's first K tile is
 //     loaded, and its scores computed, before the last P V of the unit before, the page
 //     indexes of the next unit and of the next 32 pages are fetched ahead, and O has two

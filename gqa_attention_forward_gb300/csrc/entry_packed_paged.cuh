@@ -188,7 +188,8 @@ attn_status_t check_list(const attn_kv_cache_t *c, int n, bool &empty) {
 
 // Grid of kv_move_kernel: its warps' 4 KB segments, at most 32 blocks of 8 warps per SM; more
 // blocks than are resident at once keep the memory busier than a loop in each of few (a 600 MB
-// compaction: 207 us with 2 or 4 blocks per SM, 199 with 8, 194 with 16).
+// compaction, the ranges of three runs: 198 to 208 us with 8 blocks per SM, 191 to 201 with 16, 193
+// to 195 with 32, 192 to 197 with 64).
 unsigned move_grid(const gqa::KvPool &p, long long pages, int sms) {
     const long long segs = pages * p.n_layers * 2 * p.Hkv * ((p.page * p.row16 + 255) / 256);
     const long long blocks = (segs + 7) / 8, most = 32ll * sms;

@@ -277,6 +277,11 @@ attn_status_t attn_fwd_host(const void *q_h, const void *k_h, const void *v_h, v
  *         k row, k head, v row, v head, o row, o head}, each a multiple of 8 and at
  *         least D, the larger of a pair a multiple of the smaller and no two rows
  *         overlapping ([heads, rows, D], or heads cut from one projection's output)
+ * Rounding: the weights are rounded once to the input type, half a step of each: o is off by
+ *         at most u |o| + u sum_j p_j |v_j| and fp32 terms (u 2^-8 for bf16, 2^-11 for fp16;
+ *         for fp16 2^-25 |v_j| more for each weight below 2^-14, the smallest normal number).
+ *         attn_fwd and attn_fwd_kv keep a second term of the weights where a row's sum is
+ *         small, and come nearer there; lse is fp32 in all of them.
  * Limits: total_q and total_k at most 65535 * 128.
  * Errors: as attn_fwd_kv (no error for Nq_s > Nk_s); ATTN_ERR_SHAPE for strides.
  *         Offsets that descend or leave the tensors are clamped, with no more work done
@@ -329,9 +334,10 @@ attn_status_t attn_kv_extend(const attn_kv_cache_t *cache, const int *seqs, cons
 /* Writes the keys and values of new tokens into their pages of one layer.  Packed rows
  * [cu[i], cu[i+1]) of k_new, v_new [total, Hkv, D] are the last positions of sequence
  * seqs[i] (i, when NULL), whose lens already counts them (attn_kv_extend).  strides: NULL,
- * or 4 element strides {k row, k head, v row, v head}, multiples of 8.  A page that
- * another sequence shares is not written (ATTN_ERR_PAGE), nor the rows of a sequence that
- * was named before in the list (ATTN_ERR_SHAPE). */
+ * or 4 element strides {k row, k head, v row, v head}, multiples of 8.  Rows whose page is
+ * missing, out of range or shared with another sequence are not written (ATTN_ERR_PAGE; the
+ * sequence's other rows are), nor the rows of a sequence that was named before in the list
+ * (ATTN_ERR_SHAPE). */
 attn_status_t attn_kv_append(const attn_kv_cache_t *cache, int layer, const void *k_new,
                              const void *v_new, const long long *strides, const int *cu,
                              const int *seqs, int n, int total, void *stream);
@@ -359,7 +365,8 @@ attn_status_t attn_kv_fork(const attn_kv_cache_t *cache, const int *parents, con
                            int n, void *stream);
 
 /* Empties the sequences: one reference less for each of their pages.  A sequence may be
- * named twice. */
+ * named twice.  Entries of its row that name no page of the pool, or one that has no
+ * references, are dropped with the others (ATTN_ERR_PAGE). */
 attn_status_t attn_kv_free(const attn_kv_cache_t *cache, const int *seqs, int n, void *stream);
 
 /* Moves the live pages to the front of the pool, so that they are pages 0 .. live - 1: the
@@ -390,7 +397,7 @@ attn_status_t attn_kv_compact(const attn_kv_cache_t *cache, int *live, void *str
  *           value.  Calls that can run at the same time must not share it.
  * Rows behind the last tree are left as they are.  Rows of a page past the sequence's end
  * may hold anything; a non-finite value of V at a tree's position reaches exactly the tokens
- * that see it.
+ * that see it, and one before the tree all of them.  Rounding as in attn_fwd_varlen.
  * Errors: as attn_fwd_kv, ATTN_ERR_SHAPE for Hq / Hkv > 128, ATTN_ERR_SCRATCH for a small
  * workspace; attn_last_device_error reports a tree of more than 128 tokens or of more than
  * the sequence's positions and bad offsets or sequences (ATTN_ERR_SHAPE), whose rows are then

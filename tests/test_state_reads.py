@@ -10,6 +10,8 @@ import pytest
 import torch
 
 from gqa_attention_forward_gb300 import binding, build
+from paged_util import Model
+from paged_util import build as build_cache
 
 
 def test_no_read_only_loads():
@@ -77,3 +79,34 @@ def test_calls_without_a_pause(page, ctx):
 
     for a, b in zip(loop(True), loop(False)):
         assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+def test_captured_fork_free_and_compaction():
+    """A beam step captured once and replayed: the losers are freed, the winners forked into their
+    place, the pool made dense; each replay goes on from the state of the one before."""
+    page = 16
+    c = build_cache([70, 33, 48, 5, 90], page, 2, 64, "bf16", 2, extra_pages=40, n_rows=8)
+    m = Model(c)
+
+    def i32(x):
+        return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+    losers, winners = i32([3, 4]), i32([0, 1])
+    live = torch.zeros(1, dtype=torch.int32, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        binding.kv_free(c, losers)
+        binding.kv_fork(c, winners, losers)
+        binding.kv_compact(c, live)
+    for lose, win in (([3, 4], [0, 1]), ([0, 1], [2, 2]), ([2, 7], [4, 1]), ([4, 0], [3, 7])):
+        losers.copy_(i32(lose))
+        winners.copy_(i32(win))
+        g.replay()
+        torch.cuda.synchronize()
+        m.free(lose)
+        m.fork(win, lose)
+        assert int(live) == m.compact()
+        m.same(c)
+        m.consistent()
+    assert binding.attn_last_device_error(torch.cuda.current_stream()) == binding.ATTN_OK
