@@ -76,11 +76,17 @@ def load(path: str | None = None):
         lib.attn_fwd_varlen.argtypes = [vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, vp,
                                         ctypes.c_float, i, i, vp]
         lib.attn_fwd_varlen.restype = i
+        lib.attn_fwd_varlen_window.argtypes = [vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, vp,
+                                               ctypes.c_float, i, i, i, vp]
+        lib.attn_fwd_varlen_window.restype = i
         lib.attn_fwd_tree_workspace.argtypes = [i, i, ctypes.POINTER(sz)]
         lib.attn_fwd_tree_workspace.restype = i
         lib.attn_fwd_tree.argtypes = [vp, pc, i, vp, vp, vp, vp, vp, i, i, i, vp, ctypes.c_float, vp,
                                       sz, vp]
         lib.attn_fwd_tree.restype = i
+        lib.attn_fwd_tree_window.argtypes = [vp, pc, i, vp, vp, vp, vp, vp, i, i, i, vp, ctypes.c_float,
+                                             i, i, vp, sz, vp]
+        lib.attn_fwd_tree_window.restype = i
         lib.attn_kv_scratch.argtypes = [i, i, ctypes.POINTER(sz)]
         lib.attn_kv_scratch.restype = i
         lib.attn_kv_extend.argtypes = [pc, vp, vp, i, vp]
@@ -355,6 +361,16 @@ def attn_fwd_varlen(q, k, v, o, lse, cu_q, cu_k, n_seqs, total_q, total_k, Hq, H
                                   _stream_handle(stream))
 
 
+def attn_fwd_varlen_window(q, k, v, o, lse, cu_q, cu_k, n_seqs, total_q, total_k, Hq, Hkv, D, strides, scale,
+                           window, sinks, dtype, stream=None) -> int:
+    """The C entry point with the same name; returns its status code.  ``strides``:
+    None or 8 element strides."""
+    return load().attn_fwd_varlen_window(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(cu_q), _ptr(cu_k),
+                                         int(n_seqs), int(total_q), int(total_k), int(Hq), int(Hkv), int(D),
+                                         _strides(strides), float(scale), int(window), int(sinks),
+                                         _dtype_code(dtype), _stream_handle(stream))
+
+
 _torch_module = None
 
 
@@ -441,14 +457,28 @@ def _outputs(q, dev, Hq, total, with_lse, out, lse_out, stream):
     return out, lse_out
 
 
+def _window(window, sinks):
+    """The window and the first keys as C ints (a longer window than an int holds has no end either)."""
+    if window is None:
+        if sinks != 0:
+            raise ValueError("sinks are the first keys that a window leaves visible: they need a window")
+        return None, 0
+    return min(int(window), 0x7FFFFFFF), min(int(sinks), 0x7FFFFFFF)
+
+
 def attention_varlen(q, k, v, cu_q, cu_k=None, causal: bool = True, scale: float | None = None,
-                     with_lse: bool = True, out=None, lse_out=None, stream=None):
+                     with_lse: bool = True, out=None, lse_out=None, stream=None, window: int | None = None,
+                     sinks: int = 0):
     """attn_fwd_varlen for torch CUDA tensors q [total_q,Hq,D], k/v [total_k,Hkv,D] (any row and
     head strides that the C entry point takes, e.g. heads cut from one projection's output).
 
     ``cu_q`` (and ``cu_k`` where the keys' offsets differ): int32 [n_seqs + 1] offsets on the
-    device, never read by the host.  Returns (o [total_q,Hq,D], lse [Hq,total_q]) without waiting;
-    rows behind the last sequence are not written."""
+    device, never read by the host.  ``window``, ``sinks``: attn_fwd_varlen_window (each row sees the
+    last ``window`` keys up to its own and the first ``sinks``).  Returns (o [total_q,Hq,D],
+    lse [Hq,total_q]) without waiting; rows behind the last sequence are not written."""
+    window, sinks = _window(window, sinks)
+    if window is not None and not causal:
+        raise ValueError("a window is causal")
     shape, sq = _rows(q, "q")
     kshape, sk = _rows(k, "k")
     vshape, sv = _rows(v, "v")
@@ -468,10 +498,17 @@ def attention_varlen(q, k, v, cu_q, cu_k=None, causal: bool = True, scale: float
     so = o.stride()
     if so[2] != 1:
         raise ValueError("out must have its last axis contiguous")
-    _run("attn_fwd_varlen", dev, stream, load().attn_fwd_varlen, q.data_ptr(), k.data_ptr(), v.data_ptr(),
-         o.data_ptr(), _ptr(lse), cu_q.data_ptr(), _ptr(cu_k), cu_q.numel() - 1, total_q, total_k, Hq, Hkv, D,
-         _Strides8(sq[0], sq[1], sk[0], sk[1], sv[0], sv[1], so[0], so[1]),
-         D ** -0.5 if scale is None else scale, 1 if causal else 0, _dtype_code(dtype))
+    strides = _Strides8(sq[0], sq[1], sk[0], sk[1], sv[0], sv[1], so[0], so[1])
+    if scale is None:
+        scale = D ** -0.5
+    if window is None:
+        _run("attn_fwd_varlen", dev, stream, load().attn_fwd_varlen, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+             o.data_ptr(), _ptr(lse), cu_q.data_ptr(), _ptr(cu_k), cu_q.numel() - 1, total_q, total_k, Hq, Hkv, D,
+             strides, scale, 1 if causal else 0, _dtype_code(dtype))
+    else:
+        _run("attn_fwd_varlen_window", dev, stream, load().attn_fwd_varlen_window, q.data_ptr(), k.data_ptr(),
+             v.data_ptr(), o.data_ptr(), _ptr(lse), cu_q.data_ptr(), _ptr(cu_k), cu_q.numel() - 1, total_q, total_k,
+             Hq, Hkv, D, strides, scale, window, sinks, _dtype_code(dtype))
     return o, lse
 
 
@@ -593,6 +630,16 @@ def attn_fwd_tree(q, cache, layer, o, lse, cu, seqs, parents, n_seqs, total_q, H
                                 float(scale), _ptr(workspace), int(workspace_bytes), _stream_handle(stream))
 
 
+def attn_fwd_tree_window(q, cache, layer, o, lse, cu, seqs, parents, n_seqs, total_q, Hq, strides, scale, window,
+                         sinks, workspace, workspace_bytes, stream=None) -> int:
+    """The C entry point with the same name; returns its status code.  ``strides``: None or 4
+    element strides."""
+    return load().attn_fwd_tree_window(_ptr(q), _c(cache), int(layer), _ptr(o), _ptr(lse), _ptr(cu), _ptr(seqs),
+                                       _ptr(parents), int(n_seqs), int(total_q), int(Hq), _strides(strides),
+                                       float(scale), int(window), int(sinks), _ptr(workspace), int(workspace_bytes),
+                                       _stream_handle(stream))
+
+
 def _list(t, name, cache, n=None):
     """Checks an int32 list on the cache's device (None is taken); returns its length."""
     if t is None:
@@ -673,14 +720,17 @@ _tree_bytes = {}  # (device number, sequences, D) -> bytes of attn_fwd_tree_work
 
 
 def attention_tree(q, cache, cu, seqs=None, parents=None, layer: int = 0, scale: float | None = None,
-                   with_lse: bool = True, workspace=None, out=None, lse_out=None, stream=None):
+                   with_lse: bool = True, workspace=None, out=None, lse_out=None, stream=None,
+                   window: int | None = None, sinks: int = 0):
     """attn_fwd_tree: q [total,Hq,D] holds the queries of each sequence's last tokens (offsets
     ``cu`` [n + 1]), which form a tree by ``parents`` (None: a chain; one token each: a decoding
-    step), over a KVPages ``cache``.
+    step), over a KVPages ``cache``.  ``window``, ``sinks``: attn_fwd_tree_window (each token sees the
+    last ``window`` positions up to its own and the first ``sinks``).
 
     ``workspace``: a uint8 CUDA tensor, or None to let torch allocate the size that
     attn_fwd_tree_workspace asks for.  Returns (o [total,Hq,D], lse [Hq,total]) without waiting."""
     torch = _torch()
+    window, sinks = _window(window, sinks)
     (total, Hq, D), sq = _rows(q, "q")
     dev = cache.dev
     _same(q, "q", cache.dtype, dev)
@@ -707,7 +757,15 @@ def attention_tree(q, cache, cu, seqs=None, parents=None, layer: int = 0, scale:
         _same(workspace, "workspace", torch.uint8, dev)
         if not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
-    _run("attn_fwd_tree", dev, stream, load().attn_fwd_tree, q.data_ptr(), cache.ref, layer, o.data_ptr(),
-         _ptr(lse), cu.data_ptr(), _ptr(seqs), _ptr(parents), n, total, Hq, _Strides4(sq[0], sq[1], so[0], so[1]),
-         D ** -0.5 if scale is None else scale, workspace.data_ptr(), nbytes)
+    strides = _Strides4(sq[0], sq[1], so[0], so[1])
+    if scale is None:
+        scale = D ** -0.5
+    if window is None:
+        _run("attn_fwd_tree", dev, stream, load().attn_fwd_tree, q.data_ptr(), cache.ref, layer, o.data_ptr(),
+             _ptr(lse), cu.data_ptr(), _ptr(seqs), _ptr(parents), n, total, Hq, strides, scale, workspace.data_ptr(),
+             nbytes)
+    else:
+        _run("attn_fwd_tree_window", dev, stream, load().attn_fwd_tree_window, q.data_ptr(), cache.ref, layer,
+             o.data_ptr(), _ptr(lse), cu.data_ptr(), _ptr(seqs), _ptr(parents), n, total, Hq, strides, scale, window,
+             sinks, workspace.data_ptr(), nbytes)
     return o, lse

@@ -57,6 +57,7 @@ constexpr int kTreeSeqs = 2048;    // most sequences of one launch (their length
 // 182.5 / 178.7, 12288 rows 46.2 / 41.8, 16384 rows 28.3 / 15.6, 32768 rows 88.7 / 66.4.
 constexpr int kMergeRows = 6144, kMergeCtaThreads = 128, kMergeCtaRows = 8;
 constexpr int kTreeBadTiles = 2;   // the tree's positions lie in at most two key tiles
+constexpr int kTreeBadTilesWin = 8;  // and a window's start in two, the end of the first keys in one
 
 struct TreeParams : Params {
     const int *cu, *table, *lens, *seqs, *parents;
@@ -66,6 +67,7 @@ struct TreeParams : Params {
     int page, page_shift, n_pages, table_w;
     int rt;                    // tokens per row tile: 128 / group
     int min_share;             // least weight of a CTA's share
+    int window, sinks;         // window kernels: position pos sees j <= pos with j > pos - window or j < sinks
     long long o_row, o_head;   // strides in bytes
     float *part_o;             // [2 * CTAs][128][D]
     float *part_lse;           // [2 * CTAs][128]
@@ -88,7 +90,7 @@ struct TreeUnit {
     int piece;    // -1: the whole unit; 0, 1: piece slot of this CTA
     int first;    // packed row of the tree's first token
     int bad;      // set by the guard: some bad_rows bit is set
-    uint32_t bad_rows[kTreeBadTiles][4];
+    uint32_t bad_rows[kTreeBadTilesWin][4];
 };
 
 template <int D>
@@ -137,7 +139,19 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeParams &p, int s) {
     return r;
 }
 __device__ __forceinline__ int tree_row_tiles(const TreeParams &p, int T) { return (T + p.rt - 1) / p.rt; }
-__device__ __forceinline__ int tree_key_tiles(int L) { return L > 0 ? (L + kBN - 1) / kBN : 1; }
+// Key tiles of a unit: all of the sequence's, or with a window those of the first keys and of the
+// window of the tree's first token (win_skip).
+__device__ __forceinline__ int tree_base(int T, int L) { return L > T ? L - T : 0; }
+template <bool kWindow>
+__device__ __forceinline__ int tree_key_tiles(const TreeParams &p, int T, int L) {
+    int n = L > 0 ? (L + kBN - 1) / kBN : 1;
+    if constexpr (kWindow) n -= win_skip(tree_base(T, L), p.window, p.sinks);
+    return n > 1 ? n : 1;
+}
+// Tiles that every token of a tree sees whole; the others pass the guard (window kernels).
+__device__ __forceinline__ WinWhole tree_whole(const TreeParams &p, int T, int base) {
+    return win_whole(base, base, base + T - 1, p.window, p.sinks, win_skip(base, p.window, p.sinks));
+}
 
 // 128 bits as two words.
 struct Bits128 {
@@ -168,8 +182,9 @@ __device__ __forceinline__ Bits128 bits_shr(Bits128 b, int n) {
 __device__ __forceinline__ int tree_unit_weight(int key_tiles) { return key_tiles + 2; }
 
 // Weight of sequence s in the list of units.
+template <bool kWindow>
 __device__ __forceinline__ int tree_seq_weight(const TreeParams &p, int T, int L) {
-    return p.Hkv * tree_row_tiles(p, T) * tree_unit_weight(tree_key_tiles(L));
+    return p.Hkv * tree_row_tiles(p, T) * tree_unit_weight(tree_key_tiles<kWindow>(p, T, L));
 }
 __device__ __forceinline__ int tree_share(const TreeParams &p, int total) {
     const int share = (total + p.grid - 1) / p.grid;
@@ -190,14 +205,37 @@ __device__ __forceinline__ Bits128 tree_ancestors(int t, F par) {
     return anc;
 }
 
+// With a window: of those ancestors the token's nearest `window` (itself among them) and those
+// whose position is one of the first keys.  `depth` gets the token's: its position is base + depth.
+template <typename F>
+__device__ __forceinline__ Bits128 tree_window(int t, int base, int window, int sinks, int &depth, F par) {
+    depth = -1;
+    for (int u = t; u >= 0 && u < kTreeMax; ++depth) {
+        const int up = par(u);
+        u = up < u ? up : -1;
+    }
+    Bits128 anc{0ull, 0ull};
+    int d = depth;
+    for (int u = t; u >= 0 && u < kTreeMax; --d) {
+        if (depth - d < window || base + d < sinks) {
+            if (u < 64) anc.lo |= 1ull << u; else anc.hi |= 1ull << (u - 64);
+        }
+        const int up = par(u);
+        u = up < u ? up : -1;
+    }
+    return anc;
+}
+
+// kWindow: attn_fwd_tree_window.
 // tmQ: 3-D tensor map (D, Hq, tokens), box 64 x G x (128 / G); tmK, tmV: 3-D maps
 // (D, page, n_pages * Hkv), box 64 x min(page, 128) x 1; all with the 128-byte swizzle.
-template <int D, bool kBF16>
+template <int D, bool kBF16, bool kWindow>
 __global__ void __launch_bounds__(kTreeThreads, 1)
     attn_fwd_tree_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                          const __grid_constant__ CUtensorMap tmV, const __grid_constant__ TreeParams p) {
     using L = TreeLayout<D>;
     constexpr int S = L::kStages;
+    constexpr int kBad = kWindow ? kTreeBadTilesWin : kTreeBadTiles;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -268,7 +306,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 
     if (warp == 3) {
         // -------------------------------------------------------- scheduler, and Q
-        auto weight_of = [&](int s) -> int { return s < p.n_seqs ? tree_seq_weight(p, seqs[s].x, seqs[s].y) : 0; };
+        auto weight_of = [&](int s) -> int { return s < p.n_seqs ? tree_seq_weight<kWindow>(p, seqs[s].x, seqs[s].y) : 0; };
         auto scan = [&](int x) {  // inclusive prefix sum over the lanes
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -322,7 +360,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                         }
                         before += all;
                     }
-                    nt = tree_key_tiles(seqs[seq].y);
+                    nt = tree_key_tiles<kWindow>(p, seqs[seq].x, seqs[seq].y);
                     const int uw = tree_unit_weight(nt);
                     unit = in_seq / uw;  // kv head * row tiles + row tile
                     // weights [0, uw - nt) of a unit are its change, then come its tiles; a share that
@@ -338,7 +376,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 if (more) {
                     const TreeSeq q = tree_seq(p, seq);
                     const int mt = tree_row_tiles(p, q.T), t0 = (unit % mt) * p.rt;
-                    if (lane < kTreeBadTiles * 4) u.bad_rows[lane >> 2][lane & 3] = 0;
+                    if (lane < kBad * 4) u.bad_rows[lane >> 2][lane & 3] = 0;
                     if (lane == 0) {
                         u.valid = 1;
                         u.t0 = t0;
@@ -346,7 +384,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                         u.ntok = q.T - t0 < p.rt ? q.T - t0 : p.rt;
                         u.T = q.T;
                         u.L = q.L;
-                        u.base = q.L > q.T ? q.L - q.T : 0;
+                        u.base = tree_base(q.T, q.L);
                         u.row = q.row;
                         u.kvh = unit / mt;
                         u.k0 = k0;
@@ -404,11 +442,20 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             int valid, row, kvh, k0, k1, pages;
             int win;           // first entry of window a; b holds the 32 after it
             int ent_a, ent_b;
+            int skip;
+        };
+        // With an attention window the entries are those of the unit's steps, 128 / page (at least 1) of
+        // each: entry i is that of page step_page(skip, i).
+        const int per_tile = kBN / box_rows, per_shift = p.page < kBN ? 7 - p.page_shift : 0;
+        auto step_page = [&](int skip, int i) -> int {
+            if constexpr (!kWindow) return i;
+            return ((win_key_tile<kWindow>(i >> per_shift, p.sinks, skip) << 7) >> p.page_shift) + (i & (per_tile - 1));
         };
         int slot = 0;
         uint32_t uphase = 0;
         auto entry = [&](const Cur &c, int i) -> int {
-            return c.row >= 0 && i < c.pages ? p.table[static_cast<long long>(c.row) * p.table_w + i] : -1;
+            const int x = step_page(c.skip, i);
+            return c.row >= 0 && x < c.pages ? p.table[static_cast<long long>(c.row) * p.table_w + x] : -1;
         };
         auto take = [&](Cur &c) {  // the descriptor in the slot has arrived
             const TreeUnit &u = units[slot];
@@ -419,7 +466,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 c.k0 = u.k0;
                 c.k1 = u.k1;
                 c.pages = (u.L + p.page - 1) >> p.page_shift;
-                c.win = ((c.k0 << 7) >> p.page_shift) & ~31;
+                c.skip = kWindow ? win_skip(u.base, p.window, p.sinks) : 0;
+                c.win = (kWindow ? c.k0 << per_shift : (c.k0 << 7) >> p.page_shift) & ~31;
                 c.ent_a = entry(c, c.win + lane);
                 c.ent_b = entry(c, c.win + 32 + lane);
             }
@@ -453,7 +501,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                         of_next = true;
                         t = nxt.k0;
                     }
-                    const int first = (t << 7) >> p.page_shift;
+                    const int first = kWindow ? t << per_shift : (t << 7) >> p.page_shift;
                     // V is the last to use a window: the one after the next is fetched when V leaves it
                     if (h == 1 && first >= cur.win + 32) {
                         cur.win += 32;
@@ -472,12 +520,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                     int e = at < 32 ? ea : eb;
                     if (lane < boxes) {
                         if (e < 0 || e >= p.n_pages) {
-                            if (first + piece < (of_next ? nxt.pages : cur.pages))
+                            if (step_page(of_next ? nxt.skip : cur.skip, first + piece) < (of_next ? nxt.pages : cur.pages))
                                 atomicCAS(&g_error_code, 0, static_cast<int>(ATTN_ERR_PAGE));
                             e = -1;
                         }
                         tma_load_3d(dst + a * kAtomBytes + piece * box_rows * 128, h == 1 ? &tmV : &tmK, 64 * a,
-                                    (t << 7) & (p.page - 1), e < 0 ? oob : e * p.Hkv + (of_next ? nxt.kvh : cur.kvh),
+                                    (win_key_tile<kWindow>(t, p.sinks, of_next ? nxt.skip : cur.skip) << 7) & (p.page - 1),
+                                    e < 0 ? oob : e * p.Hkv + (of_next ? nxt.kvh : cur.kvh),
                                     kv_full(stage));
                     }
                     ++loads;
@@ -506,6 +555,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             uint32_t qn = 0, un = 0, vph = 0;                // Q tiles, units, phases of v_ok
             struct Cur {
                 int valid, k0, k1, guard;
+                WinWhole w;  // with a window: all but these tiles pass the guard
             };
             auto fetch = [&](Cur &c) -> bool {
                 if (!wait_bar(unit_full(slot), uphase, p, abort_flag)) return false;
@@ -514,7 +564,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 if (c.valid) {
                     c.k0 = u.k0;
                     c.k1 = u.k1;
-                    c.guard = u.base / kBN;  // tiles from here on pass the guard
+                    if constexpr (kWindow) c.w = tree_whole(p, u.T, u.base);
+                    else c.guard = u.base / kBN;  // tiles from here on pass the guard
                 }
                 mbar_arrive(unit_empty(slot));
                 if (++slot == kTreeSlots) {
@@ -525,7 +576,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             };
             // Per key tile: the scores of the tile after it (the next unit's first one, behind the
             // last), then its P V; before the first unit a step without P V.
-            Cur cur{1, 0, 1, 0}, nxt{};
+            Cur cur{1, 0, 1, 0, {0, 0, 0}}, nxt{};
             bool ok = true, start = true;
             while (ok && cur.valid) {
                 for (int kt = cur.k0; kt < cur.k1; ++kt) {
@@ -551,7 +602,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                     // one waits until the O of the unit before the last has been read
                     const uint32_t b = pj & 1u, ob = un & 1u;
                     if (!(ok = wait_bar(kv_full(stage), phase, p, abort_flag))) break;
-                    if (kt >= cur.guard) {
+                    if (kWindow ? !cur.w(kt) : kt >= cur.guard) {
                         if (!(ok = wait_bar(v_ok(stage), (vph >> stage) & 1u, p, abort_flag))) break;
                         vph ^= 1u << stage;
                     }
@@ -592,14 +643,23 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             }
             return true;
         };
-        // the next tile: waits for it, lets the guard work on a V tile, releases the stage
-        auto pass = [&](TreeUnit *u, int kt, int guard) -> bool {
+        // the next tile: waits for it, lets the guard work on a V tile (key tile kt, the g-th guarded one of
+        // the unit), releases the stage
+        auto pass = [&](TreeUnit *u, int kt, int g) -> bool {
             if (!__all_sync(0xffffffffu, wait_bar(kv_full(stage), phase, p, abort_flag))) return false;
             if (u != nullptr) {
                 int left = u->L - kt * kBN;
                 left = left < 0 ? 0 : (left < kBN ? left : kBN);
+                // a token alone sees the keys outside [z0, z1) of a tile on the window's border, as all its heads do
+                int z0 = 0, z1 = 0;
+                if (kWindow && u->T <= 1) {
+                    z0 = p.sinks - kt * kBN;
+                    z1 = u->base - p.window + 1 - kt * kBN;
+                    z0 = z0 < 0 ? 0 : z0;
+                    z1 = z1 < kBN ? z1 : kBN;
+                }
                 const bool any = vl_guard_tile<D, kBF16>(smem + L::kKV + stage * L::kTileBytes, left, u->T > 1,
-                                                         u->bad_rows[(kt - guard) & (kTreeBadTiles - 1)], lane);
+                                                         u->bad_rows[g & (kBad - 1)], lane, z0, z1);
                 if (any && lane == 0) u->bad = 1;
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -616,12 +676,20 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         ok = fetch(cur) && (!units[cur].valid || pass(nullptr, 0, 0));
         while (ok && units[cur].valid) {
             TreeUnit &u = units[cur];
-            const int k1 = u.k1, guard = u.base / kBN;
+            const int k1 = u.k1, guard = u.base / kBN, skip = kWindow ? win_skip(u.base, p.window, p.sinks) : 0;
+            const WinWhole w = kWindow ? tree_whole(p, u.T, u.base) : WinWhole{};
+            int g = 0;
 #pragma unroll 1
             for (int kt = u.k0; ok && kt < k1; ++kt) {
                 if (kt + 1 == k1) ok = fetch(nxt);
                 if (ok && (kt + 1 < k1 || units[nxt].valid)) ok = pass(nullptr, 0, 0);
-                ok = ok && pass(kt >= guard ? &u : nullptr, kt, guard);
+                if constexpr (kWindow) {
+                    const bool look = !w(kt);
+                    ok = ok && pass(look ? &u : nullptr, win_key_tile<kWindow>(kt, p.sinks, skip), g);
+                    g += look ? 1 : 0;
+                } else {
+                    ok = ok && pass(kt >= guard ? &u : nullptr, kt, kt - guard);
+                }
             }
             __syncwarp();
             if (ok && lane == 0) mbar_arrive(unit_empty(cur));
@@ -640,6 +708,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         int kt = 0, k0 = 0, k1 = 0, tree0 = 0;
         bool valid = false, active = false, more = true;  // this row is real; some row of this warp is
         Bits128 anc{0ull, 0ull};
+        int pos = 0, skip = 0;  // with a window: this row's position, key tiles left out, tiles seen whole
+        WinWhole seen_whole{};
         float mrow = -INFINITY, l = 0.f, done_m = 0.f, done_l = 0.f;
         while (true) {
             if (kt == k1) {
@@ -667,7 +737,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                         for (int t = lane; t < u.T && t < kTreeMax; t += 32)
                             par[t] = p.parents != nullptr ? p.parents[u.first + t] : t - 1;
                         __syncwarp();
-                        if (valid) anc = tree_ancestors(u.t0 + tok, [&](int t) { return par[t]; });
+                        if (!kWindow && valid) anc = tree_ancestors(u.t0 + tok, [&](int t) { return par[t]; });
+                    }
+                    if constexpr (kWindow) {
+                        seen_whole = tree_whole(p, u.T, u.base);
+                        skip = win_skip(u.base, p.window, p.sinks);
+                        int depth = 0;
+                        if (u.T > 1 && valid)
+                            anc = tree_window(u.t0 + tok, u.base, p.window, p.sinks, depth, [&](int t) { return par[t]; });
+                        pos = u.base + depth;
                     }
                     ++un;
                 }
@@ -686,12 +764,18 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                     // weights): a quarter of the instructions of one pass over 128 columns in
                     // registers, which together with the epilogue's did not stay in the instruction
                     // cache (the first tile after an epilogue took 4700 cycles instead of 1200).
-                    const bool whole = (kt + 1) * kBN <= tree0;  // every row sees every key of the tile
-                    uint32_t w[4] = {~0u, ~0u, ~0u, ~0u};        // bit c: this row sees key kt * 128 + c
+                    const bool whole = kWindow ? seen_whole(kt) : (kt + 1) * kBN <= tree0;  // every row sees every key
+                    uint32_t w[4] = {~0u, ~0u, ~0u, ~0u};  // bit c: this row sees key c of the tile
                     if (!whole) {
-                        const int sh = kt * kBN - tree0;
+                        const int key0 = win_key_tile<kWindow>(kt, p.sinks, skip) * kBN;
+                        const int sh = key0 - tree0;
                         Bits128 see = sh >= 0 ? bits_shr(anc, sh) : bits_shl(anc, -sh);
-                        const Bits128 old = bits_below(-sh);
+                        Bits128 old = bits_below(-sh);
+                        if constexpr (kWindow) {
+                            const Bits128 gone = bits_below(pos - p.window + 1 - key0), sink = bits_below(p.sinks - key0);
+                            old.lo &= ~gone.lo | sink.lo;
+                            old.hi &= ~gone.hi | sink.hi;
+                        }
                         see.lo |= old.lo;
                         see.hi |= old.hi;
                         w[0] = static_cast<uint32_t>(see.lo);
@@ -835,16 +919,29 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                         if (*reinterpret_cast<const volatile int *>(&u.bad) != 0) {
                             // non-finite values that the guard took out of V, for the rows that see them:
                             // added to the stored row, whose other values they do not change
-                            const Bits128 seen = u.T > 1
-                                ? tree_ancestors(u.t0 + tok, [&](int t) {
-                                      return p.parents != nullptr && t < u.T ? p.parents[u.first + t] : t - 1;
-                                  })
-                                : Bits128{1ull, 0ull};
+                            auto up = [&](int t) -> int {
+                                return p.parents != nullptr && t < u.T ? p.parents[u.first + t] : t - 1;
+                            };
+                            int depth = 0;
+                            Bits128 seen{1ull, 0ull};
+                            if (u.T > 1)
+                                seen = kWindow ? tree_window(u.t0 + tok, u.base, p.window, p.sinks, depth, up)
+                                               : tree_ancestors(u.t0 + tok, up);
+                            const WinWhole w = kWindow ? tree_whole(p, u.T, u.base) : WinWhole{};
+                            const int win_skipped = kWindow ? win_skip(u.base, p.window, p.sinks) : 0;
+                            int step = u.k0 - 1, tile0 = 0;  // with a window: guarded tile g >> 2, its first key
 #pragma unroll 1
-                            for (int g = 0; g < kTreeBadTiles * 4; ++g)
+                            for (int g = 0; g < kBad * 4; ++g) {
+                                if (kWindow && (g & 3) == 0) {
+                                    do ++step; while (w(step));
+                                    tile0 = win_key_tile<kWindow>(step, p.sinks, win_skipped) * kBN;
+                                }
 #pragma unroll 1
                                 for (uint32_t bits = u.bad_rows[g >> 2][g & 3]; bits != 0; bits &= bits - 1) {
-                                    const int key = u.base / kBN * kBN + 32 * g + __ffs(bits) - 1, node = key - u.base;
+                                    const int key = (kWindow ? tile0 + 32 * (g & 3) : u.base / kBN * kBN + 32 * g) +
+                                                    __ffs(bits) - 1;
+                                    const int node = key - u.base;
+                                    if (kWindow && node < 0 && key <= u.base + depth - p.window && key >= p.sinks) continue;
                                     if (node >= 0 && !((node < 64 ? seen.lo >> node : seen.hi >> (node - 64)) & 1ull))
                                         continue;
                                     const int pg = p.table[static_cast<long long>(u.row) * p.table_w + (key >> p.page_shift)];
@@ -855,6 +952,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                                     else
                                         add_nonfinite_f32<D, kBF16>(part, vr);
                                 }
+                            }
                         }
                     }
                     tc_fence_before();
@@ -953,7 +1051,7 @@ __device__ __forceinline__ void tree_merge_row(const TreeParams &p, int c0, int 
 // The row's sequence is looked for before the wait for the kernel before; after it comes the plan.
 // (Adding the plan up here before the wait, too, saves 0.3 us of 11 with one sequence and nothing
 // with 16.)
-template <int D, bool kBF16>
+template <int D, bool kBF16, bool kWindow>
 __global__ void __launch_bounds__(32) attn_tree_merge_kernel(const __grid_constant__ TreeParams p) {
     grid_launch_dependents();
     const int lane = threadIdx.x & 31, R = static_cast<int>(blockIdx.x);
@@ -965,7 +1063,7 @@ __global__ void __launch_bounds__(32) attn_tree_merge_kernel(const __grid_consta
         if (ld_ahead_of_wait(p.cu + mid) <= tok) lo = mid; else hi = mid;
     }
     const TreeSeq q = tree_seq<true>(p, lo);
-    const int nt = tree_key_tiles(q.L), mt = tree_row_tiles(p, q.T), uw = tree_unit_weight(nt);
+    const int nt = tree_key_tiles<kWindow>(p, q.T, q.L), mt = tree_row_tiles(p, q.T), uw = tree_unit_weight(nt);
     const int t = tok - q.q0, m = t / p.rt;
     const int prow = (t - m * p.rt) * p.group + head % p.group;  // row within the tile
     grid_dependency_wait();

@@ -63,6 +63,8 @@ namespace gqa {
 constexpr int kVlSlots = 4;       // unit descriptors in flight
 constexpr int kVlSeqs = 2048;     // most sequences of one launch (their block counts lie in shared memory)
 constexpr int kVlBadTiles = 4;    // key tiles of a unit that the guard may look at
+// ... with a window: one where the first keys end, three at the window's start, three at the diagonal
+constexpr int kVlBadTilesWin = 8;
 
 struct VarlenParams : Params {
     const int *cu_q, *cu_k;  // device [n_seqs + 1]
@@ -72,6 +74,7 @@ struct VarlenParams : Params {
     int block_rows;          // query rows of a unit: 128 (pair) or 256
     int head_units;          // units per block of rows: Hq / 2 (pair) or Hq
     int most_blocks;         // blocks of rows that ascending offsets can have
+    int window, sinks;       // window kernels: row at position p sees j <= p with j > p - window or j < sinks
     int q_head_y, k_head_y, v_head_y;  // tensor map order: 1 = (D, heads, rows), 0 = (D, rows, heads)
     long long o_row, o_head, v_row, v_head;  // strides in bytes
 };
@@ -86,7 +89,7 @@ struct VlUnit {
     int nk;      // keys of the sequence
     int rel;     // row r of the block sees keys j <= r + rel under the causal mask
     int bad;     // set by the guard: some bad_rows bit is set
-    uint32_t bad_rows[kVlBadTiles][4];  // rows of the guarded V tiles with a non-finite value
+    uint32_t bad_rows[kVlBadTilesWin][4];  // rows of the guarded V tiles with a non-finite value
 };
 
 template <int D>
@@ -109,14 +112,43 @@ struct VlLayout {
 };
 static_assert(VlLayout<128>::kAlloc <= 227 * 1024, "shared memory of one CTA");
 
+// With a window, the key tiles that no row of a unit sees are left out: those between the tiles of
+// the first `sinks` keys and the tile that holds the first key of the unit's first row's window.
+// Steps j = 0, 1, .. of the unit then visit key tiles j, from the sinks' tiles on j + skip.
+__device__ __forceinline__ int win_tiles(int keys) { return (keys + kBN - 1) / kBN; }
+__device__ __forceinline__ int win_skip(int first_pos, int window, int sinks) {
+    const int lo = first_pos - window + 1, gap = lo > 0 ? lo / kBN - win_tiles(sinks) : 0;
+    return gap > 0 ? gap : 0;
+}
+template <bool kWindow>
+__device__ __forceinline__ int win_key_tile(int j, int sinks, int skip) {
+    if constexpr (!kWindow) return j;
+    return j < win_tiles(sinks) ? j : j + skip;
+}
+// The steps whose tiles the rows at positions first_pos .. last_pos see whole, of keys 0 .. nk - 1
+// (`nk`, or the first position that is not seen by all): steps below `sink` and in [w0, w1).
+struct WinWhole {
+    int sink, w0, w1;
+    __device__ __forceinline__ bool operator()(int j) const { return j < sink || (j >= w0 && j < w1); }
+};
+__device__ __forceinline__ WinWhole win_whole(int nk, int first_pos, int last_pos, int window, int sinks, int skip) {
+    const int end = first_pos + 1 < nk ? first_pos + 1 : nk;  // keys below are seen, but for the window
+    WinWhole w;
+    w.sink = end > 0 ? (sinks < end ? sinks : end) / kBN : 0;
+    w.w0 = last_pos - window >= 0 ? (last_pos - window) / kBN + 1 - skip : 0;
+    w.w1 = end > 0 ? end / kBN - skip : 0;
+    return w;
+}
+
 // Tile i of a unit: its rows, head and the key tiles [0, n) that it visits.
 struct VlTile {
     int row0;   // first row of the tile within the block
     int valid;  // query rows of the tile (0: absent)
     int rel;    // row r of the tile sees keys j <= r + rel (causal)
     int n;      // key tiles
+    int skip;   // key tiles left out behind the first ones (0 without a window)
 };
-template <bool kCausal>
+template <bool kCausal, bool kWindow>
 __device__ __forceinline__ VlTile vl_tile(const VarlenParams &p, const VlUnit &u, int i) {
     VlTile t;
     t.row0 = p.pair ? 0 : kBM * i;
@@ -125,8 +157,18 @@ __device__ __forceinline__ VlTile vl_tile(const VarlenParams &p, const VlUnit &u
     t.rel = u.rel + t.row0;
     int seen = u.nk;
     if (kCausal && t.rel + t.valid < seen) seen = t.rel + t.valid;
-    t.n = (t.valid > 0 && seen > 0) ? (seen + kBN - 1) / kBN : 0;
+    t.skip = kWindow ? win_skip(u.rel, p.window, p.sinks) : 0;
+    t.n = (t.valid > 0 && seen > 0) ? (seen + kBN - 1) / kBN - t.skip : 0;
     return t;
+}
+// The steps of tile t whose keys all its rows see (window kernels).
+__device__ __forceinline__ WinWhole vl_whole(const VarlenParams &p, const VlUnit &u, const VlTile &t) {
+    return win_whole(u.nk, t.rel, t.rel + t.valid - 1, p.window, p.sinks, t.skip);
+}
+// The same for both tiles of a unit: the others pass the guard.
+__device__ __forceinline__ WinWhole vl_unguarded(const VarlenParams &p, const VlUnit &u) {
+    const int rows = u.rows < p.block_rows ? u.rows : p.block_rows;
+    return win_whole(u.nk, u.rel, u.rel + rows - 1, p.window, p.sinks, win_skip(u.rel, p.window, p.sinks));
 }
 // Whether some row of a unit sees a key: of its rows, `rows` to the end of the sequence, the
 // last one sees most.
@@ -331,9 +373,11 @@ __device__ __forceinline__ void add_nonfinite_f32(float *o_row, const uint8_t *v
 }
 
 // The guard's work on one V tile in shared memory: rows at or past `rows` become zero;
-// with `scan`, non-finite values of the rows before are zeroed and their rows noted.
+// with `scan`, non-finite values of the rows before are zeroed and their rows noted.  Rows [z0, z1)
+// become zero, too.
 template <int D, bool kBF16>
-__device__ __forceinline__ bool vl_guard_tile(uint8_t *tile, int rows, bool scan, uint32_t *bad_rows, int lane) {
+__device__ __forceinline__ bool vl_guard_tile(uint8_t *tile, int rows, bool scan, uint32_t *bad_rows, int lane,
+                                              int z0 = 0, int z1 = 0) {
     constexpr int kAtoms = D / 64;
     const uint4 zero = make_uint4(0, 0, 0, 0);
     bool any = false;
@@ -341,6 +385,7 @@ __device__ __forceinline__ bool vl_guard_tile(uint8_t *tile, int rows, bool scan
     for (int a = 0; a < kAtoms; ++a) {
         uint4 *atom = reinterpret_cast<uint4 *>(tile + a * kAtomBytes);  // 8 chunks of 16 bytes a row
         for (int i = rows * 8 + lane; i < kBN * 8; i += 32) atom[i] = zero;
+        for (int i = z0 * 8 + lane; i < z1 * 8; i += 32) atom[i] = zero;
         if (!scan) continue;
         // 0 times a value, summed: NaN exactly where one is not finite.  The rows past the end are
         // zeros by now, so all 128 are taken, with a fixed count of loads in flight.
@@ -376,11 +421,14 @@ __device__ __forceinline__ bool vl_guard_tile(uint8_t *tile, int rows, bool scan
 
 // tmQ, tmK, tmV: 3-D tensor maps of the packed rows, box 64 columns x 128 rows of one head
 // with the 128-byte swizzle; rows past the end of the tensor read as zeros.
-template <int D, bool kBF16, bool kCausal>
+// kWindow (causal): attn_fwd_varlen_window.
+template <int D, bool kBF16, bool kCausal, bool kWindow>
 __global__ void __launch_bounds__(kWsThreads, 1)
     attn_fwd_varlen_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                            const __grid_constant__ CUtensorMap tmV, const __grid_constant__ VarlenParams p) {
+    static_assert(kCausal || !kWindow, "a window is causal");
     using L = VlLayout<D>;
+    constexpr int kBad = kWindow ? kVlBadTilesWin : kVlBadTiles;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -451,7 +499,7 @@ __global__ void __launch_bounds__(kWsThreads, 1)
             // K_0) in pairs that complete V_j's barrier together, so that the issuer waits once
             // per key tile; every stage keeps its own phase bit (fph).
             struct Cur {
-                int valid, n, n0, n1, q0, q1, head, k0;
+                int valid, n, n0, n1, q0, q1, head, k0, skip;
             };
             Ring ring;
             int slot = 0;
@@ -469,7 +517,7 @@ __global__ void __launch_bounds__(kWsThreads, 1)
                 const VlUnit &u = units[slot];
                 c.valid = u.valid;
                 if (c.valid) {
-                    const VlTile t0 = vl_tile<kCausal>(p, u, 0), t1 = vl_tile<kCausal>(p, u, 1);
+                    const VlTile t0 = vl_tile<kCausal, kWindow>(p, u, 0), t1 = vl_tile<kCausal, kWindow>(p, u, 1);
                     c.n0 = t0.n;
                     c.n1 = t1.n;
                     c.n = t0.n > t1.n ? t0.n : t1.n;
@@ -477,6 +525,7 @@ __global__ void __launch_bounds__(kWsThreads, 1)
                     c.q1 = u.q0 + t1.row0;
                     c.head = u.head;
                     c.k0 = u.k0;
+                    c.skip = t0.skip;
                 }
                 mbar_arrive(unit_empty(slot));
                 if (++slot == kVlSlots) {
@@ -502,7 +551,8 @@ __global__ void __launch_bounds__(kWsThreads, 1)
                 mbar_arrive_expect_tx(kv_full(0), L::kTileBytes);
                 armed |= 1u;
                 fph ^= 1u;
-                issue(sKV, &tmK, p.k_head_y, cur.k0, cur.head / p.group, kv_full(0));
+                issue(sKV, &tmK, p.k_head_y, cur.k0 + win_key_tile<kWindow>(0, p.sinks, cur.skip) * kBN,
+                      cur.head / p.group, kv_full(0));
                 ring.next();
                 ok = load_q(0, cur) && load_q(1, cur);
             }
@@ -510,11 +560,11 @@ __global__ void __launch_bounds__(kWsThreads, 1)
                 const int kvh = cur.head / p.group;
                 for (int j = 0; j < cur.n && ok; ++j) {
                     bool two = true;
-                    int krow = cur.k0 + (j + 1) * kBN, khead = kvh;
+                    int krow = cur.k0 + win_key_tile<kWindow>(j + 1, p.sinks, cur.skip) * kBN, khead = kvh;
                     if (j + 1 == cur.n) {
                         if (!(ok = fetch(nxt))) break;
                         two = nxt.valid != 0;
-                        krow = nxt.k0;
+                        krow = nxt.k0 + win_key_tile<kWindow>(0, p.sinks, nxt.skip) * kBN;
                         khead = nxt.head / p.group;
                     }
                     const int vs = ring.s;
@@ -525,7 +575,8 @@ __global__ void __launch_bounds__(kWsThreads, 1)
                     mbar_arrive_expect_tx(kv_full(vs), L::kTileBytes * (two ? 2u : 1u));
                     armed |= 1u << vs;
                     fph ^= 1u << vs;
-                    issue(sKV + vs * L::kTileBytes, &tmV, p.v_head_y, cur.k0 + j * kBN, kvh, kv_full(vs));
+                    issue(sKV + vs * L::kTileBytes, &tmV, p.v_head_y,
+                          cur.k0 + win_key_tile<kWindow>(j, p.sinks, cur.skip) * kBN, kvh, kv_full(vs));
                     ring.next();
                     if (two) {
                         issue(sKV + ring.s * L::kTileBytes, &tmK, p.k_head_y, krow, khead, kv_full(vs));
@@ -548,6 +599,7 @@ __global__ void __launch_bounds__(kWsThreads, 1)
             // ---------------------------------------------------- MMA issuer
             struct Cur {
                 int valid, n, n0, n1, g0;  // g0: tiles from here on pass the guard before P V reads them
+                WinWhole w;                // with a window: all but these steps do
             };
             Ring ring;
             uint32_t fph = 0;
@@ -566,11 +618,12 @@ __global__ void __launch_bounds__(kWsThreads, 1)
                 const VlUnit &u = units[slot];
                 c.valid = u.valid;
                 if (c.valid) {
-                    const VlTile t0 = vl_tile<kCausal>(p, u, 0), t1 = vl_tile<kCausal>(p, u, 1);
+                    const VlTile t0 = vl_tile<kCausal, kWindow>(p, u, 0), t1 = vl_tile<kCausal, kWindow>(p, u, 1);
                     c.n0 = t0.n;
                     c.n1 = t1.n;
                     c.n = t0.n > t1.n ? t0.n : t1.n;
-                    c.g0 = vl_first_masked<kCausal>(u, t0);
+                    if constexpr (kWindow) c.w = vl_unguarded(p, u);
+                    else c.g0 = vl_first_masked<kCausal>(u, t0);
                 } else {
                     c.n0 = c.n1 = 0;
                 }
@@ -587,14 +640,19 @@ __global__ void __launch_bounds__(kWsThreads, 1)
             // change of unit, before the first unit a step without a V tile) shares one copy for
             // both tiles: instructions that run once per unit have left the cache by then, which
             // cost 3000 cycles per unit with a copy for each case.
-            Cur cur{1, 1, 0, 0, INT_MAX}, nxt{};
+            Cur cur{1, 1, 0, 0, INT_MAX, {1, 0, 0}}, nxt{};
             bool ok = true, start = true;
             while (ok && cur.valid) {
-                // steps [1, inner) are whole for both tiles, with no guard and no change of unit
+                // steps [1, inner) (with a window those from w.w0 on) are whole for both tiles, with no guard
+                // and no change of unit
                 int inner = (cur.n0 < cur.n1 ? cur.n0 : cur.n1) - 1;
-                if (cur.g0 < inner) inner = cur.g0;
+                if constexpr (kWindow) {
+                    if (cur.w.w1 < inner) inner = cur.w.w1;
+                } else {
+                    if (cur.g0 < inner) inner = cur.g0;
+                }
                 for (int j = 0; j < cur.n; ++j) {
-                    if (j == 1) {
+                    if (kWindow ? j > 0 && j >= cur.w.w0 && j < inner : j == 1) {
                         for (; j < inner; ++j) {
                             const int vs = ring.s;
                             if (!(ok = wait_full(vs))) break;  // V_j and K_{j+1}
@@ -626,7 +684,7 @@ __global__ void __launch_bounds__(kWsThreads, 1)
                     if (last && !(ok = fetch(nxt))) break;
                     if (start && !nxt.valid) break;
                     if (!(ok = wait_full(vs))) break;  // V_j and the K tile after it
-                    if (j >= cur.g0) {
+                    if (kWindow ? !cur.w(j) : j >= cur.g0) {
                         const int b = vs >> 1;
                         if (!(ok = wait_bar(v_ok(b), (vph >> b) & 1u, p, abort_flag))) break;
                         vph ^= 1u << b;
@@ -687,18 +745,20 @@ __global__ void __launch_bounds__(kWsThreads, 1)
                 VlUnit u;
                 u.valid = us.valid, u.rows = us.rows, u.nk = us.nk, u.rel = us.rel;
                 if (!u.valid) break;
-                const VlTile t0 = vl_tile<kCausal>(p, u, 0), t1 = vl_tile<kCausal>(p, u, 1);
-                const int n = t0.n > t1.n ? t0.n : t1.n, g0 = vl_first_masked<kCausal>(u, t0);
-                if (lane < kVlBadTiles * 4) us.bad_rows[lane >> 2][lane & 3] = 0;
+                const VlTile t0 = vl_tile<kCausal, kWindow>(p, u, 0), t1 = vl_tile<kCausal, kWindow>(p, u, 1);
+                const int n = t0.n > t1.n ? t0.n : t1.n, g0 = kWindow ? 0 : vl_first_masked<kCausal>(u, t0);
+                const WinWhole w = kWindow ? vl_unguarded(p, u) : WinWhole{};
+                int g = 0;  // guarded tiles so far
+                if (lane < kBad * 4) us.bad_rows[lane >> 2][lane & 3] = 0;
                 __syncwarp();
                 for (int j = 0; j < n; ++j, ++t) {
                     const int b = t & 1u, vs = 1 + 2 * b;
                     if (!(ok = __all_sync(0xffffffffu, wait_bar(kv_full(vs), (t >> 1) & 1u, p, abort_flag)))) break;
-                    if (j >= g0) {
-                        const int left = u.nk - j * kBN;
+                    if (kWindow ? !w(j) : j >= g0) {
+                        const int left = u.nk - win_key_tile<kWindow>(j, p.sinks, t0.skip) * kBN;
                         const bool any = vl_guard_tile<D, kBF16>(smem + L::kKV + vs * L::kTileBytes,
                                                                  left < kBN ? left : kBN, kCausal,
-                                                                 us.bad_rows[(j - g0) & (kVlBadTiles - 1)], lane);
+                                                                 us.bad_rows[(kWindow ? g++ : j - g0) & (kBad - 1)], lane);
                         if (any && lane == 0) us.bad = 1;
                         fence_proxy_async_smem();
                         __syncwarp();
@@ -786,6 +846,8 @@ __global__ void __launch_bounds__(kWsThreads, 1)
         uint32_t uphase = 1;
         float done_m = 0.f, done_l = 0.f;
         int j = 0, n = 0, first_masked = 0, lim0 = 0;
+        int pos = 0, skip = 0;  // with a window: this row's position, key tiles left out, steps seen whole
+        WinWhole seen_whole{};
         // m_ref: the max the probabilities are taken against (updated lazily);
         // m_top: the true running row max; l: running sum in units of 2^(m_ref*c).
         float m_ref = -INFINITY, m_top = -INFINITY, l = 0.f;
@@ -804,9 +866,15 @@ __global__ void __launch_bounds__(kWsThreads, 1)
                 more = u.valid != 0;
                 n = 0;
                 if (more) {
-                    const VlTile t = vl_tile<kCausal>(p, u, i);
+                    const VlTile t = vl_tile<kCausal, kWindow>(p, u, i);
                     n = t.n;
-                    first_masked = vl_first_masked<kCausal>(u, t);
+                    if constexpr (kWindow) {
+                        seen_whole = vl_whole(p, u, t);
+                        pos = r + t.rel;
+                        skip = t.skip;
+                    } else {
+                        first_masked = vl_first_masked<kCausal>(u, t);
+                    }
                     lim0 = u.nk - 1;  // this row keeps the keys up to lim0
                     if (kCausal && r + t.rel < lim0) lim0 = r + t.rel;
                 }
@@ -836,7 +904,7 @@ __global__ void __launch_bounds__(kWsThreads, 1)
                     const float mr = m_ref == -INFINITY ? 0.f : m_ref;
                     return make_float2(-mr * c, -mr * c);
                 };
-                if (j < first_masked) {
+                if (kWindow ? seen_whole(j) : j < first_masked) {
                     uint32_t s[128];
                     float mq[4];
 #pragma unroll
@@ -866,15 +934,30 @@ __global__ void __launch_bounds__(kWsThreads, 1)
                     // A masked tile, once or twice per unit: 32 columns at a time, in two passes over
                     // TMEM, which is few instructions to fetch each time (P, 16 columns of pairs,
                     // overwrites scores that have been read).
-                    const int lim = lim0 - j * kBN;  // this row keeps the columns up to lim
+                    const int col0 = win_key_tile<kWindow>(j, p.sinks, skip) * kBN;
+                    const int lim = lim0 - col0;  // this row keeps the columns up to lim
                     // Of columns 32 q .. every row of the warp sees all for q < q_all and none for
                     // q >= q_none: on a causal diagonal all but one of the four steps need no selects.
                     const int lo = __reduce_min_sync(0xffffffffu, lim), hi = __reduce_max_sync(0xffffffffu, lim);
                     const int q_all = lo < 31 ? 0 : (lo + 1) >> 5, q_none = hi < 0 ? 0 : (hi >> 5) + 1;
+                    // with a window: of those up to lim the columns past wlim or below sk
+                    const int wlim = kWindow ? pos - p.window - col0 : 0, sk = kWindow ? p.sinks - col0 : 0;
+                    const int wlo = kWindow ? __reduce_min_sync(0xffffffffu, wlim) : 0;
+                    const int whi = kWindow ? __reduce_max_sync(0xffffffffu, wlim) : 0;
+                    auto all = [&](int q) -> bool {
+                        return q < q_all && (!kWindow || 32 * q > whi || 32 * q + 31 < sk);
+                    };
+                    auto none = [&](int q) -> bool {
+                        return q >= q_none || (kWindow && 32 * q + 31 <= wlo && 32 * q >= sk);
+                    };
+                    auto sees = [&](int e, int q) -> bool {
+                        return e <= lim - 32 * q && (!kWindow || e > wlim - 32 * q || e < sk - 32 * q);
+                    };
 #pragma unroll 1
                     for (int q = 0; q < 4 && q < q_none; ++q) {
                         uint32_t s[32];
-                        if (q < q_all) {
+                        if (kWindow && none(q)) continue;
+                        if (all(q)) {
                             float mq[1];
                             tmem_ld32_max(tS + 32 * q, s, mq[0]);
                             tmem_ld_wait(s, mq);
@@ -885,7 +968,7 @@ __global__ void __launch_bounds__(kWsThreads, 1)
                             float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
                             for (int e = 0; e < 32; ++e)
-                                mx[e & 1] = fmaxf(mx[e & 1], e <= lim - 32 * q ? u2f(s[e]) : -INFINITY);
+                                mx[e & 1] = fmaxf(mx[e & 1], sees(e, q) ? u2f(s[e]) : -INFINITY);
                             m_top = fmax3(m_top, mx[0], mx[1]);
                         }
                     }
@@ -893,7 +976,7 @@ __global__ void __launch_bounds__(kWsThreads, 1)
 #pragma unroll 1
                     for (int q = 0; q < 4; ++q) {
                         uint32_t s[32], pk[16];
-                        if (q >= q_none) {
+                        if (none(q)) {
 #pragma unroll
                             for (int e = 0; e < 16; ++e) pk[e] = 0u;
                             tmem_st16(tS + 16 * q, pk);
@@ -901,10 +984,10 @@ __global__ void __launch_bounds__(kWsThreads, 1)
                         }
                         tmem_ld32(tS + 32 * q, s);
                         tmem_ld_wait(s);
-                        if (q >= q_all) {
+                        if (!all(q)) {
 #pragma unroll
                             for (int e = 0; e < 32; ++e)
-                                if (e > lim - 32 * q) s[e] = __float_as_uint(-INFINITY);
+                                if (!sees(e, q)) s[e] = __float_as_uint(-INFINITY);
                         }
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
@@ -943,7 +1026,7 @@ __global__ void __launch_bounds__(kWsThreads, 1)
                 const VlUnit &us = units[done_slot];
                 VlUnit u;
                 u.rows = us.rows, u.nk = us.nk, u.rel = us.rel;
-                const VlTile t = vl_tile<kCausal>(p, u, i);
+                const VlTile t = vl_tile<kCausal, kWindow>(p, u, i);
                 const int wvalid = t.valid - wq * 32;  // rows of this warp
                 if (t.n > 0) {
                     if (!__all_sync(0xffffffffu, wait_bar(o_full(i), ocount & 1u, p, abort_flag))) break;
@@ -1000,17 +1083,26 @@ __global__ void __launch_bounds__(kWsThreads, 1)
                     // non-finite values that the guard took out of V, for the rows that see them: added
                     // to the stored row, whose other values they do not change
                     if (t.n > 0 && *reinterpret_cast<const volatile int *>(&us.bad) != 0 && lane < wvalid) {
-                        const int g0 = vl_first_masked<kCausal>(u, vl_tile<kCausal>(p, u, 0)) * kBN;
+                        const VlTile t0 = vl_tile<kCausal, kWindow>(p, u, 0);
+                        const int g0 = kWindow ? 0 : vl_first_masked<kCausal>(u, t0) * kBN;
+                        const WinWhole w = kWindow ? vl_unguarded(p, u) : WinWhole{};
                         const uint8_t *vh = p.v_ptr + (us.head / p.group) * p.v_head + us.k0 * p.v_row;
                         int lim = u.nk - 1;
                         if (kCausal && r + t.rel < lim) lim = r + t.rel;
+                        int step = -1, tile0 = 0;  // with a window: the step of guarded tile g >> 2, its first key
 #pragma unroll 1
-                        for (int g = 0; g < kVlBadTiles * 4; ++g)
+                        for (int g = 0; g < kBad * 4; ++g) {
+                            if (kWindow && (g & 3) == 0) {
+                                do ++step; while (w(step));
+                                tile0 = win_key_tile<kWindow>(step, p.sinks, t0.skip) * kBN;
+                            }
 #pragma unroll 1
                             for (uint32_t bits = us.bad_rows[g >> 2][g & 3]; bits != 0; bits &= bits - 1) {
-                                const int key = g0 + 32 * g + __ffs(bits) - 1;
-                                if (key <= lim) add_nonfinite<D, kBF16>(otile + lane * p.o_row, vh + key * p.v_row);
+                                const int key = (kWindow ? tile0 + 32 * (g & 3) : g0 + 32 * g) + __ffs(bits) - 1;
+                                if (key <= lim && (!kWindow || key > r + t.rel - p.window || key < p.sinks))
+                                    add_nonfinite<D, kBF16>(otile + lane * p.o_row, vh + key * p.v_row);
                             }
+                        }
                     }
                 }
                 __syncwarp();

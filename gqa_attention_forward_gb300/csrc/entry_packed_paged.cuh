@@ -101,26 +101,26 @@ void common_params(gqa::Params &prm, void *o, float *lse, int Hq, int Hkv, float
     prm.inject_stall = g_inject_stall.load();
 }
 
-template <int D, bool BF16, bool CAUSAL>
+template <int D, bool BF16, bool CAUSAL, bool WINDOW = false>
 attn_status_t launch_varlen(int dev, int kid, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                             const gqa::VarlenParams &prm, unsigned grid, cudaStream_t s) {
-    auto kern = gqa::attn_fwd_varlen_kernel<D, BF16, CAUSAL>;
+    auto kern = gqa::attn_fwd_varlen_kernel<D, BF16, CAUSAL, WINDOW>;
     constexpr int smem = gqa::VlLayout<D>::kAlloc;
     if (attn_status_t st = set_smem_limit(dev, 24 + kid, kern, smem); st != ATTN_OK) return st;
     return launch_dependent(kern, grid, gqa::kWsThreads, smem, s, tq, tk, tv, prm);
 }
 
-template <int D, bool BF16>
+template <int D, bool BF16, bool WINDOW>
 attn_status_t launch_tree(int dev, int kid, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                           const gqa::TreeParams &prm, unsigned grid, cudaStream_t s) {
-    auto kern = gqa::attn_fwd_tree_kernel<D, BF16>;
+    auto kern = gqa::attn_fwd_tree_kernel<D, BF16, WINDOW>;
     constexpr int smem = gqa::TreeLayout<D>::kAlloc;
-    if (attn_status_t st = set_smem_limit(dev, 32 + kid, kern, smem); st != ATTN_OK) return st;
+    if (attn_status_t st = set_smem_limit(dev, 36 + kid, kern, smem); st != ATTN_OK) return st;
     if (attn_status_t st = launch_dependent(kern, grid, gqa::kTreeThreads, smem, s, tq, tk, tv, prm);
         st != ATTN_OK)
         return st;
     if (prm.plan != nullptr)
-        return launch_dependent(gqa::attn_tree_merge_kernel<D, BF16>, static_cast<unsigned>(prm.total_q) * prm.Hq, 32, 0,
+        return launch_dependent(gqa::attn_tree_merge_kernel<D, BF16, WINDOW>, static_cast<unsigned>(prm.total_q) * prm.Hq, 32, 0,
                                 s, prm);
     constexpr unsigned per_cta = gqa::kBM / gqa::kMergeCtaRows;
     return launch_dependent(gqa::attn_tree_merge_ctas_kernel<D, BF16>, grid * per_cta, gqa::kMergeCtaThreads, 0, s, prm);
@@ -196,13 +196,16 @@ unsigned move_grid(const gqa::KvPool &p, long long pages, int sms) {
     return static_cast<unsigned>(blocks < most ? (blocks > 0 ? blocks : 1) : most);
 }
 
-}  // namespace
+// A window and a number of first keys as the kernels take them: no sum of theirs with a position
+// passes 32 bits.
+constexpr int kWindowMost = 1 << 30;
+bool window_ok(int window, int sinks) { return window >= 1 && sinks >= 0; }
 
-extern "C" {
-
-attn_status_t attn_fwd_varlen(const void *q, const void *k, const void *v, void *o, float *lse, const int *cu_q,
-                              const int *cu_k, int n_seqs, int total_q, int total_k, int Hq, int Hkv, int D,
-                              const long long *strides, float scale, int causal, attn_dtype_t dtype, void *stream) {
+// attn_fwd_varlen (window 0) and attn_fwd_varlen_window.
+attn_status_t run_varlen(const void *q, const void *k, const void *v, void *o, float *lse, const int *cu_q,
+                         const int *cu_k, int n_seqs, int total_q, int total_k, int Hq, int Hkv, int D,
+                         const long long *strides, float scale, int causal, int window, int sinks, attn_dtype_t dtype,
+                         void *stream) {
     if (n_seqs < 0 || total_q < 0 || total_k < 0 || Hq < 0 || Hkv < 1 || Hq % Hkv != 0) return ATTN_ERR_SHAPE;
     if (!(std::isfinite(scale) && scale > 0.f)) return ATTN_ERR_SHAPE;
     if (D != 64 && D != 128) return ATTN_ERR_HEADDIM;
@@ -250,7 +253,12 @@ attn_status_t attn_fwd_varlen(const void *q, const void *k, const void *v, void 
         return no_map();
     const unsigned grid = static_cast<unsigned>(units < g_dev_sms[dev] ? units : g_dev_sms[dev]);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const int kid = (D == 128 ? 4 : 0) + (bf16 ? 2 : 0) + (causal ? 1 : 0);
+    // a window that no sequence can leave, or first keys that are all keys: the causal mask
+    if (window >= total_k || sinks >= total_k) window = 0;
+    prm.window = window < kWindowMost ? window : kWindowMost;
+    prm.sinks = sinks < kWindowMost ? sinks : kWindowMost;
+    const int kid = window > 0 ? 8 + (D == 128 ? 2 : 0) + (bf16 ? 1 : 0)
+                               : (D == 128 ? 4 : 0) + (bf16 ? 2 : 0) + (causal ? 1 : 0);
     auto launch = [&]() {
         switch (kid) {
             case 0: return launch_varlen<64, false, false>(dev, kid, tq, tk, tv, prm, grid, s);
@@ -260,7 +268,11 @@ attn_status_t attn_fwd_varlen(const void *q, const void *k, const void *v, void 
             case 4: return launch_varlen<128, false, false>(dev, kid, tq, tk, tv, prm, grid, s);
             case 5: return launch_varlen<128, false, true>(dev, kid, tq, tk, tv, prm, grid, s);
             case 6: return launch_varlen<128, true, false>(dev, kid, tq, tk, tv, prm, grid, s);
-            default: return launch_varlen<128, true, true>(dev, kid, tq, tk, tv, prm, grid, s);
+            case 7: return launch_varlen<128, true, true>(dev, kid, tq, tk, tv, prm, grid, s);
+            case 8: return launch_varlen<64, false, true, true>(dev, kid, tq, tk, tv, prm, grid, s);
+            case 9: return launch_varlen<64, true, true, true>(dev, kid, tq, tk, tv, prm, grid, s);
+            case 10: return launch_varlen<128, false, true, true>(dev, kid, tq, tk, tv, prm, grid, s);
+            default: return launch_varlen<128, true, true, true>(dev, kid, tq, tk, tv, prm, grid, s);
         }
     };
     // at most kVlSeqs sequences per launch; a launch leaves the rows of the others alone
@@ -274,24 +286,10 @@ attn_status_t attn_fwd_varlen(const void *q, const void *k, const void *v, void 
     return ATTN_OK;
 }
 
-attn_status_t attn_fwd_tree_workspace(int n_seqs, int D, size_t *bytes) {
-    if (bytes == nullptr) return ATTN_ERR_NULL;
-    *bytes = 0;
-    if (n_seqs < 0) return ATTN_ERR_SHAPE;
-    if (D != 64 && D != 128) return ATTN_ERR_HEADDIM;
-    int dev = 0;
-    if (attn_status_t st = check_device(&dev); st != ATTN_OK) return st;
-    const size_t rows = static_cast<size_t>(g_dev_sms[dev]) * 2 * gqa::kBM;
-    const int launch_seqs = n_seqs < gqa::kTreeSeqs ? n_seqs : gqa::kTreeSeqs;
-    const size_t plan = (static_cast<size_t>(launch_seqs) + 1) * sizeof(int), starts = g_dev_sms[dev] * sizeof(int4);
-    *bytes = rows * (D + 1) * sizeof(float) + (plan > starts ? plan : starts);
-    return ATTN_OK;
-}
-
-attn_status_t attn_fwd_tree(const void *q, const attn_kv_cache_t *cache, int layer, void *o, float *lse, const int *cu,
-                            const int *seqs, const int *parents, int n_seqs, int total_q, int Hq,
-                            const long long *strides, float scale, void *workspace, size_t workspace_bytes,
-                            void *stream) {
+// attn_fwd_tree (window 0) and attn_fwd_tree_window.
+attn_status_t run_tree(const void *q, const attn_kv_cache_t *cache, int layer, void *o, float *lse, const int *cu,
+                       const int *seqs, const int *parents, int n_seqs, int total_q, int Hq, const long long *strides,
+                       float scale, int window, int sinks, void *workspace, size_t workspace_bytes, void *stream) {
     if (attn_status_t st = check_cache(cache); st != ATTN_OK) return st;
     const int Hkv = cache->Hkv, D = cache->D;
     if (n_seqs < 0 || total_q < 0 || Hq < 0 || Hq % Hkv != 0 || Hq / Hkv > 128) return ATTN_ERR_SHAPE;
@@ -357,13 +355,21 @@ attn_status_t attn_fwd_tree(const void *q, const attn_kv_cache_t *cache, int lay
     const unsigned grid = static_cast<unsigned>(most < sms ? most : sms);
     prm.grid = static_cast<int>(grid);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const int kid = (D == 128 ? 2 : 0) + (bf16 ? 1 : 0);
+    // a window that no sequence can leave, or first keys that are all keys: the plain call
+    if (window >= cache->table_width * cache->page || sinks >= cache->table_width * cache->page) window = 0;
+    prm.window = window < kWindowMost ? window : kWindowMost;
+    prm.sinks = sinks < kWindowMost ? sinks : kWindowMost;
+    const int kid = (window > 0 ? 4 : 0) + (D == 128 ? 2 : 0) + (bf16 ? 1 : 0);
     auto launch = [&]() {
         switch (kid) {
-            case 0: return launch_tree<64, false>(dev, kid, tq, tk, tv, prm, grid, s);
-            case 1: return launch_tree<64, true>(dev, kid, tq, tk, tv, prm, grid, s);
-            case 2: return launch_tree<128, false>(dev, kid, tq, tk, tv, prm, grid, s);
-            default: return launch_tree<128, true>(dev, kid, tq, tk, tv, prm, grid, s);
+            case 0: return launch_tree<64, false, false>(dev, kid, tq, tk, tv, prm, grid, s);
+            case 1: return launch_tree<64, true, false>(dev, kid, tq, tk, tv, prm, grid, s);
+            case 2: return launch_tree<128, false, false>(dev, kid, tq, tk, tv, prm, grid, s);
+            case 3: return launch_tree<128, true, false>(dev, kid, tq, tk, tv, prm, grid, s);
+            case 4: return launch_tree<64, false, true>(dev, kid, tq, tk, tv, prm, grid, s);
+            case 5: return launch_tree<64, true, true>(dev, kid, tq, tk, tv, prm, grid, s);
+            case 6: return launch_tree<128, false, true>(dev, kid, tq, tk, tv, prm, grid, s);
+            default: return launch_tree<128, true, true>(dev, kid, tq, tk, tv, prm, grid, s);
         }
     };
     // at most kTreeSeqs sequences per launch, and no more than the list's 32-bit weights hold
@@ -377,6 +383,57 @@ attn_status_t attn_fwd_tree(const void *q, const attn_kv_cache_t *cache, int lay
         if (attn_status_t e = launch(); e != ATTN_OK) return e;
     }
     return ATTN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+attn_status_t attn_fwd_varlen(const void *q, const void *k, const void *v, void *o, float *lse, const int *cu_q,
+                              const int *cu_k, int n_seqs, int total_q, int total_k, int Hq, int Hkv, int D,
+                              const long long *strides, float scale, int causal, attn_dtype_t dtype, void *stream) {
+    return run_varlen(q, k, v, o, lse, cu_q, cu_k, n_seqs, total_q, total_k, Hq, Hkv, D, strides, scale, causal, 0, 0, dtype,
+                      stream);
+}
+
+attn_status_t attn_fwd_varlen_window(const void *q, const void *k, const void *v, void *o, float *lse, const int *cu_q,
+                                     const int *cu_k, int n_seqs, int total_q, int total_k, int Hq, int Hkv, int D,
+                                     const long long *strides, float scale, int window, int sinks, attn_dtype_t dtype,
+                                     void *stream) {
+    if (!window_ok(window, sinks)) return ATTN_ERR_SHAPE;
+    return run_varlen(q, k, v, o, lse, cu_q, cu_k, n_seqs, total_q, total_k, Hq, Hkv, D, strides, scale, 1, window, sinks,
+                      dtype, stream);
+}
+
+attn_status_t attn_fwd_tree_workspace(int n_seqs, int D, size_t *bytes) {
+    if (bytes == nullptr) return ATTN_ERR_NULL;
+    *bytes = 0;
+    if (n_seqs < 0) return ATTN_ERR_SHAPE;
+    if (D != 64 && D != 128) return ATTN_ERR_HEADDIM;
+    int dev = 0;
+    if (attn_status_t st = check_device(&dev); st != ATTN_OK) return st;
+    const size_t rows = static_cast<size_t>(g_dev_sms[dev]) * 2 * gqa::kBM;
+    const int launch_seqs = n_seqs < gqa::kTreeSeqs ? n_seqs : gqa::kTreeSeqs;
+    const size_t plan = (static_cast<size_t>(launch_seqs) + 1) * sizeof(int), starts = g_dev_sms[dev] * sizeof(int4);
+    *bytes = rows * (D + 1) * sizeof(float) + (plan > starts ? plan : starts);
+    return ATTN_OK;
+}
+
+attn_status_t attn_fwd_tree(const void *q, const attn_kv_cache_t *cache, int layer, void *o, float *lse, const int *cu,
+                            const int *seqs, const int *parents, int n_seqs, int total_q, int Hq,
+                            const long long *strides, float scale, void *workspace, size_t workspace_bytes,
+                            void *stream) {
+    return run_tree(q, cache, layer, o, lse, cu, seqs, parents, n_seqs, total_q, Hq, strides, scale, 0, 0, workspace,
+                    workspace_bytes, stream);
+}
+
+attn_status_t attn_fwd_tree_window(const void *q, const attn_kv_cache_t *cache, int layer, void *o, float *lse,
+                                   const int *cu, const int *seqs, const int *parents, int n_seqs, int total_q, int Hq,
+                                   const long long *strides, float scale, int window, int sinks, void *workspace,
+                                   size_t workspace_bytes, void *stream) {
+    if (!window_ok(window, sinks)) return ATTN_ERR_SHAPE;
+    return run_tree(q, cache, layer, o, lse, cu, seqs, parents, n_seqs, total_q, Hq, strides, scale, window, sinks, workspace,
+                    workspace_bytes, stream);
 }
 
 attn_status_t attn_kv_scratch(int n_pages, int n_rows, size_t *bytes) {

@@ -294,6 +294,22 @@ attn_status_t attn_fwd_varlen(const void *q, const void *k, const void *v, void 
                               float scale, int causal, attn_dtype_t dtype, void *stream);
 
 /*
+ * attn_fwd_varlen_window -- attn_fwd_varlen with the causal mask and a sliding window: the row
+ * at position pos = i + Nk_s - Nq_s of sequence s sees the keys j <= pos with j > pos - window
+ * (itself and the window - 1 before it) or j < sinks (the first keys, which stay visible).
+ *
+ * window  at least 1; one of total_k or more is the causal mask alone.  sinks: at least 0.
+ * Key tiles that no row of a block sees are neither loaded nor computed.
+ * Everything else, rounding, values in masked places, limits and errors among it: as
+ * attn_fwd_varlen with causal set; ATTN_ERR_SHAPE also for window < 1 or sinks < 0.
+ */
+attn_status_t attn_fwd_varlen_window(const void *q, const void *k, const void *v, void *o, float *lse,
+                                     const int *cu_q, const int *cu_k, int n_seqs, int total_q,
+                                     int total_k, int Hq, int Hkv, int D, const long long *strides,
+                                     float scale, int window, int sinks, attn_dtype_t dtype,
+                                     void *stream);
+
+/*
  * A paged key/value cache.  All pointers are device memory owned by the caller.
  *
  * k, v    pools [n_layers, n_pages, Hkv, page, D] contiguous, dtype, 16-byte aligned
@@ -408,6 +424,27 @@ attn_status_t attn_fwd_tree(const void *q, const attn_kv_cache_t *cache, int lay
                             float *lse, const int *cu, const int *seqs, const int *parents,
                             int n_seqs, int total_q, int Hq, const long long *strides,
                             float scale, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * attn_fwd_tree_window -- attn_fwd_tree with a sliding window; with one token per sequence, the
+ * decoding step over the window.
+ *
+ * A token with d ancestors in its tree stands at position pos = base + d, base being the number
+ * of positions before the tree, and sees what a sequence of those before the tree, its ancestors
+ * and itself would show it: positions before the tree j > pos - window or j < sinks; itself and
+ * its nearest window - 1 ancestors; and ancestors that stand at a position below sinks.
+ *
+ * window  at least 1; one of table_width * page or more is attn_fwd_tree.  sinks: at least 0.
+ * Positions count the rows that the cache holds: where attn_kv_evict has cut a sequence, its
+ * rows have moved up.  Of the pages, those that hold a part of a run of 128 positions (from a
+ * multiple of 128) of which some token sees one are read; the others may be missing.
+ * Everything else: as attn_fwd_tree; ATTN_ERR_SHAPE also for window < 1 or sinks < 0.
+ */
+attn_status_t attn_fwd_tree_window(const void *q, const attn_kv_cache_t *cache, int layer, void *o,
+                                   float *lse, const int *cu, const int *seqs, const int *parents,
+                                   int n_seqs, int total_q, int Hq, const long long *strides,
+                                   float scale, int window, int sinks, void *workspace,
+                                   size_t workspace_bytes, void *stream);
 
 /* Static, human-readable name of a status code. */
 const char *attn_status_str(attn_status_t status);
