@@ -103,6 +103,10 @@ def load(path: str | None = None):
         lib.attn_kv_free.restype = i
         lib.attn_kv_compact.argtypes = [pc, vp, vp]
         lib.attn_kv_compact.restype = i
+        lib.attn_kv_weigh.argtypes = [pc, i, vp, vp, vp, vp, vp, i, i, i, vp, ctypes.c_float, i, vp]
+        lib.attn_kv_weigh.restype = i
+        lib.attn_kv_evict.argtypes = [pc, vp, i, vp, i, i, i, vp]
+        lib.attn_kv_evict.restype = i
         lib.attn_test_force_splits.argtypes = [i]
         lib.attn_test_force_splits.restype = None
         lib.attn_status_str.argtypes = [i]
@@ -343,7 +347,7 @@ def attention(q, k, v, causal: bool = True, scale: float | None = None, with_lse
 
 
 # ------------------------------------------------------------------ packed sequences
-_Strides4, _Strides8 = ctypes.c_longlong * 4, ctypes.c_longlong * 8
+_Strides2, _Strides4, _Strides8 = (ctypes.c_longlong * n for n in (2, 4, 8))
 
 
 def _strides(values):
@@ -457,13 +461,18 @@ def _outputs(q, dev, Hq, total, with_lse, out, lse_out, stream):
     return out, lse_out
 
 
+def _c_int(x):
+    """A count as a C int: one beyond its range is as good as the largest, or as -1."""
+    return max(-1, min(int(x), 0x7FFFFFFF))
+
+
 def _window(window, sinks):
-    """The window and the first keys as C ints (a longer window than an int holds has no end either)."""
+    """The window and the first keys as C ints."""
     if window is None:
         if sinks != 0:
             raise ValueError("sinks are the first keys that a window leaves visible: they need a window")
         return None, 0
-    return min(int(window), 0x7FFFFFFF), min(int(sinks), 0x7FFFFFFF)
+    return _c_int(window), _c_int(sinks)
 
 
 def attention_varlen(q, k, v, cu_q, cu_k=None, causal: bool = True, scale: float | None = None,
@@ -560,6 +569,14 @@ class KVPages:
                          n_pages, page, Hkv, D, self.n_rows, self.table_width, _dtype_code(k.dtype))
         self.ref = ctypes.byref(self.c)
 
+    def weights(self):
+        """Sums of attention weights for kv_weigh and kv_evict, all zero: fp32 [n_layers, n_rows, Hkv,
+        table_width * page]."""
+        import torch
+
+        return torch.zeros((self.n_layers, self.n_rows, self.Hkv, self.table_width * self.page), dtype=torch.float32,
+                           device=self.device)
+
     @classmethod
     def empty(cls, n_layers, n_pages, Hkv, page, D, n_rows, table_width, dtype, device="cuda"):
         """A cache without sequences (pool contents undefined)."""
@@ -612,6 +629,21 @@ def attn_kv_free(cache, seqs, n, stream=None) -> int:
 def attn_kv_compact(cache, live, stream=None) -> int:
     """The C entry point with the same name; returns its status code."""
     return load().attn_kv_compact(_c(cache), _ptr(live), _stream_handle(stream))
+
+
+def attn_kv_weigh(cache, layer, q, lse, weights, cu, seqs, n, total_q, Hq, strides, scale, accumulate,
+                  stream=None) -> int:
+    """The C entry point with the same name; returns its status code.  ``strides``: None or 2
+    element strides."""
+    return load().attn_kv_weigh(_c(cache), int(layer), _ptr(q), _ptr(lse), _ptr(weights), _ptr(cu), _ptr(seqs), int(n),
+                                int(total_q), int(Hq), _strides(strides), float(scale), int(bool(accumulate)),
+                                _stream_handle(stream))
+
+
+def attn_kv_evict(cache, seqs, n, weights, sinks, heavy, recent, stream=None) -> int:
+    """The C entry point with the same name; returns its status code."""
+    return load().attn_kv_evict(_c(cache), _ptr(seqs), int(n), _ptr(weights), int(sinks), int(heavy), int(recent),
+                                _stream_handle(stream))
 
 
 def attn_fwd_tree_workspace(n_seqs, D):
@@ -714,6 +746,46 @@ def kv_compact(cache, live=None, stream=None):
         _ints(live, "live", cache.dev, (1,))
     _run("attn_kv_compact", cache.dev, stream, load().attn_kv_compact, cache.ref, live.data_ptr())
     return live
+
+
+def _weights(t, cache):
+    _same(t, "weights", _torch().float32, cache.dev)
+    shape = (cache.n_layers, cache.n_rows, cache.Hkv, cache.table_width * cache.page)
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"weights must be contiguous {list(shape)}")
+    return t
+
+
+def kv_weigh(cache, weights, q, lse, cu, seqs=None, layer: int = 0, scale: float | None = None,
+             accumulate: bool = True, stream=None):
+    """attn_kv_weigh: adds to ``weights`` (KVPages.weights) the attention weight that each position
+    receives from the sequences' last tokens, whose queries are q [total,Hq,D] (offsets ``cu`` [n + 1])
+    and whose attention over all positions gave ``lse`` [Hq,total]."""
+    (total, Hq, D), sq = _rows(q, "q")
+    dev = cache.dev
+    _same(q, "q", cache.dtype, dev)
+    if D != cache.D or Hq % cache.Hkv != 0:
+        raise ValueError("q must be [total, Hq, D] with the cache's D and Hq a multiple of its Hkv")
+    _same(lse, "lse", _torch().float32, dev)
+    if lse.shape != (Hq, total) or not lse.is_contiguous():
+        raise ValueError(f"lse must be contiguous [{Hq}, {total}]")
+    _weights(weights, cache)
+    n = _list(cu, "cu", cache) - 1
+    _list(seqs, "seqs", cache, n)
+    _run("attn_kv_weigh", dev, stream, load().attn_kv_weigh, cache.ref, layer, q.data_ptr(), lse.data_ptr(),
+         weights.data_ptr(), cu.data_ptr(), _ptr(seqs), n, total, Hq, _Strides2(sq[0], sq[1]),
+         D ** -0.5 if scale is None else scale, 1 if accumulate else 0)
+
+
+def kv_evict(cache, seqs=None, weights=None, sinks: int = 0, heavy: int = 0, recent: int = 0, stream=None):
+    """attn_kv_evict: sequences (all rows, when ``seqs`` is None) of more than sinks + heavy + recent positions
+    keep, in each layer and kv head, their first ``sinks``, their last ``recent`` and the ``heavy`` others with
+    the largest ``weights`` (KVPages.weights; None only when heavy is 0)."""
+    n = cache.n_rows if seqs is None else _list(seqs, "seqs", cache)
+    if weights is not None:
+        _weights(weights, cache)
+    _run("attn_kv_evict", cache.dev, stream, load().attn_kv_evict, cache.ref, _ptr(seqs), n, _ptr(weights), _c_int(sinks),
+         _c_int(heavy), _c_int(recent))
 
 
 _tree_bytes = {}  # (device number, sequences, D) -> bytes of attn_fwd_tree_workspace

@@ -5,7 +5,9 @@
 
 #include "attn_fwd_tree.cuh"
 #include "attn_fwd_varlen.cuh"
+#include "kv_evict.cuh"
 #include "kv_pages.cuh"
+#include "kv_weigh.cuh"
 
 namespace {
 
@@ -124,6 +126,15 @@ attn_status_t launch_tree(int dev, int kid, const CUtensorMap &tq, const CUtenso
                                 s, prm);
     constexpr unsigned per_cta = gqa::kBM / gqa::kMergeCtaRows;
     return launch_dependent(gqa::attn_tree_merge_ctas_kernel<D, BF16>, grid * per_cta, gqa::kMergeCtaThreads, 0, s, prm);
+}
+
+template <int D, bool BF16>
+attn_status_t launch_weigh(int dev, int kid, const CUtensorMap &tq, const CUtensorMap &tf, const CUtensorMap &tk,
+                           const gqa::WeighParams &prm, unsigned grid, cudaStream_t s) {
+    auto kern = gqa::kv_weigh_kernel<D, BF16>;
+    constexpr int smem = gqa::WeighLayout<D>::kAlloc;
+    if (attn_status_t st = set_smem_limit(dev, 44 + kid, kern, smem); st != ATTN_OK) return st;
+    return launch_dependent(kern, grid, gqa::kWgThreads, smem, s, tq, tf, tk, prm);
 }
 
 // Least weight of a CTA's share in the tree kernel (a unit weighs its key tiles and two more).
@@ -531,6 +542,89 @@ attn_status_t attn_kv_free(const attn_kv_cache_t *cache, const int *seqs, int n,
     const long long blocks = (static_cast<long long>(n) * cache->table_width + 255) / 256, most = 4ll * g_dev_sms[dev];
     return launch_dependent(gqa::kv_free_kernel, static_cast<unsigned>(blocks < most ? blocks : most), 256, 0,
                             static_cast<cudaStream_t>(stream), pool_of(cache), seqs, n);
+}
+
+attn_status_t attn_kv_weigh(const attn_kv_cache_t *cache, int layer, const void *q, const float *lse, float *weights,
+                            const int *cu, const int *seqs, int n, int total_q, int Hq, const long long *strides,
+                            float scale, int accumulate, void *stream) {
+    int dev = 0;
+    bool empty = false;
+    if (attn_status_t st = check_list(cache, n, empty); st != ATTN_OK || empty) return st;
+    const int Hkv = cache->Hkv, D = cache->D;
+    if (layer < 0 || layer >= cache->n_layers || total_q < 0 || Hq < 1 || Hq % Hkv != 0 || Hq / Hkv > 128)
+        return ATTN_ERR_SHAPE;
+    if (!(std::isfinite(scale) && scale > 0.f)) return ATTN_ERR_SHAPE;
+    if (total_q == 0) return ATTN_OK;
+    if (!q || !lse || !weights || !cu) return ATTN_ERR_NULL;
+    if (misaligned(q, 16) || misaligned(lse, 4) || misaligned(weights, 4) || misaligned(cu, 4) || misaligned(seqs, 4))
+        return ATTN_ERR_ALIGN;
+    if (n > cache->n_rows) return ATTN_ERR_SHAPE;
+    const long long st[2] = {strides ? strides[0] : static_cast<long long>(Hq) * D, strides ? strides[1] : D};
+    if (!strides_ok(st[0], st[1], total_q, Hq, D)) return ATTN_ERR_SHAPE;
+    // a box of tokens x heads lies token by token in the tile: tokens are the outer axis of q
+    if (total_q > 1 && Hq > 1 && st[0] < st[1]) return ATTN_ERR_SHAPE;
+    // unit numbers are 32-bit
+    const long long width = static_cast<long long>(cache->table_width) * cache->page;
+    if (((width + 255) / 256) * Hkv * n > INT_MAX / 2) return ATTN_ERR_SHAPE;
+    if (attn_status_t e = check_device(&dev); e != ATTN_OK) return e;
+    gqa::WeighParams prm = {};
+    common_params(prm, nullptr, nullptr, Hq, Hkv, scale);
+    const size_t layer_bytes = static_cast<size_t>(cache->n_pages) * Hkv * cache->page * D * 2;
+    prm.cu = cu;
+    prm.seqs = seqs;
+    prm.table = cache->table;
+    prm.lens = cache->lens;
+    prm.lse_in = lse;
+    prm.weights = weights + static_cast<size_t>(layer) * cache->n_rows * Hkv * width;
+    prm.n_seqs = n;
+    prm.total_q = total_q;
+    prm.Hkv = Hkv;
+    prm.n_rows = cache->n_rows;
+    prm.page = cache->page;
+    prm.page_shift = log2_of(cache->page);
+    prm.n_pages = cache->n_pages;
+    prm.table_w = cache->table_width;
+    prm.rt = 128 / prm.group;
+    prm.few = prm.group < gqa::kWgFewRows ? gqa::kWgFewRows / prm.group : 1;
+    prm.accumulate = accumulate != 0 ? 1 : 0;
+    const bool bf16 = cache->dtype == ATTN_BF16;
+    CUtensorMap tq, tf, tk;
+    int head_y = 0;
+    if (!encode_packed_map(&tq, q, bf16, D, total_q, Hq, st[0], st[1], prm.rt, prm.group, &head_y) || head_y != 1 ||
+        !encode_packed_map(&tf, q, bf16, D, total_q, Hq, st[0], st[1], prm.few, prm.group, &head_y) ||
+        !encode_pool_map(&tk, static_cast<const uint8_t *>(cache->k) + layer * layer_bytes, bf16, D, cache->page,
+                         static_cast<long long>(cache->n_pages) * Hkv))
+        return no_map();
+    const long long most = ((width + 255) / 256) * Hkv * n;
+    const unsigned grid = static_cast<unsigned>(most < g_dev_sms[dev] ? most : g_dev_sms[dev]);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int kid = (D == 128 ? 2 : 0) + (bf16 ? 1 : 0);
+    switch (kid) {
+        case 0: return launch_weigh<64, false>(dev, kid, tq, tf, tk, prm, grid, s);
+        case 1: return launch_weigh<64, true>(dev, kid, tq, tf, tk, prm, grid, s);
+        case 2: return launch_weigh<128, false>(dev, kid, tq, tf, tk, prm, grid, s);
+        default: return launch_weigh<128, true>(dev, kid, tq, tf, tk, prm, grid, s);
+    }
+}
+
+attn_status_t attn_kv_evict(const attn_kv_cache_t *cache, const int *seqs, int n, float *weights, int sinks, int heavy,
+                            int recent, void *stream) {
+    int dev = 0;
+    bool empty = false;
+    if (attn_status_t st = check_list(cache, n, empty); st != ATTN_OK || empty) return st;
+    if (n > cache->n_rows || sinks < 0 || heavy < 0 || recent < 0) return ATTN_ERR_SHAPE;
+    if (heavy > 0 && !weights) return ATTN_ERR_NULL;
+    if (misaligned(seqs, 4) || misaligned(weights, 4)) return ATTN_ERR_ALIGN;
+    const long long blocks = static_cast<long long>(n) * cache->n_layers * cache->Hkv;
+    if (blocks > INT_MAX) return ATTN_ERR_SHAPE;
+    if (attn_status_t st = check_device(&dev); st != ATTN_OK) return st;
+    const gqa::KvEvict x = {seqs, weights, n, sinks, heavy, recent, static_cast<long long>(sinks) + heavy + recent};
+    const gqa::KvPool p = pool_of(cache);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (attn_status_t st = launch_dependent(gqa::kv_evict_kernel, static_cast<unsigned>(blocks), gqa::kEvThreads, 0, s, p, x);
+        st != ATTN_OK)
+        return st;
+    return launch_dependent(gqa::kv_evict_end_kernel, static_cast<unsigned>(n), 256, 0, s, p, x);
 }
 
 attn_status_t attn_kv_compact(const attn_kv_cache_t *cache, int *live, void *stream) {

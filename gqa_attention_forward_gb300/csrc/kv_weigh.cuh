@@ -1,0 +1,507 @@
+// The weight that each cached position receives (attn_kv_weigh): what an eviction by accumulated
+// attention weight goes by.
+//
+// For the last T_s positions of sequence s, whose queries are packed rows [cu[s], cu[s+1]), and
+// their attention's log-sum-exp, the call adds to the sums of every kv head
+//   w_j (+)= sum_{t, g} exp(scale q_{t,g}.k_j - lse_{t,g})   over tokens t at or behind j
+// and the G query heads of the kv head: the column sums of the softmax whose row sums are 1, which
+// the online softmax of the page "从零开始写Qwen3" (deepseek.csdn.net/6a3201f8..., section
+// "在线softmax") never holds.
+//
+// What bounds it: with few tokens HBM (K is read once, 2 D G T flops per key); with whole prompts
+// the tensor cores and the exponentials alike (2 D flops and one exp2 per row and key, of which an
+// SM does about 8192 and 32 a cycle: 512 cycles of each for 128 keys and 128 rows).
+//
+// The product is taken transposed, S^T = K Q^T: a TMEM lane, and so a thread, owns a key, and the
+// sum over the rows is a sum over a thread's own columns, without shuffles, atomics or a second
+// pass; the rows' log-sum-exps are the same for all threads and come from shared memory.  A unit is
+// 256 keys of a kv head (two 128-key tiles that share every Q tile, one warpgroup each) against all
+// row tiles that see one of them, so that every position's sum has one owner and a fixed order.
+// Row tiles hold 128 / G tokens (row = token * G + head in the group).
+//
+// Units go in the order of the sequences, the first keys (which most tokens see) first, the kv
+// heads next to each other, and are dealt to the CTAs in snake order.
+//
+// Roles (384 threads): warp 0 MMA issuer, warp 1 TMA producer of Q, and the rows' log-sum-exps,
+// warp 2 TMA producer of K (the lanes issue one page box each), warp 3 scheduler (and TMEM),
+// warps 4-7 and 8-11 the sums of key tile 0 and 1.  K has two buffers of a unit, Q a ring of
+// three tiles.  TMEM: S^T of tile a, buffer b in columns [256 a + 128 b, + 128).
+#pragma once
+#include <cuda.h>  // CUtensorMap
+
+#include "attn_fwd_tree.cuh"
+#include "kernel_common.cuh"
+
+namespace gqa {
+
+constexpr int kWgThreads = 384;
+constexpr int kWgQStages = 3, kWgSlots = 3, kWgLse = 3;
+constexpr int kWgFewRows = 16;  // rows of the small Q box: with few tokens a full one is 32 KB beside 64 KB of K
+
+struct WeighParams : Params {
+    const int *cu, *table, *lens, *seqs;
+    const float *lse_in;
+    float *weights;  // of the layer: [n_rows][Hkv][positions]
+    int n_seqs, total_q, Hkv, n_rows;
+    int page, page_shift, n_pages, table_w;
+    int rt, few;     // tokens of a row tile, of the small box
+    int accumulate;
+};
+
+struct WeighUnit {
+    int valid;
+    int row, kvh;
+    int key0, L;    // first key of the unit, positions of the sequence
+    int q0, T;      // packed row of the first token, tokens
+    int base;       // positions before the tokens
+    int m0, m1;     // row tiles
+};
+
+template <int D>
+struct WeighLayout {
+    static constexpr int kTileBytes = (D / 64) * kAtomBytes;
+    static constexpr int kK = 0;  // two buffers of two tiles
+    static constexpr int kQ = kK + 4 * kTileBytes;
+    static constexpr int kLse = kQ + kWgQStages * kTileBytes;
+    static constexpr int kBar = kLse + kWgLse * 512;
+    // k_full[2], k_empty[2], q_full[S], q_empty[S], l_full[S], l_empty[S], s_full[2][2], s_empty[2][2], mma_done,
+    // unit_full[slots], unit_empty[slots]
+    static constexpr int kNumBars = 4 + 2 * kWgQStages + 2 * kWgLse + 8 + 1 + 2 * kWgSlots;
+    static constexpr int kTmemSlot = kBar + kNumBars * 8;
+    static constexpr int kAbort = kTmemSlot + 4;
+    static constexpr int kUnits = kAbort + 4;
+    static constexpr int kUsed = kUnits + kWgSlots * static_cast<int>(sizeof(WeighUnit));
+    // more than half of an SM's shared memory: one CTA (all 512 TMEM columns) per SM
+    static constexpr int kAlloc = (kUsed + 1024) > 118 * 1024 ? (kUsed + 1024) : 118 * 1024;
+};
+static_assert(WeighLayout<128>::kAlloc <= 227 * 1024, "shared memory of one CTA");
+
+// 4-byte global -> shared copy.
+__device__ __forceinline__ void cp_async_4(uint32_t dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// S^T = K Q^T of 128 keys and N rows (K-major operands).
+template <int D, int kk = 0>
+__device__ __forceinline__ void mma_kq(uint32_t td, uint32_t k_lo, uint32_t q_lo, uint32_t idesc) {
+    if constexpr (kk < D / 16) {
+        constexpr uint32_t off = (kk >> 2) * (kAtomBytes >> 4) + (kk & 3) * 2;
+        const uint64_t hi = static_cast<uint64_t>(kDescHi) << 32;
+        mma_f16_ss(td, hi | (k_lo + off), hi | (q_lo + off), idesc, kk > 0 ? 1u : 0u);
+        mma_kq<D, kk + 1>(td, k_lo, q_lo, idesc);
+    }
+}
+
+// tmQ: 3-D tensor map (D, Hq, tokens), box 64 x G x rt; tmF the same with a box of `few` tokens; tmK: 3-D map
+// (D, page, n_pages * Hkv), box 64 x min(page, 128) x 1; all with the 128-byte swizzle.
+template <int D, bool kBF16>
+__global__ void __launch_bounds__(kWgThreads, 1)
+    kv_weigh_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmF,
+                    const __grid_constant__ CUtensorMap tmK, const __grid_constant__ WeighParams p) {
+    using L = WeighLayout<D>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t *smem = smem_raw + (base - raw);
+    const uint32_t sK = base + L::kK, sQ = base + L::kQ, sL = base + L::kLse;
+    const uint32_t bar0 = base + L::kBar;
+    constexpr int QS = kWgQStages, LS = kWgLse;
+    auto k_full = [&](int b) { return bar0 + 8u * b; };
+    auto k_empty = [&](int b) { return bar0 + 8u * (2 + b); };
+    auto q_full = [&](int s) { return bar0 + 8u * (4 + s); };
+    auto q_empty = [&](int s) { return bar0 + 8u * (4 + QS + s); };
+    auto l_full = [&](int s) { return bar0 + 8u * (4 + 2 * QS + s); };
+    auto l_empty = [&](int s) { return bar0 + 8u * (4 + 2 * QS + LS + s); };
+    auto s_full = [&](int a, int b) { return bar0 + 8u * (4 + 2 * QS + 2 * LS + 2 * a + b); };
+    auto s_empty = [&](int a, int b) { return bar0 + 8u * (8 + 2 * QS + 2 * LS + 2 * a + b); };
+    const uint32_t mma_done = bar0 + 8u * (12 + 2 * QS + 2 * LS);
+    auto unit_full = [&](int s) { return bar0 + 8u * (13 + 2 * QS + 2 * LS + s); };
+    auto unit_empty = [&](int s) { return bar0 + 8u * (13 + 2 * QS + 2 * LS + kWgSlots + s); };
+    volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(smem + L::kTmemSlot);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kAbort);
+    WeighUnit *units = reinterpret_cast<WeighUnit *>(smem + L::kUnits);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    grid_launch_dependents();
+    if (threadIdx.x == 32) {
+        tma_prefetch_map(&tmQ);
+        tma_prefetch_map(&tmF);
+        tma_prefetch_map(&tmK);
+    }
+    if (threadIdx.x == 0) {
+        *abort_flag = 0;
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(k_full(b), 1);
+            mbar_init(k_empty(b), 1);
+            for (int a = 0; a < 2; ++a) {
+                mbar_init(s_full(a, b), 1);
+                mbar_init(s_empty(a, b), 4);  // one arrival per warp of the tile
+            }
+        }
+        for (int s = 0; s < QS; ++s) {
+            mbar_init(q_full(s), 1);
+            mbar_init(q_empty(s), 1);
+        }
+        for (int s = 0; s < LS; ++s) {
+            mbar_init(l_full(s), 32);  // the copies of each lane
+            mbar_init(l_empty(s), 8);
+        }
+        mbar_init(mma_done, 1);
+        for (int s = 0; s < kWgSlots; ++s) {
+            mbar_init(unit_full(s), 1);
+            mbar_init(unit_empty(s), 11);  // K, Q, MMA issuer, 8 warps of sums
+        }
+        fence_mbar_init();
+    }
+    if (warp == 3) {
+        tmem_alloc(base + L::kTmemSlot, 512);
+        tmem_relinquish();
+    }
+    // the set-up above overlaps the kernel before this one; its results are read from here on
+    grid_dependency_wait();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    // a role's place in the units' slots
+    struct Place {
+        int slot = 0;
+        uint32_t phase = 0;
+        __device__ __forceinline__ void next() {
+            if (++slot == kWgSlots) {
+                slot = 0;
+                phase ^= 1u;
+            }
+        }
+    };
+    auto tiles_of = [&](const WeighUnit &u) { return u.L - u.key0 > kBN ? 2 : 1; };
+
+    if (warp == 3) {
+        // -------------------------------------------------------- scheduler
+        // 32 sequences at a time, a lane each: where they are, their blocks of 256 keys, units before them
+        int s0 = -32, T = 0, len = 0, row = -1, q0 = 0, blocks = 0, incl = 0;
+        int before = 0, batch = 0;      // units before the 32, and of them
+        long long tokens = 0;           // of the sequences before the 32
+        bool bad = false;
+        auto load = [&]() {
+            s0 += 32;
+            before += batch;
+            const int s = s0 + lane;
+            T = blocks = 0;
+            long long upto = 0;
+            if (s < p.n_seqs) {
+                const VlSpan q = vl_span(p.cu, s, p.total_q);
+                row = p.seqs != nullptr ? p.seqs[s] : s;
+                q0 = q.a;
+                T = q.b - q.a;
+                const bool in = row >= 0 && row < p.n_rows;
+                len = in ? p.lens[row] : 0;
+                // a sequence named before in the list would be added to by two units at once
+                bool again = false;
+                if (p.seqs != nullptr)
+                    for (int j = 0; j < s; ++j) again |= p.seqs[j] == row;
+                if (q.bad || !in || again || len < T || len > (static_cast<long long>(p.table_w) << p.page_shift)) {
+                    bad = true;
+                    T = 0;
+                }
+                upto = T;
+            }
+            // offsets that descend can overlap: no more rows than ascending ones can have
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long y = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += y;
+            }
+            if (T > 0 && tokens + upto > p.total_q) {
+                bad = true;
+                T = 0;
+            }
+            tokens += __shfl_sync(0xffffffffu, upto, 31);
+            if (T > 0) blocks = (len + 2 * kBN - 1) / (2 * kBN);
+            incl = blocks * p.Hkv;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += y;
+            }
+            batch = __shfl_sync(0xffffffffu, incl, 31);
+        };
+        load();
+        Place at;
+        for (unsigned r = 0;; ++r) {
+            const unsigned c = (r & 1u) ? (gridDim.x - 1u - blockIdx.x) : blockIdx.x;
+            const int t = static_cast<int>(r * gridDim.x + c);
+            while (s0 < p.n_seqs && t >= before + batch) load();
+            const bool more = s0 < p.n_seqs;
+            if (!__all_sync(0xffffffffu, wait_bar(unit_empty(at.slot), at.phase ^ 1u, p, abort_flag))) break;
+            if (more) {
+                const int src = __ffs(__ballot_sync(0xffffffffu, before + incl > t)) - 1;
+                if (lane == src) {
+                    const int in = t - before - (incl - blocks * p.Hkv);
+                    WeighUnit &u = units[at.slot];
+                    u.valid = 1;
+                    u.row = row;
+                    u.kvh = in % p.Hkv;
+                    u.key0 = in / p.Hkv * (2 * kBN);
+                    u.L = len;
+                    u.q0 = q0;
+                    u.T = T;
+                    u.base = len - T;
+                    u.m0 = u.key0 > u.base ? (u.key0 - u.base) / p.rt : 0;
+                    u.m1 = (T + p.rt - 1) / p.rt;
+                }
+            } else if (lane == 0) {
+                units[at.slot].valid = 0;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(unit_full(at.slot));
+            if (!more) break;
+            at.next();
+        }
+        if (__any_sync(0xffffffffu, bad) && lane == 0) atomicCAS(&g_error_code, 0, static_cast<int>(ATTN_ERR_SHAPE));
+    } else if (warp == 2) {
+        // -------------------------------------------------------- TMA producer of K
+        constexpr int kAtoms = D / 64;
+        const int box_rows = p.page < kBN ? p.page : kBN;
+        const int boxes = (kBN / box_rows) * kAtoms;  // per tile, at most 16
+        // lane b issues box b: atom b % kAtoms of page piece b / kAtoms of the unit's keys
+        const int piece = lane / kAtoms, a = lane % kAtoms, key = piece * box_rows;
+        Place at;
+        int n = 0, kvh = 0, tiles = 0, page = 0, first = 0, L0 = 0;
+        bool valid = false;
+        auto take = [&]() -> bool {
+            if (!__all_sync(0xffffffffu, wait_bar(unit_full(at.slot), at.phase, p, abort_flag))) return false;
+            const WeighUnit &u = units[at.slot];
+            valid = u.valid != 0;
+            if (valid) {
+                kvh = u.kvh;
+                tiles = tiles_of(u);
+                first = u.key0;
+                L0 = u.L;
+                page = lane < boxes * tiles && first + key < L0
+                    ? p.table[static_cast<long long>(u.row) * p.table_w + ((first + key) >> p.page_shift)] : -1;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(unit_empty(at.slot));
+            at.next();
+            return true;
+        };
+        bool ok = take();
+        for (; ok && valid; ++n) {
+            const int b = n & 1;
+            if (!(ok = __all_sync(0xffffffffu, wait_bar(k_empty(b), ((n >> 1) & 1u) ^ 1u, p, abort_flag)))) break;
+            if (lane == 0) mbar_arrive_expect_tx(k_full(b), static_cast<uint32_t>(tiles * L::kTileBytes));
+            __syncwarp();
+            if (lane < boxes * tiles) {
+                int e = page;
+                if (e < 0 || e >= p.n_pages) {
+                    if (first + key < L0) atomicCAS(&g_error_code, 0, static_cast<int>(ATTN_ERR_PAGE));
+                    e = p.n_pages;  // one past the last: reads as zeros
+                }
+                const int tile = key / kBN;
+                tma_load_3d(sK + (2 * b + tile) * L::kTileBytes + a * kAtomBytes + (key & (kBN - 1)) * 128, &tmK, 64 * a,
+                            (first + key) & (p.page - 1), e * p.Hkv + (e < p.n_pages ? kvh : 0), k_full(b));
+            }
+            __syncwarp();
+            ok = take();
+        }
+        if (lane == 0) {
+            // every copy has landed before the CTA exits (also after a timeout)
+            if (n > 0) drain_bar(k_full((n - 1) & 1), ((n - 1) >> 1) & 1, p);
+            if (n > 1) drain_bar(k_full(n & 1), ((n - 2) >> 1) & 1, p);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // -------------------------------------------------------- TMA producer of Q, log-sum-exps
+        Place at;
+        int s = 0, ls = 0, loads = 0;
+        uint32_t ph = 0, lph = 0;
+        bool ok = true;
+        while (ok) {
+            if (!(ok = __all_sync(0xffffffffu, wait_bar(unit_full(at.slot), at.phase, p, abort_flag)))) break;
+            const WeighUnit u = units[at.slot];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(unit_empty(at.slot));
+            at.next();
+            if (!u.valid) break;
+            for (int m = u.m0; m < u.m1; ++m) {
+                const int tok0 = u.q0 + m * p.rt, left = u.T - m * p.rt;
+                if (!(ok = __all_sync(0xffffffffu, wait_bar(q_empty(s), ph ^ 1u, p, abort_flag)))) break;
+                if (!p.inject_stall) {
+                    if (lane == 0) {
+                        const bool few = left <= p.few;
+                        mbar_arrive_expect_tx(q_full(s), static_cast<uint32_t>(p.group * (few ? p.few : p.rt)) * D * 2);
+#pragma unroll
+                        for (int x = 0; x < D / 64; ++x)
+                            tma_load_3d(sQ + s * L::kTileBytes + x * kAtomBytes, few ? &tmF : &tmQ, 64 * x, u.kvh * p.group,
+                                        tok0, q_full(s));
+                    }
+                    ++loads;
+                }
+                if (!(ok = __all_sync(0xffffffffu, wait_bar(l_empty(ls), lph ^ 1u, p, abort_flag)))) break;
+                const int rows = (left < p.rt ? left : p.rt) * p.group;
+                for (int r = lane; r < rows; r += 32) {
+                    const int t = r / p.group, g = r - t * p.group;
+                    cp_async_4(sL + ls * 512 + r * 4,
+                               p.lse_in + static_cast<size_t>(u.kvh * p.group + g) * p.total_q + tok0 + t);
+                }
+                cp_async_arrive(l_full(ls));
+                if (++s == QS) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+                if (++ls == LS) {
+                    ls = 0;
+                    lph ^= 1u;
+                }
+            }
+        }
+        cp_async_commit();
+        cp_async_wait<0>();
+        if (lane == 0)
+            for (int st = 0; st < QS; ++st)  // the last load of each stage
+                if (loads > st) drain_bar(q_full(st), ((loads - 1 - st) / QS) & 1, p);
+        __syncwarp();
+    } else if (warp == 0) {
+        if (lane == 0) {
+            // ---------------------------------------------------- MMA issuer
+            const uint32_t dk = desc_lo(sK, 16), dq = desc_lo(sQ, 16);
+            constexpr uint32_t kTile16 = L::kTileBytes >> 4;
+            Place at;
+            int s = 0, n = 0;
+            uint32_t ph = 0, steps[2] = {0, 0};
+            bool ok = true;
+            while (ok) {
+                if (!(ok = wait_bar(unit_full(at.slot), at.phase, p, abort_flag))) break;
+                const WeighUnit &us = units[at.slot];
+                const int valid = us.valid, m0 = us.m0, m1 = us.m1, T = us.T, tiles = tiles_of(us);
+                mbar_arrive(unit_empty(at.slot));
+                at.next();
+                if (!valid) break;
+                const int b = n & 1;
+                if (!(ok = wait_bar(k_full(b), (n >> 1) & 1u, p, abort_flag))) break;
+                for (int m = m0; m < m1 && ok; ++m) {
+                    if (!(ok = wait_bar(q_full(s), ph, p, abort_flag))) break;
+                    const int left = T - m * p.rt, rows = (left < p.rt ? left : p.rt) * p.group;
+                    const uint32_t idesc = idesc_f16_f32acc(kBF16, 128, (rows + 15) & ~15, false);
+#pragma unroll
+                    for (int a = 0; a < 2; ++a) {
+                        if (a >= tiles) break;
+                        const uint32_t sb = steps[a] & 1u;
+                        if (!(ok = wait_bar(s_empty(a, sb), ((steps[a] >> 1) & 1u) ^ 1u, p, abort_flag))) break;
+                        ++steps[a];
+                        tc_fence_after();
+                        mma_kq<D>(tmem + 256u * a + 128u * sb, dk + (2 * b + a) * kTile16, dq + s * kTile16, idesc);
+                        mma_commit(s_full(a, sb));
+                    }
+                    if (!ok) break;
+                    mma_commit(q_empty(s));
+                    if (++s == QS) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                }
+                mma_commit(k_empty(b));
+                ++n;
+            }
+            // TMEM and shared memory stay alive until every issued MMA is done.
+            mma_commit(mma_done);
+            drain_bar(mma_done, 0, p);
+        }
+        __syncwarp();
+    } else {
+        // -------------------------------------------------------- sums, a key per thread
+        const int a = (warp - 4) >> 2, wq = warp & 3;
+        const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
+        const float c = p.scale_log2;
+        const float2 c2 = make_float2(c, c), nl2 = make_float2(-1.4426950408889634f, -1.4426950408889634f);
+        const long long width = static_cast<long long>(p.table_w) << p.page_shift;
+        Place at;
+        uint32_t steps = 0, lph = 0;
+        int ls = 0;
+        bool ok = true;
+        while (ok) {
+            if (!(ok = __all_sync(0xffffffffu, wait_bar(unit_full(at.slot), at.phase, p, abort_flag)))) break;
+            const WeighUnit u = units[at.slot];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(unit_empty(at.slot));
+            at.next();
+            if (!u.valid) break;
+            const int warp_key = u.key0 + kBN * a + 32 * wq, key = warp_key + lane;
+            const bool mine = a < tiles_of(u), real = key < u.L;
+            float *w = p.weights + (static_cast<long long>(u.row) * p.Hkv + u.kvh) * width + key;
+            // the sum so far is on its way while the scores are computed; a new token's position begins here
+            float old = 0.f;
+            if (p.accumulate && real && key < u.base) old = *w;
+            float sum = 0.f;
+            for (int m = u.m0; m < u.m1; ++m) {
+                const uint32_t lse = sL + ls * 512;
+                const uint32_t sb = steps & 1u;
+                if (!(ok = __all_sync(0xffffffffu, wait_bar(l_full(ls), lph, p, abort_flag)))) break;
+                if (mine) {
+                    if (!(ok = __all_sync(0xffffffffu, wait_bar(s_full(a, sb), (steps >> 1) & 1u, p, abort_flag)))) break;
+                    ++steps;
+                    tc_fence_after();
+                    __syncwarp();
+                    const uint32_t tS = tmem + 256u * a + 128u * sb + lane_off;
+                    const int left = u.T - m * p.rt, cols = (left < p.rt ? left : p.rt) * p.group;
+                    // this key's columns are [c0, cols): those of tokens at or behind it
+                    const int tok0 = u.base + m * p.rt;
+                    auto first_col = [&](int k) -> int {
+                        const int t = k - tok0;
+                        return (t < 0 ? 0 : (t < p.rt ? t : p.rt)) * p.group;
+                    };
+                    const int c0 = first_col(key), c0_low = first_col(warp_key), c0_high = first_col(warp_key + 31);
+                    float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll 1
+                    for (int q = 0; q < cols; q += 32) {
+                        if (c0_low >= q + 32) continue;  // no key of the warp has one of these
+                        uint32_t s[32];
+                        tmem_ld32(tS + q, s);
+                        tmem_ld_wait(s);
+                        const bool whole = c0_high <= q && q + 32 <= cols;
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4) {
+                            const uint4 l4 = ld_shared_v4(lse + (q + e) * 4);
+                            const float2 n0 = fmul2(make_float2(u2f(l4.x), u2f(l4.y)), nl2);
+                            const float2 n1 = fmul2(make_float2(u2f(l4.z), u2f(l4.w)), nl2);
+                            float2 x0 = ffma2(make_float2(u2f(s[e]), u2f(s[e + 1])), c2, n0);
+                            float2 x1 = ffma2(make_float2(u2f(s[e + 2]), u2f(s[e + 3])), c2, n1);
+                            if (!whole) {
+                                // a column that is not this key's adds nothing, whatever it holds
+                                const int d = q + e;
+                                if (d < c0 || d >= cols) x0.x = -INFINITY;
+                                if (d + 1 < c0 || d + 1 >= cols) x0.y = -INFINITY;
+                                if (d + 2 < c0 || d + 2 >= cols) x1.x = -INFINITY;
+                                if (d + 3 < c0 || d + 3 >= cols) x1.y = -INFINITY;
+                            }
+                            acc[0] = fadd2(acc[0], make_float2(ex2_approx(x0.x), ex2_approx(x0.y)));
+                            acc[1] = fadd2(acc[1], make_float2(ex2_approx(x1.x), ex2_approx(x1.y)));
+                        }
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(s_empty(a, sb));
+                    acc[0] = fadd2(acc[0], acc[1]);
+                    sum += acc[0].x + acc[0].y;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(l_empty(ls));
+                if (++ls == LS) {
+                    ls = 0;
+                    lph ^= 1u;
+                }
+            }
+            if (ok && mine && real) *w = old + sum;
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 3) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+}  // namespace gqa

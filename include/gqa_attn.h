@@ -446,6 +446,53 @@ attn_status_t attn_fwd_tree_window(const void *q, const attn_kv_cache_t *cache, 
                                    float scale, int window, int sinks, void *workspace,
                                    size_t workspace_bytes, void *stream);
 
+/*
+ * The weights of cached positions, and eviction by them: a cache of bounded size.
+ *
+ * weights [n_layers][n_rows][Hkv][table_width * page] fp32, device, 4-byte aligned, owned by the
+ * caller: entry j of a sequence's row is the attention weight that its position j has received, in
+ * one layer, from the query heads of one kv head.  The library keeps no copy of it: a program
+ * that forks a sequence copies its row, one that compacts pages need do nothing.
+ *
+ * attn_kv_weigh -- adds what the last T = cu[i+1] - cu[i] positions of sequence seqs[i] (i, when
+ * NULL) pay, a chain of any length up to the whole sequence:
+ *   weights[j] (+)= sum over those tokens t at or behind j, and the Hq / Hkv heads,
+ *                   of exp(scale q_t . k_j - lse_t)
+ * Their queries are packed rows [cu[i], cu[i+1]) of q, their keys are in the cache.
+ *
+ * q           [total_q, Hq, D], cache->dtype, 16-byte aligned; strides: NULL, or 2 element strides
+ *             {row, head}, rows outside heads
+ * lse         [Hq, total_q] fp32: what attn_fwd_varlen or attn_fwd_tree gave for these rows and
+ *             all keys up to their own (of a call with a window the sums would not be weights)
+ * accumulate  the sums of the positions before the T tokens go on where they stood; 0: they begin at
+ *             zero.  Those of the tokens' own positions begin at zero in either case.  Entries
+ *             behind the sequence, and sequences without tokens, are left as they are.
+ * Scores and sums are fp32, each position's in a fixed order: one result for the same inputs.  A
+ * key or query that a pair does not join (a later token, rows behind the end) never matters.
+ * Errors: as attn_fwd_tree; attn_last_device_error reports ATTN_ERR_SHAPE for offsets, lengths
+ * and sequences out of range, T above the sequence's length and a sequence named twice (its first
+ * entry counts), whose weights are then left as they were, and ATTN_ERR_PAGE for a missing page,
+ * whose positions' weights are then undefined.
+ */
+attn_status_t attn_kv_weigh(const attn_kv_cache_t *cache, int layer, const void *q, const float *lse,
+                            float *weights, const int *cu, const int *seqs, int n, int total_q,
+                            int Hq, const long long *strides, float scale, int accumulate,
+                            void *stream);
+
+/* Cuts sequences seqs[i] (i, when NULL) of more than sinks + heavy + recent positions back to
+ * that many.  In every layer and kv head the first `sinks` and the last `recent` stay, and of
+ * those between the `heavy` largest in weights (equal ones: the lowest positions; NaN and negative
+ * ones count as 0), in their order: their rows of K and V and their weights move up, so that a
+ * position's row then differs from head to head, but all have one length.  Weights behind the new
+ * end, up to the old one, become 0; rows there stay as they are; the pages behind it are given back.
+ * weights may be NULL when heavy is 0 (the oldest positions behind the first go).
+ * A sequence of no more positions is left as it is, its pages too.  Pages from that of position
+ * `sinks` to the new end are written and must not be shared (those of whole pages of first positions
+ * may be): ATTN_ERR_PAGE, also for one that is missing up to the old end; ATTN_ERR_SHAPE for a
+ * sequence or length out of range and the second entry of a sequence named twice. */
+attn_status_t attn_kv_evict(const attn_kv_cache_t *cache, const int *seqs, int n, float *weights,
+                            int sinks, int heavy, int recent, void *stream);
+
 /* Static, human-readable name of a status code. */
 const char *attn_status_str(attn_status_t status);
 
