@@ -16,24 +16,33 @@ bool misaligned(const void *ptr, uintptr_t a) { return (reinterpret_cast<uintptr
 // Launch with the dependent-launch attribute: the kernel's set-up overlaps the tail of the
 // kernel before it, for which it waits (griddepcontrol.wait) before it reads memory.
 template <typename... KArgs, typename... Args>
-attn_status_t launch_dependent(void (*kern)(KArgs...), unsigned grid, unsigned block, size_t smem, cudaStream_t s,
-                               Args... args) {
-    cudaLaunchAttribute attr[1];
+attn_status_t launch_clusters(void (*kern)(KArgs...), unsigned grid, unsigned cluster, unsigned block, size_t smem,
+                              cudaStream_t s, Args... args) {
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(block);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 0 ? 2 : 1;  // 0: as the kernel says itself
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
     if (e != cudaSuccess) {
         note_cuda_error(e, "kernel launch");
         return ATTN_ERR_LAUNCH;
     }
     return ATTN_OK;
+}
+template <typename... KArgs, typename... Args>
+attn_status_t launch_dependent(void (*kern)(KArgs...), unsigned grid, unsigned block, size_t smem, cudaStream_t s,
+                               Args... args) {
+    return launch_clusters(kern, grid, 0, block, smem, s, args...);
 }
 
 // A stride pair (elements) of a [rows, heads, D] or [heads, rows, D] tensor: multiples of 8
@@ -396,6 +405,26 @@ attn_status_t run_tree(const void *q, const attn_kv_cache_t *cache, int layer, v
     return ATTN_OK;
 }
 
+// Blocks of a cluster of kv_evict_kernel.  With a choice to make, all of them look for it, and more
+// than one pays only where the sequences, layers and heads leave SMs without work (32 of them, of
+// 65000 positions: 510 us with 1 block, 293, 191, 153 with 2, 4, 8; 512 of 1000 to 8000 111, 115, 150,
+// 220; 256 of 65000 820, 937, 827, 964); without one, more and smaller blocks even out the end (512 of
+// 2000 to 4000: 182, 167, 174, 204; 2560 759, 751, 770, 960).
+unsigned evict_cluster(long long problems, bool choose, int sms) {
+    unsigned c = 1;
+    while (c < gqa::kEvClusterMost && problems * c < (choose ? 1ll : 6ll) * sms) c *= 2;
+    return c;
+}
+
+template <bool CHOOSE>
+attn_status_t launch_evict(int dev, long long problems, const gqa::KvPool &p, const gqa::KvEvict &x, cudaStream_t s) {
+    auto kern = gqa::kv_evict_kernel<CHOOSE>;
+    constexpr int smem = static_cast<int>(sizeof(gqa::EvictShared));
+    if (attn_status_t st = set_smem_limit(dev, 48 + (CHOOSE ? 1 : 0), kern, smem); st != ATTN_OK) return st;
+    const unsigned cluster = evict_cluster(problems, CHOOSE, g_dev_sms[dev]);
+    return launch_clusters(kern, static_cast<unsigned>(problems) * cluster, cluster, gqa::kEvThreads, smem, s, p, x);
+}
+
 }  // namespace
 
 extern "C" {
@@ -615,13 +644,16 @@ attn_status_t attn_kv_evict(const attn_kv_cache_t *cache, const int *seqs, int n
     if (n > cache->n_rows || sinks < 0 || heavy < 0 || recent < 0) return ATTN_ERR_SHAPE;
     if (heavy > 0 && !weights) return ATTN_ERR_NULL;
     if (misaligned(seqs, 4) || misaligned(weights, 4)) return ATTN_ERR_ALIGN;
-    const long long blocks = static_cast<long long>(n) * cache->n_layers * cache->Hkv;
-    if (blocks > INT_MAX) return ATTN_ERR_SHAPE;
+    // one cluster per sequence, layer and kv head; rows of a layer are numbered in 32 bits
+    const long long problems = static_cast<long long>(n) * cache->n_layers * cache->Hkv;
+    if (problems > INT_MAX / gqa::kEvClusterMost ||
+        static_cast<long long>(cache->n_pages) * cache->Hkv * cache->page > 0xFFFFFFFFll)
+        return ATTN_ERR_SHAPE;
     if (attn_status_t st = check_device(&dev); st != ATTN_OK) return st;
     const gqa::KvEvict x = {seqs, weights, n, sinks, heavy, recent, static_cast<long long>(sinks) + heavy + recent};
     const gqa::KvPool p = pool_of(cache);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (attn_status_t st = launch_dependent(gqa::kv_evict_kernel, static_cast<unsigned>(blocks), gqa::kEvThreads, 0, s, p, x);
+    if (attn_status_t st = heavy > 0 ? launch_evict<true>(dev, problems, p, x, s) : launch_evict<false>(dev, problems, p, x, s);
         st != ATTN_OK)
         return st;
     return launch_dependent(gqa::kv_evict_end_kernel, static_cast<unsigned>(n), 256, 0, s, p, x);
