@@ -19,13 +19,17 @@
 // row tiles that see one of them, so that every position's sum has one owner and a fixed order.
 // Row tiles hold 128 / G tokens (row = token * G + head in the group).
 //
-// Units go in the order of the sequences, the first keys (which most tokens see) first, the kv
-// heads next to each other, and are dealt to the CTAs in snake order.
+// Units of up to 32 sequences are dealt to the CTAs by the number of their row tiles, most first (a
+// sequence's blocks of keys have fewer and fewer, so that lane s of the scheduler finds sequence s's
+// block of a level in closed form); more sequences in their order, as a pass over all of them for
+// each level would take too long.
 //
-// Roles (384 threads): warp 0 MMA issuer, warp 1 TMA producer of Q, and the rows' log-sum-exps,
-// warp 2 TMA producer of K (the lanes issue one page box each), warp 3 scheduler (and TMEM),
-// warps 4-7 and 8-11 the sums of key tile 0 and 1.  K has two buffers of a unit, Q a ring of
-// three tiles.  TMEM: S^T of tile a, buffer b in columns [256 a + 128 b, + 128).
+// Roles (640 threads): warp 0 MMA issuer, warp 1 TMA producer of Q, and the rows' log-sum-exps,
+// warp 2 TMA producer of K (the lanes issue one page box each), warp 3 scheduler (and TMEM), and
+// four warpgroups of sums, two to a key tile with 64 columns each (one alone needs 2300 cycles for
+// 128 x 128 scores, mostly its own latencies, the products 504).  K has two buffers of a unit, Q a
+// ring of three tiles.  TMEM: S^T of tile a, buffer b in columns [256 a + 128 b, + 128).  At a
+// unit's end the second warpgroup of a tile hands its sums to the first through a column of its buffer.
 #pragma once
 #include <cuda.h>  // CUtensorMap
 
@@ -34,7 +38,11 @@
 
 namespace gqa {
 
-constexpr int kWgThreads = 384;
+constexpr int kWgThreads = 640;
+constexpr int kWgKeys = 2 * kBN;  // of a unit
+// Units of so many row tiles (the largest) and more are dealt one by one, to up to 256 CTAs.  For 12
+// prompts of 1 to 4096 the longest share is then 64 row tiles and the mean 61; in snake order 82.
+constexpr int kWgGreedy = 4, kWgLoads = 8;
 constexpr int kWgQStages = 3, kWgSlots = 3, kWgLse = 3;
 constexpr int kWgFewRows = 16;  // rows of the small Q box: with few tokens a full one is 32 KB beside 64 KB of K
 
@@ -64,9 +72,9 @@ struct WeighLayout {
     static constexpr int kQ = kK + 4 * kTileBytes;
     static constexpr int kLse = kQ + kWgQStages * kTileBytes;
     static constexpr int kBar = kLse + kWgLse * 512;
-    // k_full[2], k_empty[2], q_full[S], q_empty[S], l_full[S], l_empty[S], s_full[2][2], s_empty[2][2], mma_done,
+    // k_full[2], k_empty[2], q_full[S], q_empty[S], l_full[S], l_empty[S], s_full[2], s_empty[2], x_full[2], mma_done,
     // unit_full[slots], unit_empty[slots]
-    static constexpr int kNumBars = 4 + 2 * kWgQStages + 2 * kWgLse + 8 + 1 + 2 * kWgSlots;
+    static constexpr int kNumBars = 4 + 2 * kWgQStages + 2 * kWgLse + 4 + 2 + 1 + 2 * kWgSlots;
     static constexpr int kTmemSlot = kBar + kNumBars * 8;
     static constexpr int kAbort = kTmemSlot + 4;
     static constexpr int kUnits = kAbort + 4;
@@ -81,7 +89,7 @@ __device__ __forceinline__ void cp_async_4(uint32_t dst, const void *src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 
-// S^T = K Q^T of 128 keys and N rows (K-major operands).
+// S^T = K Q^T of 128 keys and N rows (K-major operands), for few rows; mma_qk with K in Q's place for 128.
 template <int D, int kk = 0>
 __device__ __forceinline__ void mma_kq(uint32_t td, uint32_t k_lo, uint32_t q_lo, uint32_t idesc) {
     if constexpr (kk < D / 16) {
@@ -112,11 +120,12 @@ __global__ void __launch_bounds__(kWgThreads, 1)
     auto q_empty = [&](int s) { return bar0 + 8u * (4 + QS + s); };
     auto l_full = [&](int s) { return bar0 + 8u * (4 + 2 * QS + s); };
     auto l_empty = [&](int s) { return bar0 + 8u * (4 + 2 * QS + LS + s); };
-    auto s_full = [&](int a, int b) { return bar0 + 8u * (4 + 2 * QS + 2 * LS + 2 * a + b); };
-    auto s_empty = [&](int a, int b) { return bar0 + 8u * (8 + 2 * QS + 2 * LS + 2 * a + b); };
-    const uint32_t mma_done = bar0 + 8u * (12 + 2 * QS + 2 * LS);
-    auto unit_full = [&](int s) { return bar0 + 8u * (13 + 2 * QS + 2 * LS + s); };
-    auto unit_empty = [&](int s) { return bar0 + 8u * (13 + 2 * QS + 2 * LS + kWgSlots + s); };
+    auto s_full = [&](int b) { return bar0 + 8u * (4 + 2 * QS + 2 * LS + b); };  // of both tiles
+    auto s_empty = [&](int b) { return bar0 + 8u * (6 + 2 * QS + 2 * LS + b); };
+    auto x_full = [&](int a) { return bar0 + 8u * (8 + 2 * QS + 2 * LS + a); };  // sums have been handed over
+    const uint32_t mma_done = bar0 + 8u * (10 + 2 * QS + 2 * LS);
+    auto unit_full = [&](int s) { return bar0 + 8u * (11 + 2 * QS + 2 * LS + s); };
+    auto unit_empty = [&](int s) { return bar0 + 8u * (11 + 2 * QS + 2 * LS + kWgSlots + s); };
     volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(smem + L::kTmemSlot);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kAbort);
     WeighUnit *units = reinterpret_cast<WeighUnit *>(smem + L::kUnits);
@@ -133,10 +142,9 @@ __global__ void __launch_bounds__(kWgThreads, 1)
         for (int b = 0; b < 2; ++b) {
             mbar_init(k_full(b), 1);
             mbar_init(k_empty(b), 1);
-            for (int a = 0; a < 2; ++a) {
-                mbar_init(s_full(a, b), 1);
-                mbar_init(s_empty(a, b), 4);  // one arrival per warp of the tile
-            }
+            mbar_init(x_full(b), 4);
+            mbar_init(s_full(b), 1);
+            mbar_init(s_empty(b), 16);  // one arrival per warp of sums
         }
         for (int s = 0; s < QS; ++s) {
             mbar_init(q_full(s), 1);
@@ -144,12 +152,12 @@ __global__ void __launch_bounds__(kWgThreads, 1)
         }
         for (int s = 0; s < LS; ++s) {
             mbar_init(l_full(s), 32);  // the copies of each lane
-            mbar_init(l_empty(s), 8);
+            mbar_init(l_empty(s), 16);
         }
         mbar_init(mma_done, 1);
         for (int s = 0; s < kWgSlots; ++s) {
             mbar_init(unit_full(s), 1);
-            mbar_init(unit_empty(s), 11);  // K, Q, MMA issuer, 8 warps of sums
+            mbar_init(unit_empty(s), 19);  // K, Q, MMA issuer, 16 warps of sums
         }
         fence_mbar_init();
     }
@@ -179,10 +187,19 @@ __global__ void __launch_bounds__(kWgThreads, 1)
     if (warp == 3) {
         // -------------------------------------------------------- scheduler
         // 32 sequences at a time, a lane each: where they are, their blocks of 256 keys, units before them
-        int s0 = -32, T = 0, len = 0, row = -1, q0 = 0, blocks = 0, incl = 0;
+        int s0 = -32, T = 0, len = 0, row = -1, q0 = 0, blocks = 0, incl = 0, block0 = 0;
         int before = 0, batch = 0;      // units before the 32, and of them
         long long tokens = 0;           // of the sequences before the 32
         bool bad = false;
+        auto count = [&](int mine) {
+            incl = mine * p.Hkv;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += y;
+            }
+            batch = __shfl_sync(0xffffffffu, incl, 31);
+        };
         auto load = [&]() {
             s0 += 32;
             before += batch;
@@ -217,32 +234,62 @@ __global__ void __launch_bounds__(kWgThreads, 1)
                 T = 0;
             }
             tokens += __shfl_sync(0xffffffffu, upto, 31);
-            if (T > 0) blocks = (len + 2 * kBN - 1) / (2 * kBN);
-            incl = blocks * p.Hkv;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += y;
-            }
-            batch = __shfl_sync(0xffffffffu, incl, 31);
+            if (T > 0) blocks = (len + kWgKeys - 1) / kWgKeys;
+            count(blocks);
         };
         load();
+        // the levels of up to 32 sequences: a lane's blocks [block0, block0 + on) are on the level
+        const bool levels = p.n_seqs <= 32;
+        const int all = blocks, tiles = (T + p.rt - 1) / p.rt, old = len - T;
+        int level = INT_MAX, on = blocks;
+        auto tiles_of_block = [&](int b) { return tiles - (b * kWgKeys > old ? (b * kWgKeys - old) / p.rt : 0); };
+        // the first block of fewer than l tiles: it starts tiles - l + 1 of them or more behind the first token
+        auto fewer = [&](int l) -> int {
+            if (l > tiles) return 0;
+            const long long from = old + static_cast<long long>(tiles - l + 1) * p.rt;
+            return static_cast<int>((from + kWgKeys - 1) / kWgKeys);
+        };
+        auto next_level = [&]() -> bool {
+            int b = fewer(level);
+            const int mine = b < all ? tiles_of_block(b) : 0;
+            level = __reduce_max_sync(0xffffffffu, mine);
+            if (level == 0) return false;
+            before += batch;
+            block0 = b;
+            on = mine == level ? (fewer(level) < all ? fewer(level) : all) - b : 0;
+            count(on);
+            return true;
+        };
+        bool more = true;
+        // goes on to unit t (t never decreases, but for a new start); more: there is one
+        auto seek = [&](int t) {
+            if (levels) {
+                while (more && t >= before + batch) more = next_level();
+            } else {
+                while (more && t >= before + batch) {
+                    load();
+                    on = blocks;
+                    more = s0 < p.n_seqs;
+                }
+            }
+        };
+        auto restart = [&]() {
+            level = INT_MAX;
+            before = batch = 0;
+            more = true;
+        };
         Place at;
-        for (unsigned r = 0;; ++r) {
-            const unsigned c = (r & 1u) ? (gridDim.x - 1u - blockIdx.x) : blockIdx.x;
-            const int t = static_cast<int>(r * gridDim.x + c);
-            while (s0 < p.n_seqs && t >= before + batch) load();
-            const bool more = s0 < p.n_seqs;
-            if (!__all_sync(0xffffffffu, wait_bar(unit_empty(at.slot), at.phase ^ 1u, p, abort_flag))) break;
+        auto emit = [&](int t) -> bool {  // unit t, or where there is no more the end
+            if (!__all_sync(0xffffffffu, wait_bar(unit_empty(at.slot), at.phase ^ 1u, p, abort_flag))) return false;
             if (more) {
                 const int src = __ffs(__ballot_sync(0xffffffffu, before + incl > t)) - 1;
                 if (lane == src) {
-                    const int in = t - before - (incl - blocks * p.Hkv);
+                    const int in = t - before - (incl - on * p.Hkv);
                     WeighUnit &u = units[at.slot];
                     u.valid = 1;
                     u.row = row;
                     u.kvh = in % p.Hkv;
-                    u.key0 = in / p.Hkv * (2 * kBN);
+                    u.key0 = (block0 + in / p.Hkv) * kWgKeys;
                     u.L = len;
                     u.q0 = q0;
                     u.T = T;
@@ -255,8 +302,50 @@ __global__ void __launch_bounds__(kWgThreads, 1)
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(unit_full(at.slot));
-            if (!more) break;
             at.next();
+            return true;
+        };
+        const int grid = static_cast<int>(gridDim.x), me = static_cast<int>(blockIdx.x);
+        if (levels) restart();
+        seek(me);
+        bool ok = emit(me);
+        if (ok && more && levels && level >= kWgGreedy && grid <= 32 * kWgLoads) {
+            // Every unit goes to the CTA with the least row tiles so far, which all CTAs work out alike:
+            // the first ones in order, then one by one.  Lane l keeps CTAs l, l + 32, ..
+            unsigned load_of[kWgLoads];
+#pragma unroll
+            for (int e = 0; e < kWgLoads; ++e) load_of[e] = lane + 32 * e < grid ? 0u : 0xFFFFFFu;
+            restart();
+            for (seek(0); more && before < grid; seek(before + batch)) {
+#pragma unroll
+                for (int e = 0; e < kWgLoads; ++e)
+                    if (lane + 32 * e >= before && lane + 32 * e < before + batch && lane + 32 * e < grid)
+                        load_of[e] = static_cast<unsigned>(level);
+                if (before + batch >= grid) break;
+            }
+            for (int t = grid; ok; ++t) {
+                seek(t);
+                if (!more) break;
+                unsigned best = 0xFFFFFFFFu;
+#pragma unroll
+                for (int e = 0; e < kWgLoads; ++e) {
+                    const unsigned x = load_of[e] << 8 | static_cast<unsigned>(lane + 32 * e);
+                    best = x < best ? x : best;
+                }
+                best = __reduce_min_sync(0xffffffffu, best);
+                const int c = static_cast<int>(best & 255u);
+#pragma unroll
+                for (int e = 0; e < kWgLoads; ++e)
+                    if (c == lane + 32 * e) load_of[e] += static_cast<unsigned>(level);
+                if (c == me) ok = emit(t);
+            }
+            if (ok) emit(0);
+        } else {
+            for (unsigned r = 1; ok && more; ++r) {
+                const int t = static_cast<int>(r * gridDim.x) + ((r & 1u) ? grid - 1 - me : me);
+                seek(t);
+                ok = emit(t);
+            }
         }
         if (__any_sync(0xffffffffu, bad) && lane == 0) atomicCAS(&g_error_code, 0, static_cast<int>(ATTN_ERR_SHAPE));
     } else if (warp == 2) {
@@ -316,6 +405,12 @@ __global__ void __launch_bounds__(kWgThreads, 1)
         Place at;
         int s = 0, ls = 0, loads = 0;
         uint32_t ph = 0, lph = 0;
+        long long off[4];  // of this lane's rows of a tile: token in the tile, head in the group
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int r = lane + 32 * e, t = r / p.group;
+            off[e] = static_cast<long long>(r - t * p.group) * p.total_q + t;
+        }
         bool ok = true;
         while (ok) {
             if (!(ok = __all_sync(0xffffffffu, wait_bar(unit_full(at.slot), at.phase, p, abort_flag)))) break;
@@ -340,11 +435,10 @@ __global__ void __launch_bounds__(kWgThreads, 1)
                 }
                 if (!(ok = __all_sync(0xffffffffu, wait_bar(l_empty(ls), lph ^ 1u, p, abort_flag)))) break;
                 const int rows = (left < p.rt ? left : p.rt) * p.group;
-                for (int r = lane; r < rows; r += 32) {
-                    const int t = r / p.group, g = r - t * p.group;
-                    cp_async_4(sL + ls * 512 + r * 4,
-                               p.lse_in + static_cast<size_t>(u.kvh * p.group + g) * p.total_q + tok0 + t);
-                }
+                const float *from = p.lse_in + static_cast<long long>(u.kvh) * p.group * p.total_q + tok0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (lane + 32 * e < rows) cp_async_4(sL + ls * 512 + (lane + 32 * e) * 4, from + off[e]);
                 cp_async_arrive(l_full(ls));
                 if (++s == QS) {
                     s = 0;
@@ -369,12 +463,12 @@ __global__ void __launch_bounds__(kWgThreads, 1)
             constexpr uint32_t kTile16 = L::kTileBytes >> 4;
             Place at;
             int s = 0, n = 0;
-            uint32_t ph = 0, steps[2] = {0, 0};
+            uint32_t ph = 0, step = 0;
             bool ok = true;
             while (ok) {
                 if (!(ok = wait_bar(unit_full(at.slot), at.phase, p, abort_flag))) break;
                 const WeighUnit &us = units[at.slot];
-                const int valid = us.valid, m0 = us.m0, m1 = us.m1, T = us.T, tiles = tiles_of(us);
+                const int valid = us.valid, m0 = us.m0, m1 = us.m1, T = us.T;
                 mbar_arrive(unit_empty(at.slot));
                 at.next();
                 if (!valid) break;
@@ -383,18 +477,21 @@ __global__ void __launch_bounds__(kWgThreads, 1)
                 for (int m = m0; m < m1 && ok; ++m) {
                     if (!(ok = wait_bar(q_full(s), ph, p, abort_flag))) break;
                     const int left = T - m * p.rt, rows = (left < p.rt ? left : p.rt) * p.group;
-                    const uint32_t idesc = idesc_f16_f32acc(kBF16, 128, (rows + 15) & ~15, false);
-#pragma unroll
-                    for (int a = 0; a < 2; ++a) {
-                        if (a >= tiles) break;
-                        const uint32_t sb = steps[a] & 1u;
-                        if (!(ok = wait_bar(s_empty(a, sb), ((steps[a] >> 1) & 1u) ^ 1u, p, abort_flag))) break;
-                        ++steps[a];
-                        tc_fence_after();
-                        mma_kq<D>(tmem + 256u * a + 128u * sb, dk + (2 * b + a) * kTile16, dq + s * kTile16, idesc);
-                        mma_commit(s_full(a, sb));
+                    const uint32_t sb = step & 1u;
+                    if (!(ok = wait_bar(s_empty(sb), ((step >> 1) & 1u) ^ 1u, p, abort_flag))) break;
+                    tc_fence_after();
+                    // (where the sequence ends in the first tile the second one's scores are never looked at)
+                    const uint32_t td = tmem + 128u * sb, k_lo = dk + 2 * b * kTile16, q_lo = dq + s * kTile16;
+                    if (rows > 64) {
+                        mma_qk<D, kBF16>(td, k_lo, q_lo);
+                        mma_qk<D, kBF16>(td + 256u, k_lo + kTile16, q_lo);
+                    } else {
+                        const uint32_t idesc = idesc_f16_f32acc(kBF16, 128, (rows + 15) & ~15, false);
+                        mma_kq<D>(td, k_lo, q_lo, idesc);
+                        mma_kq<D>(td + 256u, k_lo + kTile16, q_lo, idesc);
                     }
-                    if (!ok) break;
+                    mma_commit(s_full(sb));
+                    ++step;
                     mma_commit(q_empty(s));
                     if (++s == QS) {
                         s = 0;
@@ -411,13 +508,14 @@ __global__ void __launch_bounds__(kWgThreads, 1)
         __syncwarp();
     } else {
         // -------------------------------------------------------- sums, a key per thread
-        const int a = (warp - 4) >> 2, wq = warp & 3;
-        const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
+        const int a = (warp - 4) >> 3, wq = warp & 3;
+        const int half = ((warp - 4) >> 2) & 1;  // this warpgroup's columns: [64 half, 64 half + 64)
+        const uint32_t tA = tmem + 256u * a + (static_cast<uint32_t>(wq * 32) << 16);
         const float c = p.scale_log2;
         const float2 c2 = make_float2(c, c), nl2 = make_float2(-1.4426950408889634f, -1.4426950408889634f);
         const long long width = static_cast<long long>(p.table_w) << p.page_shift;
         Place at;
-        uint32_t steps = 0, lph = 0;
+        uint32_t step = 0, lph = 0, xph = 0;
         int ls = 0;
         bool ok = true;
         while (ok) {
@@ -428,22 +526,22 @@ __global__ void __launch_bounds__(kWgThreads, 1)
             at.next();
             if (!u.valid) break;
             const int warp_key = u.key0 + kBN * a + 32 * wq, key = warp_key + lane;
-            const bool mine = a < tiles_of(u), real = key < u.L;
+            const bool real = key < u.L, some = warp_key < u.L;
             float *w = p.weights + (static_cast<long long>(u.row) * p.Hkv + u.kvh) * width + key;
             // the sum so far is on its way while the scores are computed; a new token's position begins here
             float old = 0.f;
-            if (p.accumulate && real && key < u.base) old = *w;
+            if (half == 0 && p.accumulate && real && key < u.base) old = *w;
+            const int most = u.T - u.m0 * p.rt;  // tokens of the unit's row tiles
+            const bool both = (most < p.rt ? most : p.rt) * p.group > 64;  // the second warpgroup has columns
             float sum = 0.f;
-            for (int m = u.m0; m < u.m1; ++m) {
-                const uint32_t lse = sL + ls * 512;
-                const uint32_t sb = steps & 1u;
+            for (int m = u.m0; m < u.m1; ++m, ++step) {
+                const float *lse = reinterpret_cast<const float *>(smem + L::kLse + ls * 512);
+                const uint32_t sb = step & 1u, tS = tA + 128u * sb;
                 if (!(ok = __all_sync(0xffffffffu, wait_bar(l_full(ls), lph, p, abort_flag)))) break;
-                if (mine) {
-                    if (!(ok = __all_sync(0xffffffffu, wait_bar(s_full(a, sb), (steps >> 1) & 1u, p, abort_flag)))) break;
-                    ++steps;
+                if (!(ok = __all_sync(0xffffffffu, wait_bar(s_full(sb), (step >> 1) & 1u, p, abort_flag)))) break;
+                if (some) {
                     tc_fence_after();
                     __syncwarp();
-                    const uint32_t tS = tmem + 256u * a + 128u * sb + lane_off;
                     const int left = u.T - m * p.rt, cols = (left < p.rt ? left : p.rt) * p.group;
                     // this key's columns are [c0, cols): those of tokens at or behind it
                     const int tok0 = u.base + m * p.rt;
@@ -453,18 +551,13 @@ __global__ void __launch_bounds__(kWgThreads, 1)
                     };
                     const int c0 = first_col(key), c0_low = first_col(warp_key), c0_high = first_col(warp_key + 31);
                     float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll 1
-                    for (int q = 0; q < cols; q += 32) {
-                        if (c0_low >= q + 32) continue;  // no key of the warp has one of these
-                        uint32_t s[32];
-                        tmem_ld32(tS + q, s);
-                        tmem_ld_wait(s);
-                        const bool whole = c0_high <= q && q + 32 <= cols;
+                    // 32 columns: exp2(s c - lse log2 e) of four at a time
+                    auto add = [&](const uint32_t (&s)[32], int q, bool whole) {
 #pragma unroll
                         for (int e = 0; e < 32; e += 4) {
-                            const uint4 l4 = ld_shared_v4(lse + (q + e) * 4);
-                            const float2 n0 = fmul2(make_float2(u2f(l4.x), u2f(l4.y)), nl2);
-                            const float2 n1 = fmul2(make_float2(u2f(l4.z), u2f(l4.w)), nl2);
+                            const float4 l4 = *reinterpret_cast<const float4 *>(lse + q + e);
+                            const float2 n0 = fmul2(make_float2(l4.x, l4.y), nl2);
+                            const float2 n1 = fmul2(make_float2(l4.z, l4.w), nl2);
                             float2 x0 = ffma2(make_float2(u2f(s[e]), u2f(s[e + 1])), c2, n0);
                             float2 x1 = ffma2(make_float2(u2f(s[e + 2]), u2f(s[e + 3])), c2, n1);
                             if (!whole) {
@@ -478,10 +571,28 @@ __global__ void __launch_bounds__(kWgThreads, 1)
                             acc[0] = fadd2(acc[0], make_float2(ex2_approx(x0.x), ex2_approx(x0.y)));
                             acc[1] = fadd2(acc[1], make_float2(ex2_approx(x1.x), ex2_approx(x1.y)));
                         }
+                    };
+                    const int q0 = 64 * half, q1 = cols < q0 + 64 ? cols : q0 + 64;
+                    if (c0_high <= q0 && q1 == q0 + 64) {
+                        // every key of the warp has all columns
+                        uint32_t s[32];
+                        tmem_ld32(tS + q0, s);
+                        tmem_ld_wait(s);
+                        add(s, q0, true);
+                        tmem_ld32(tS + q0 + 32, s);
+                        tmem_ld_wait(s);
+                        add(s, q0 + 32, true);
+                    } else {
+#pragma unroll 1
+                        for (int q = q0; q < q1; q += 32) {
+                            if (c0_low >= q + 32) continue;  // no key of the warp has one of these
+                            uint32_t s[32];
+                            tmem_ld32(tS + q, s);
+                            tmem_ld_wait(s);
+                            add(s, q, false);
+                        }
                     }
                     tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(s_empty(a, sb));
                     acc[0] = fadd2(acc[0], acc[1]);
                     sum += acc[0].x + acc[0].y;
                 }
@@ -491,8 +602,36 @@ __global__ void __launch_bounds__(kWgThreads, 1)
                     ls = 0;
                     lph ^= 1u;
                 }
+                if (half == 0 || !both || m + 1 < u.m1) {
+                    if (lane == 0) mbar_arrive(s_empty(sb));
+                } else {
+                    // this one's sums are handed over in its last buffer, which the other then frees
+                    uint32_t x[1] = {__float_as_uint(sum)};
+                    tmem_st1(tS + 64u, x);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(x_full(a));
+                }
             }
-            if (ok && mine && real) *w = old + sum;
+            if (!ok) break;
+            if (both) {
+                if (half == 0) {
+                    const uint32_t sb = (step - 1u) & 1u;
+                    if (!(ok = __all_sync(0xffffffffu, wait_bar(x_full(a), xph, p, abort_flag)))) break;
+                    tc_fence_after();
+                    __syncwarp();
+                    uint32_t x[1];
+                    tmem_ld1(tA + 128u * sb + 64u, x);
+                    tmem_ld_wait(x);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(s_empty(sb));
+                    sum += u2f(x[0]);
+                }
+                xph ^= 1u;
+            }
+            if (half == 0 && real) *w = old + sum;
         }
     }
 
