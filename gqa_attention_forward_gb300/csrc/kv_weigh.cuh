@@ -72,9 +72,9 @@ struct WeighLayout {
     static constexpr int kQ = kK + 4 * kTileBytes;
     static constexpr int kLse = kQ + kWgQStages * kTileBytes;
     static constexpr int kBar = kLse + kWgLse * 512;
-    // k_full[2], k_empty[2], q_full[S], q_empty[S], l_full[S], l_empty[S], s_full[2], s_empty[2], x_full[2], mma_done,
+    // k_full[2], k_empty[2], q_full[S], q_empty[S], l_full[S], l_empty[S], s_full[2], s_empty[2], x_full[2][2], mma_done,
     // unit_full[slots], unit_empty[slots]
-    static constexpr int kNumBars = 4 + 2 * kWgQStages + 2 * kWgLse + 4 + 2 + 1 + 2 * kWgSlots;
+    static constexpr int kNumBars = 4 + 2 * kWgQStages + 2 * kWgLse + 4 + 4 + 1 + 2 * kWgSlots;
     static constexpr int kTmemSlot = kBar + kNumBars * 8;
     static constexpr int kAbort = kTmemSlot + 4;
     static constexpr int kUnits = kAbort + 4;
@@ -122,10 +122,12 @@ __global__ void __launch_bounds__(kWgThreads, 1)
     auto l_empty = [&](int s) { return bar0 + 8u * (4 + 2 * QS + LS + s); };
     auto s_full = [&](int b) { return bar0 + 8u * (4 + 2 * QS + 2 * LS + b); };  // of both tiles
     auto s_empty = [&](int b) { return bar0 + 8u * (6 + 2 * QS + 2 * LS + b); };
-    auto x_full = [&](int a) { return bar0 + 8u * (8 + 2 * QS + 2 * LS + a); };  // sums have been handed over
-    const uint32_t mma_done = bar0 + 8u * (10 + 2 * QS + 2 * LS);
-    auto unit_full = [&](int s) { return bar0 + 8u * (11 + 2 * QS + 2 * LS + s); };
-    auto unit_empty = [&](int s) { return bar0 + 8u * (11 + 2 * QS + 2 * LS + kWgSlots + s); };
+    // tile a's sums have been handed over in buffer b: a barrier for each buffer, so that it cannot turn again
+    // before the other warpgroup, which frees the buffer, has seen it
+    auto x_full = [&](int a, int b) { return bar0 + 8u * (8 + 2 * QS + 2 * LS + 2 * a + b); };
+    const uint32_t mma_done = bar0 + 8u * (12 + 2 * QS + 2 * LS);
+    auto unit_full = [&](int s) { return bar0 + 8u * (13 + 2 * QS + 2 * LS + s); };
+    auto unit_empty = [&](int s) { return bar0 + 8u * (13 + 2 * QS + 2 * LS + kWgSlots + s); };
     volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(smem + L::kTmemSlot);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kAbort);
     WeighUnit *units = reinterpret_cast<WeighUnit *>(smem + L::kUnits);
@@ -142,7 +144,8 @@ __global__ void __launch_bounds__(kWgThreads, 1)
         for (int b = 0; b < 2; ++b) {
             mbar_init(k_full(b), 1);
             mbar_init(k_empty(b), 1);
-            mbar_init(x_full(b), 4);
+            mbar_init(x_full(0, b), 4);
+            mbar_init(x_full(1, b), 4);
             mbar_init(s_full(b), 1);
             mbar_init(s_empty(b), 16);  // one arrival per warp of sums
         }
@@ -611,25 +614,23 @@ __global__ void __launch_bounds__(kWgThreads, 1)
                     tmem_st_wait();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(x_full(a));
+                    if (lane == 0) mbar_arrive(x_full(a, sb));
                 }
             }
             if (!ok) break;
-            if (both) {
-                if (half == 0) {
-                    const uint32_t sb = (step - 1u) & 1u;
-                    if (!(ok = __all_sync(0xffffffffu, wait_bar(x_full(a), xph, p, abort_flag)))) break;
-                    tc_fence_after();
-                    __syncwarp();
-                    uint32_t x[1];
-                    tmem_ld1(tA + 128u * sb + 64u, x);
-                    tmem_ld_wait(x);
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(s_empty(sb));
-                    sum += u2f(x[0]);
-                }
-                xph ^= 1u;
+            if (both && half == 0) {
+                const uint32_t sb = (step - 1u) & 1u;
+                if (!(ok = __all_sync(0xffffffffu, wait_bar(x_full(a, sb), (xph >> sb) & 1u, p, abort_flag)))) break;
+                xph ^= 1u << sb;
+                tc_fence_after();
+                __syncwarp();
+                uint32_t x[1];
+                tmem_ld1(tA + 128u * sb + 64u, x);
+                tmem_ld_wait(x);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(s_empty(sb));
+                sum += u2f(x[0]);
             }
             if (half == 0 && real) *w = old + sum;
         }

@@ -411,3 +411,22 @@ def test_a_bounded_cache_as_it_is_used():
     cut()
     binding.kv_free(cache, rows)
     assert status() == binding.ATTN_OK and bool((cache.refs == 0).all())
+
+
+@pytest.mark.parametrize("T", [32, 20])
+def test_units_of_one_row_tile_hand_their_sums_over_in_turn(T):
+    """Thousands of units with one row tile each, in which both warpgroups of a key tile have columns:
+    every call ends, and gives what the first gave."""
+    lens = [2000 + 37 * i for i in range(16)]
+    cache = build(lens, 64, 8, 128, "bf16", seed=31)
+    q = queries(16 * T, 32, 128, "bf16", 32)
+    lse = torch.full((32, 16 * T), 9.0, device="cuda")
+    weights, first = cache.weights(), None
+    for _ in range(40):
+        binding.kv_weigh(cache, weights, q, lse, offsets([T] * 16), accumulate=False)
+        first = weights.clone() if first is None else first
+        assert torch.equal(weights, first)
+    assert status() == binding.ATTN_OK
+    for s in (0, 15):
+        want, tol = weigh_plain(q[s * T:s * T + T], lse[:, s * T:s * T + T], gather(cache, s)[0], T, 1 / math.sqrt(128))
+        close(weights[0, s, :, :lens[s]], want, tol, f"sequence {s}")
