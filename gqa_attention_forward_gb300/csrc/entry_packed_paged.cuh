@@ -627,6 +627,12 @@ attn_status_t attn_kv_weigh(const attn_kv_cache_t *cache, int layer, const void 
     const long long most = ((width + 255) / 256) * Hkv * n;
     const unsigned grid = static_cast<unsigned>(most < g_dev_sms[dev] ? most : g_dev_sms[dev]);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (seqs != nullptr && n > gqa::kWgClaim) {
+        const gqa::KvPool pool = pool_of(cache);
+        if (attn_status_t e = launch_dependent(gqa::kv_claim_kernel, 1, gqa::kPlanThreads, 0, s, pool, seqs, n); e != ATTN_OK)
+            return e;
+        prm.claim = pool.claim;
+    }
     const int kid = (D == 128 ? 2 : 0) + (bf16 ? 1 : 0);
     switch (kid) {
         case 0: return launch_weigh<64, false>(dev, kid, tq, tf, tk, prm, grid, s);

@@ -35,6 +35,7 @@
 
 #include "attn_fwd_tree.cuh"
 #include "kernel_common.cuh"
+#include "kv_pages.cuh"
 
 namespace gqa {
 
@@ -54,6 +55,7 @@ struct WeighParams : Params {
     int page, page_shift, n_pages, table_w;
     int rt, few;     // tokens of a row tile, of the small box
     int accumulate;
+    const int *claim;  // of each row of the table the first entry of seqs that names it; null: few entries
 };
 
 struct WeighUnit {
@@ -98,6 +100,19 @@ __device__ __forceinline__ void mma_kq(uint32_t td, uint32_t k_lo, uint32_t q_lo
         mma_f16_ss(td, hi | (k_lo + off), hi | (q_lo + off), idesc, kk > 0 ? 1u : 0u);
         mma_kq<D, kk + 1>(td, k_lo, q_lo, idesc);
     }
+}
+
+// The first entry of the list that names each row, for lists in which looking through the entries before
+// takes longer than a launch (every CTA of the kernel below looks).
+constexpr int kWgClaim = 64;
+__global__ void __launch_bounds__(kPlanThreads) kv_claim_kernel(const KvPool c, const int *seqs, int n) {
+    grid_launch_dependents();
+    grid_dependency_wait();
+    for (int i = threadIdx.x; i < n; i += kPlanThreads)
+        if (seqs[i] >= 0 && seqs[i] < c.n_rows) c.claim[seqs[i]] = INT_MAX;
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += kPlanThreads)
+        if (seqs[i] >= 0 && seqs[i] < c.n_rows) atomicMin(&c.claim[seqs[i]], i);
 }
 
 // tmQ: 3-D tensor map (D, Hq, tokens), box 64 x G x rt; tmF the same with a box of `few` tokens; tmK: 3-D map
@@ -218,7 +233,9 @@ __global__ void __launch_bounds__(kWgThreads, 1)
                 len = in ? p.lens[row] : 0;
                 // a sequence named before in the list would be added to by two units at once
                 bool again = false;
-                if (p.seqs != nullptr)
+                if (p.claim != nullptr)
+                    again = in && p.claim[row] != s;
+                else if (p.seqs != nullptr)
                     for (int j = 0; j < s; ++j) again |= p.seqs[j] == row;
                 if (q.bad || !in || again || len < T || len > (static_cast<long long>(p.table_w) << p.page_shift)) {
                     bad = true;

@@ -469,6 +469,7 @@ attn_status_t attn_fwd_tree_window(const void *q, const attn_kv_cache_t *cache, 
  *             behind the sequence, and sequences without tokens, are left as they are.
  * Scores and sums are fp32, each position's in a fixed order: one result for the same inputs.  A
  * key or query that a pair does not join (a later token, rows behind the end) never matters.
+ * Limits: n sequences of the table's width have less than 2^30 / Hkv blocks of 256 positions.
  * Errors: as attn_fwd_tree; attn_last_device_error reports ATTN_ERR_SHAPE for offsets, lengths
  * and sequences out of range, T above the sequence's length and a sequence named twice (its first
  * entry counts), whose weights are then left as they were, and ATTN_ERR_PAGE for a missing page,

@@ -154,6 +154,30 @@ def test_weigh_refuses_what_is_out_of_range():
     assert status() == binding.ATTN_ERR_PAGE
 
 
+def test_weigh_over_a_long_list_of_chosen_rows():
+    """More entries than are looked through one by one: each row's first entry counts, the others are refused."""
+    lens = [1 + (13 * i) % 300 for i in range(90)]
+    cache = build(lens, 16, 2, 64, "bf16", seed=41)
+    rows = [(7 * i) % 90 for i in range(90)]
+    rows[20], rows[70], rows[89], rows[5] = rows[3], rows[69], rows[0], -1
+    q, scale = queries(90, 4, 64, "bf16", 42), 1 / 8
+    lse = torch.zeros((4, 90), device="cuda")
+    for i, s in enumerate(rows):
+        lse[:, i:i + 1] = logsumexps(q[i:i + 1], gather(cache, max(s, 0))[0], 1, scale)
+    weights = cache.weights() + 1
+    binding.kv_weigh(cache, weights, q, lse, offsets([1] * 90), seqs=i32(rows))
+    assert status() == binding.ATTN_ERR_SHAPE
+    for s in range(90):
+        if s not in rows:
+            assert bool((weights[0, s] == 1).all())
+            continue
+        i, n = rows.index(s), lens[s]
+        want, tol = weigh_plain(q[i:i + 1], lse[:, i:i + 1], gather(cache, s)[0], 1, scale)
+        want[:, :n - 1] += 1
+        close(weights[0, s, :, :n], want, tol + F * want, f"row {s}")
+        assert bool((weights[0, s, :, n:] == 1).all())
+
+
 # ---------------------------------------------------------------- eviction
 def evict(model, weights, seqs, sinks, heavy, recent):
     """The operator on a host model of the cache, and on its weights (a list of arrays, or None)."""
