@@ -904,13 +904,31 @@ __global__ void __launch_bounds__(kWsThreads, 1)
                     const float mr = m_ref == -INFINITY ? 0.f : m_ref;
                     return make_float2(-mr * c, -mr * c);
                 };
-                if (kWindow ? seen_whole(j) : j < first_masked) {
+                // (with a window masked tiles are too many of all to be worth the two passes below)
+                if (kWindow || j < first_masked) {
                     uint32_t s[128];
                     float mq[4];
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
                         tmem_ld32_max(tS + 32 * q, *reinterpret_cast<uint32_t(*)[32]>(&s[32 * q]), mq[q]);
                     tmem_ld_wait(s, mq);
+                    if (kWindow && !seen_whole(j)) {
+                        // this row sees column e where e <= lim and (e > from or e < sk)
+                        const int col0 = win_key_tile<kWindow>(j, p.sinks, skip) * kBN;
+                        const int lim = lim0 - col0, from = pos - p.window - col0, sk = p.sinks - col0;
+                        auto below = [](int n) -> uint32_t { return n <= 0 ? 0u : (n >= 32 ? ~0u : (1u << n) - 1u); };
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const uint32_t see = below(lim + 1 - 32 * q) & (~below(from + 1 - 32 * q) | below(sk - 32 * q));
+                            if (__all_sync(0xffffffffu, see == ~0u)) continue;
+                            mq[q] = -INFINITY;
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) {
+                                if (!((see >> e) & 1u)) s[32 * q + e] = __float_as_uint(-INFINITY);
+                                mq[q] = fmaxf(mq[q], u2f(s[32 * q + e]));
+                            }
+                        }
+                    }
                     m_top = fmaxf(m_top, fmax3(mq[0], mq[1], fmaxf(mq[2], mq[3])));
                     const float2 nmc2 = reference();
 #pragma unroll
@@ -934,30 +952,15 @@ __global__ void __launch_bounds__(kWsThreads, 1)
                     // A masked tile, once or twice per unit: 32 columns at a time, in two passes over
                     // TMEM, which is few instructions to fetch each time (P, 16 columns of pairs,
                     // overwrites scores that have been read).
-                    const int col0 = win_key_tile<kWindow>(j, p.sinks, skip) * kBN;
-                    const int lim = lim0 - col0;  // this row keeps the columns up to lim
+                    const int lim = lim0 - j * kBN;  // this row keeps the columns up to lim
                     // Of columns 32 q .. every row of the warp sees all for q < q_all and none for
                     // q >= q_none: on a causal diagonal all but one of the four steps need no selects.
                     const int lo = __reduce_min_sync(0xffffffffu, lim), hi = __reduce_max_sync(0xffffffffu, lim);
                     const int q_all = lo < 31 ? 0 : (lo + 1) >> 5, q_none = hi < 0 ? 0 : (hi >> 5) + 1;
-                    // with a window: of those up to lim the columns past wlim or below sk
-                    const int wlim = kWindow ? pos - p.window - col0 : 0, sk = kWindow ? p.sinks - col0 : 0;
-                    const int wlo = kWindow ? __reduce_min_sync(0xffffffffu, wlim) : 0;
-                    const int whi = kWindow ? __reduce_max_sync(0xffffffffu, wlim) : 0;
-                    auto all = [&](int q) -> bool {
-                        return q < q_all && (!kWindow || 32 * q > whi || 32 * q + 31 < sk);
-                    };
-                    auto none = [&](int q) -> bool {
-                        return q >= q_none || (kWindow && 32 * q + 31 <= wlo && 32 * q >= sk);
-                    };
-                    auto sees = [&](int e, int q) -> bool {
-                        return e <= lim - 32 * q && (!kWindow || e > wlim - 32 * q || e < sk - 32 * q);
-                    };
 #pragma unroll 1
                     for (int q = 0; q < 4 && q < q_none; ++q) {
                         uint32_t s[32];
-                        if (kWindow && none(q)) continue;
-                        if (all(q)) {
+                        if (q < q_all) {
                             float mq[1];
                             tmem_ld32_max(tS + 32 * q, s, mq[0]);
                             tmem_ld_wait(s, mq);
@@ -968,7 +971,7 @@ __global__ void __launch_bounds__(kWsThreads, 1)
                             float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
                             for (int e = 0; e < 32; ++e)
-                                mx[e & 1] = fmaxf(mx[e & 1], sees(e, q) ? u2f(s[e]) : -INFINITY);
+                                mx[e & 1] = fmaxf(mx[e & 1], e <= lim - 32 * q ? u2f(s[e]) : -INFINITY);
                             m_top = fmax3(m_top, mx[0], mx[1]);
                         }
                     }
@@ -976,7 +979,7 @@ __global__ void __launch_bounds__(kWsThreads, 1)
 #pragma unroll 1
                     for (int q = 0; q < 4; ++q) {
                         uint32_t s[32], pk[16];
-                        if (none(q)) {
+                        if (q >= q_none) {
 #pragma unroll
                             for (int e = 0; e < 16; ++e) pk[e] = 0u;
                             tmem_st16(tS + 16 * q, pk);
@@ -984,10 +987,10 @@ __global__ void __launch_bounds__(kWsThreads, 1)
                         }
                         tmem_ld32(tS + 32 * q, s);
                         tmem_ld_wait(s);
-                        if (!all(q)) {
+                        if (q >= q_all) {
 #pragma unroll
                             for (int e = 0; e < 32; ++e)
-                                if (!sees(e, q)) s[e] = __float_as_uint(-INFINITY);
+                                if (e > lim - 32 * q) s[e] = __float_as_uint(-INFINITY);
                         }
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
