@@ -33,6 +33,13 @@
 // 4-7 softmax (one row per thread).  P stays in TMEM over its scores.  TMEM: S0 [0,128),
 // S1 [128,256), O0 [256,256+D), O1 [384,384+D).
 //
+// Window (attn_fwd_tree_window).  A unit's tiles are those of the first keys and those from the first
+// position of the window of the tree's first token on, numbered without a gap; the bits of a row are
+// cut to the token's nearest ancestors and the positions of its window.  16 sequences of one token,
+// window 1024: 26 us captured, of which 8.5 are bytes at the copy rate, 7 pass until the first scores
+// and 5 in the merge; 8 trees of 1 to 60, window 4096: 40 us.  (Leaving out the page pieces of a
+// tile that no token sees reads 10% less and takes 0.5 and 1 us more.)
+//
 // Pages.  A page is [Hkv, page, D]; a tile is min(page, 128)-row boxes.  A page index past
 // the end of the sequence or out of range is replaced by one past the last page, whose box
 // reads as zeros; the second also sets the device error word.  Rows of the last page past

@@ -45,6 +45,17 @@
 // Rounding.  P is rounded to the input type, against a stale row max (weights up to 2^8 of the
 // reference): half a step of each weight, the same as the output's own rounding.
 //
+// Window (attn_fwd_varlen_window).  A unit visits the key tiles of the first keys and those from the
+// first key of its first row's window on; tiles that no row sees are neither loaded nor computed (4
+// D flops per visible pair bound it in the same way, plus what the tiles on the three borders, the
+// end of the first keys, the window's start and the diagonal, hold besides: with a window of 512 half
+// of the steps).  Masked tiles go in one pass, as a word of bits per row and 32 columns: with windows
+// they are too many of all tiles for the two passes of the plain kernel (12 prompts of 1 to 4096,
+// Hq 16, D 128, window 512: 84.4 us in two passes, 82.1 in one; one prompt of 200, window 64, D 64
+// 11.0 and 9.0; two of 16384 and 9001, Hq 32, window 2048 611 and 587, 1.37 PFLOP/s).  Taking the first
+// keys' tile as products of 16 ceil(n / 16) keys saves a sixth of the first case's MMAs and costs
+// time (84.7): the steps' round trips between the roles bound short units, not their products.
+//
 // Value guard.  A 128-row V box of the last key tile reaches into the next sequence (or
 // into rows behind the last one, which may hold anything), and P = 0 times infinity or
 // NaN is NaN.  The guard zeroes those rows in shared memory before P V reads them.  In

@@ -12,6 +12,16 @@
 // the tensor cores and the exponentials alike (2 D flops and one exp2 per row and key, of which an
 // SM does about 8192 and 32 a cycle: 512 cycles of each for 128 keys and 128 rows).
 //
+// Measured, GB300: 16 sequences of 2 to 8192 positions and a token each (Hq 32, Hkv 8, D 128) 37 us
+// with the copy that resets the case, 1.5 us per 64 KB of K and SM while it streams (6.6 TB/s), 4 us
+// until the first tile; the last 32 tokens of 32000 15 us; 12 whole prompts of 1 to 4096 (Hq 16) 85
+// us, 0.82 PFLOP/s.  A step of 256 keys and 128 rows then takes 2200 cycles, of which the tensor
+// pipe and the exponentials are busy for about 1000 each, and its two halves, the issuer's waits,
+// products and commits (1800) and the sums' barriers, TMEM loads and exponentials (1900), bound it
+// alike: without the exponentials, with a quarter of the products or half of Q's loads it takes the
+// same time, with half of the sums' work 7% less.  (Two issuing threads 88 us, K in TMEM as the A
+// operand 87, the next step's scores loaded ahead 94.)
+//
 // The product is taken transposed, S^T = K Q^T: a TMEM lane, and so a thread, owns a key, and the
 // sum over the rows is a sum over a thread's own columns, without shuffles, atomics or a second
 // pass; the rows' log-sum-exps are the same for all threads and come from shared memory.  A unit is
