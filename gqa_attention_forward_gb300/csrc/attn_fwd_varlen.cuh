@@ -298,7 +298,8 @@ struct VlWalk {
 // the instruction's own block: the upper word is a constant, the lower one (start address and
 // leading offset, in 16-byte units) a base plus a constant, so that one register per operand is
 // live and no descriptors are hoisted out of the issuer's loop (there they spilled).  What the
-// kernel still spills is 12 bytes stored and 4 loaded at D = 128, 24 and 88 to 96 at D = 64, in all.
+// kernel still spills is 12 bytes stored and 4 loaded at D = 128, 24 and 88 to 96 at D = 64, in all (with
+// a window 12 and 4, 32 and 512).
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // stride 1024 B, version 1, swizzle 128 B
 __device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo_bytes) {
     return ((saddr & 0x3FFFFu) >> 4) | ((lbo_bytes >> 4) << 16);

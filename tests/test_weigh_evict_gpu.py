@@ -454,3 +454,120 @@ def test_units_of_one_row_tile_hand_their_sums_over_in_turn(T):
     for s in (0, 15):
         want, tol = weigh_plain(q[s * T:s * T + T], lse[:, s * T:s * T + T], gather(cache, s)[0], T, 1 / math.sqrt(128))
         close(weights[0, s, :, :lens[s]], want, tol, f"sequence {s}")
+
+
+def test_whole_prompts_of_many_units():
+    """More units than CTAs, dealt by the work that they have."""
+    lens = [1500, 33, 900, 1, 1200, 700, 128, 1024, 513, 256, 90, 400]
+    Hq, Hkv, D = 16, 8, 64
+    cache = build(lens, 32, Hkv, D, "f16", seed=51)
+    q, scale, a = queries(sum(lens), Hq, D, "f16", 52), 0.125, 0
+    lse = torch.empty((Hq, sum(lens)), device="cuda")
+    for s, n in enumerate(lens):
+        lse[:, a:a + n] = logsumexps(q[a:a + n], gather(cache, s)[0], n, scale)
+        a += n
+    weights = cache.weights() + 5
+    binding.kv_weigh(cache, weights, q, lse, offsets(lens))
+    assert status() == binding.ATTN_OK
+    a = 0
+    for s, n in enumerate(lens):
+        want, tol = weigh_plain(q[a:a + n], lse[:, a:a + n], gather(cache, s)[0], n, scale)
+        close(weights[0, s, :, :n], want, tol, f"prompt {s}")
+        assert bool((weights[0, s, :, n:] == 5).all())
+        a += n
+
+
+@pytest.mark.parametrize("layers,Hkv,n,page", [(1, 1, 300000, 1024), (20, 8, 40000, 256), (1, 2, 70000, 16)])
+def test_eviction_from_very_long_sequences(layers, Hkv, n, page):
+    """More positions than a cluster (of 8 blocks, of one) holds bits of at a time, with ties on the border."""
+    sinks, heavy, recent, D = 5, 1234, 777, 64
+    keep = sinks + heavy + recent
+    cache = build([n], page, Hkv, D, "bf16", n_layers=layers, seed=61)
+    weights = torch.floor(torch.rand(cache.weights().shape, device="cuda") ** 4 * 3000) / 3000
+    k, v, w, table = cache.k.clone(), cache.v.clone(), weights[:, 0].clone(), cache.table.clone()
+    binding.kv_evict(cache, i32([0]), weights, sinks=sinks, heavy=heavy, recent=recent)
+    assert status() == binding.ATTN_OK and cache.lens.tolist() == [keep]
+    best = torch.sort(w[:, :, sinks:n - recent], dim=-1, descending=True, stable=True).indices[:, :, :heavy] + sinks
+    at = torch.arange(n, device="cuda").expand(layers, Hkv, n)
+    src = torch.cat([at[:, :, :sinks], best.sort(-1).values, at[:, :, n - recent:]], -1)
+    dst, row = at[:, :, :keep], table[0].long()
+    L, H = torch.arange(layers, device="cuda")[:, None, None], torch.arange(Hkv, device="cuda")[None, :, None]
+    for old, new in ((k, cache.k), (v, cache.v)):
+        old[L, row[dst // page], H, dst % page] = old[L, row[src // page], H, src % page]
+        assert torch.equal(old.view(torch.int16), new.view(torch.int16))
+    w2 = torch.zeros_like(w)
+    w2[:, :, :keep] = torch.gather(w, 2, src)
+    assert torch.equal(weights[:, 0, :, :n], w2[:, :, :n])
+    used = -(-keep // page)
+    assert torch.equal(cache.table[0, :used], table[0, :used]) and bool((cache.table[0, used:] == -1).all())
+    assert int(cache.refs.sum()) == used
+
+
+def test_a_wait_that_runs_out_ends_the_call_and_the_next_one_is_right():
+    cache = build([900, 300], 64, 2, 128, "bf16", seed=71)
+    T = [40, 3]
+    q, lse = queries(43, 8, 128, "bf16", 72), torch.full((8, 43), 6.0, device="cuda")
+    good, weights, lib = cache.weights(), cache.weights(), binding.load()
+    binding.kv_weigh(cache, good, q, lse, offsets(T))
+    o, _ = binding.attention_tree(q, cache, offsets(T), window=200, sinks=4)
+    x = queries(300, 8, 128, "bf16", 73)
+    p, _ = binding.attention_varlen(x, x[:, :2], x[:, 2:4], offsets([300]), window=40, sinks=4)
+    assert status() == binding.ATTN_OK
+    for call in (lambda: binding.kv_weigh(cache, weights, q, lse, offsets(T)),
+                 lambda: binding.attention_tree(q, cache, offsets(T), window=200, sinks=4),
+                 lambda: binding.attention_varlen(x, x[:, :2], x[:, 2:4], offsets([300]), window=40, sinks=4)):
+        try:
+            lib.attn_test_set_wait_timeout_ns(20_000_000)
+            lib.attn_test_inject_stall(1)
+            call()
+        finally:
+            lib.attn_test_inject_stall(0)
+            lib.attn_test_set_wait_timeout_ns(0)
+        assert status() == binding.ATTN_ERR_TIMEOUT
+        call()
+        assert status() == binding.ATTN_OK
+    weights.zero_()
+    binding.kv_weigh(cache, weights, q, lse, offsets(T))
+    assert torch.equal(weights, good)
+    assert torch.equal(o, binding.attention_tree(q, cache, offsets(T), window=200, sinks=4)[0])
+    assert torch.equal(p, binding.attention_varlen(x, x[:, :2], x[:, 2:4], offsets([300]), window=40, sinks=4)[0])
+
+
+def test_calls_on_two_streams_and_in_two_graphs():
+    """Two caches at once, each on its own stream, and a graph of each replayed at once."""
+    sides = []
+    for seed in (81, 82):
+        cache = build([700 + seed, 300, 500], 32, 2, 64, "f16", seed=seed, n_layers=2)
+        q, lse = queries(30, 4, 64, "f16", seed), torch.full((4, 30), 5.5, device="cuda")
+        weights, cu = cache.weights(), offsets([10, 10, 10])
+        state = [x.clone() for x in (cache.k, cache.v, cache.table, cache.lens, cache.refs)]
+        s = torch.cuda.Stream()
+
+        def step(cache=cache, q=q, lse=lse, weights=weights, cu=cu, state=state):
+            for x, y in zip((cache.k, cache.v, cache.table, cache.lens, cache.refs), state):
+                x.copy_(y)
+            for layer in (0, 1):
+                binding.kv_weigh(cache, weights, q, lse, cu, layer=layer, accumulate=False)
+            binding.kv_evict(cache, None, weights, sinks=3, heavy=100, recent=60)
+
+        step()
+        torch.cuda.synchronize()
+        want = [x.clone() for x in (cache.k, cache.v, cache.table, cache.lens, cache.refs, weights)]
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=s):
+                step()
+        sides.append((cache, weights, want, step, s, graph))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for cache, weights, want, step, s, graph in sides:
+            with torch.cuda.stream(s):
+                step()
+                graph.replay()
+    torch.cuda.synchronize()
+    assert status() == binding.ATTN_OK
+    for cache, weights, want, step, s, graph in sides:
+        for x, y in zip((cache.k, cache.v, cache.table, cache.lens, cache.refs, weights), want):
+            assert torch.equal(x, y)
+        assert cache.lens.tolist() == [163, 163, 163]
