@@ -469,9 +469,7 @@ def _c_int(x):
 def _window(window, sinks):
     """The window and the first keys as C ints."""
     if window is None:
-        if sinks != 0:
-            raise ValueError("sinks are the first keys that a window leaves visible: they need a window")
-        return None, 0
+        raise ValueError("sinks are the first keys that a window leaves visible: they need a window")
     return _c_int(window), _c_int(sinks)
 
 
@@ -485,9 +483,10 @@ def attention_varlen(q, k, v, cu_q, cu_k=None, causal: bool = True, scale: float
     device, never read by the host.  ``window``, ``sinks``: attn_fwd_varlen_window (each row sees the
     last ``window`` keys up to its own and the first ``sinks``).  Returns (o [total_q,Hq,D],
     lse [Hq,total_q]) without waiting; rows behind the last sequence are not written."""
-    window, sinks = _window(window, sinks)
-    if window is not None and not causal:
-        raise ValueError("a window is causal")
+    if window is not None or sinks != 0:
+        window, sinks = _window(window, sinks)
+        if not causal:
+            raise ValueError("a window is causal")
     shape, sq = _rows(q, "q")
     kshape, sk = _rows(k, "k")
     vshape, sv = _rows(v, "v")
@@ -802,7 +801,8 @@ def attention_tree(q, cache, cu, seqs=None, parents=None, layer: int = 0, scale:
     ``workspace``: a uint8 CUDA tensor, or None to let torch allocate the size that
     attn_fwd_tree_workspace asks for.  Returns (o [total,Hq,D], lse [Hq,total]) without waiting."""
     torch = _torch()
-    window, sinks = _window(window, sinks)
+    if window is not None or sinks != 0:
+        window, sinks = _window(window, sinks)
     (total, Hq, D), sq = _rows(q, "q")
     dev = cache.dev
     _same(q, "q", cache.dtype, dev)
