@@ -337,9 +337,12 @@ __global__ void __launch_bounds__(kWgThreads, 1)
         };
         const int grid = static_cast<int>(gridDim.x), me = static_cast<int>(blockIdx.x);
         if (levels) restart();
+        seek(0);
+        // how units are dealt is one choice for all CTAs: it goes by the largest unit, not by a CTA's own first
+        const bool greedy = levels && more && level >= kWgGreedy && grid <= 32 * kWgLoads;
         seek(me);
         bool ok = emit(me);
-        if (ok && more && levels && level >= kWgGreedy && grid <= 32 * kWgLoads) {
+        if (ok && more && greedy) {
             // Every unit goes to the CTA with the least row tiles so far, which all CTAs work out alike:
             // the first ones in order, then one by one.  Lane l keeps CTAs l, l + 32, ..
             unsigned load_of[kWgLoads];

@@ -477,6 +477,26 @@ def test_whole_prompts_of_many_units():
         a += n
 
 
+@pytest.mark.parametrize("long,short,n_short,Hkv", [(1300, 200, 31, 12), (700, 100, 31, 16), (3000, 130, 20, 16)])
+def test_large_and_small_units_share_the_first_round(long, short, n_short, Hkv):
+    """Units of many row tiles beside so many of few that the CTAs' first ones are of both kinds, and several rounds follow."""
+    lens, D = [long] + [short + i for i in range(n_short)], 64
+    cache = build(lens, 64, Hkv, D, "bf16", seed=55)
+    q, scale, a = queries(sum(lens), Hkv, D, "bf16", 56), 0.125, 0
+    lse = torch.empty((Hkv, sum(lens)), device="cuda")
+    for s, n in enumerate(lens):
+        lse[:, a:a + n] = logsumexps(q[a:a + n], gather(cache, s)[0], n, scale)
+        a += n
+    weights = torch.full_like(cache.weights(), -3.0)
+    binding.kv_weigh(cache, weights, q, lse, offsets(lens))
+    assert status() == binding.ATTN_OK
+    a = 0
+    for s, n in enumerate(lens):
+        want, tol = weigh_plain(q[a:a + n], lse[:, a:a + n], gather(cache, s)[0], n, scale)
+        close(weights[0, s, :, :n], want, tol, f"prompt {s}")
+        a += n
+
+
 @pytest.mark.parametrize("layers,Hkv,n,page", [(1, 1, 300000, 1024), (20, 8, 40000, 256), (1, 2, 70000, 16)])
 def test_eviction_from_very_long_sequences(layers, Hkv, n, page):
     """More positions than a cluster (of 8 blocks, of one) holds bits of at a time, with ties on the border."""
