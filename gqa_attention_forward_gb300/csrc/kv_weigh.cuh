@@ -14,13 +14,14 @@
 //
 // Measured, GB300: 16 sequences of 2 to 8192 positions and a token each (Hq 32, Hkv 8, D 128) 37 us
 // with the copy that resets the case, 1.5 us per 64 KB of K and SM while it streams (6.6 TB/s), 4 us
-// until the first tile; the last 32 tokens of 32000 15 us; 12 whole prompts of 1 to 4096 (Hq 16) 85
-// us, 0.82 PFLOP/s.  A step of 256 keys and 128 rows then takes 2200 cycles, of which the tensor
-// pipe and the exponentials are busy for about 1000 each, and its two halves, the issuer's waits,
-// products and commits (1800) and the sums' barriers, TMEM loads and exponentials (1900), bound it
-// alike: without the exponentials, with a quarter of the products or half of Q's loads it takes the
-// same time, with half of the sums' work 7% less.  (Two issuing threads 88 us, K in TMEM as the A
-// operand 87, the next step's scores loaded ahead 94.)
+// until the first tile; the last 32 tokens of 32000 15 us; 12 whole prompts of 1 to 4096 (Hq 16) 81
+// us, 0.86 PFLOP/s; one of 32768 (Hq 32) 3327 us, 1.32 PFLOP/s; one of 512 beside 31 sequences of 32768
+// with a token each 318 us, 6.66 TB/s.  A step of 256 keys and 128 rows takes 1800 to 2200 cycles, of
+// which the tensor pipe and the exponentials are busy for about 1000 each, and its two halves, the
+// issuer's waits, products and commits (1800) and the sums' barriers, TMEM loads and exponentials
+// (1900), bound it alike: without the exponentials, with a quarter of the products or half of Q's loads
+// the 12 prompts take the same time, with half of the sums' work 7% less.  (Two issuing threads 3 us
+// more, K in TMEM as the A operand 2, the next step's scores loaded ahead 8.)
 //
 // The product is taken transposed, S^T = K Q^T: a TMEM lane, and so a thread, owns a key, and the
 // sum over the rows is a sum over a thread's own columns, without shuffles, atomics or a second
@@ -31,8 +32,9 @@
 //
 // Units of up to 32 sequences are dealt to the CTAs by the number of their row tiles, most first (a
 // sequence's blocks of keys have fewer and fewer, so that lane s of the scheduler finds sequence s's
-// block of a level in closed form); more sequences in their order, as a pass over all of them for
-// each level would take too long.
+// block of a level in closed form), large ones to the CTA with the least work, the rest in snake
+// order; those of more sequences in the order of these, as a pass over all for each level would
+// take too long.
 //
 // Roles (640 threads): warp 0 MMA issuer, warp 1 TMA producer of Q, and the rows' log-sum-exps,
 // warp 2 TMA producer of K (the lanes issue one page box each), warp 3 scheduler (and TMEM), and
@@ -51,9 +53,10 @@ namespace gqa {
 
 constexpr int kWgThreads = 640;
 constexpr int kWgKeys = 2 * kBN;  // of a unit
-// Units of so many row tiles (the largest) and more are dealt one by one, to up to 256 CTAs.  For 12
-// prompts of 1 to 4096 the longest share is then 64 row tiles and the mean 61; in snake order 82.
-constexpr int kWgGreedy = 4, kWgLoads = 8;
+// Units of so many row tiles and more are dealt one by one, to up to 256 CTAs, a few to each (every CTA
+// works out all of it, about 80 ns a unit, in which the GPU does 11 row tiles).  For 12 prompts of 1
+// to 4096 the longest share is then 64 row tiles and the mean 61; in snake order 82.
+constexpr int kWgGreedy = 8, kWgRounds = 8, kWgLoads = 8;
 constexpr int kWgQStages = 3, kWgSlots = 3, kWgLse = 3;
 constexpr int kWgFewRows = 16;  // rows of the small Q box: with few tokens a full one is 32 KB beside 64 KB of K
 
@@ -342,42 +345,49 @@ __global__ void __launch_bounds__(kWgThreads, 1)
         const bool greedy = levels && more && level >= kWgGreedy && grid <= 32 * kWgLoads;
         seek(me);
         bool ok = emit(me);
-        if (ok && more && greedy) {
-            // Every unit goes to the CTA with the least row tiles so far, which all CTAs work out alike:
-            // the first ones in order, then one by one.  Lane l keeps CTAs l, l + 32, ..
-            unsigned load_of[kWgLoads];
+        if (ok && more) {
+            int t = grid;
+            if (greedy) {
+                // A unit goes to the CTA with the least row tiles so far, which all CTAs work out alike: the first
+                // ones in order, then one by one.  Lane l keeps CTAs l, l + 32, ..
+                constexpr unsigned kNone = 0xFFFFFFu;
+                unsigned load_of[kWgLoads];
 #pragma unroll
-            for (int e = 0; e < kWgLoads; ++e) load_of[e] = lane + 32 * e < grid ? 0u : 0xFFFFFFu;
-            restart();
-            for (seek(0); more && before < grid; seek(before + batch)) {
+                for (int e = 0; e < kWgLoads; ++e) load_of[e] = lane + 32 * e < grid ? 0u : kNone;
+                restart();
+                for (seek(0); more && before < grid; seek(before + batch)) {
 #pragma unroll
-                for (int e = 0; e < kWgLoads; ++e)
-                    if (lane + 32 * e >= before && lane + 32 * e < before + batch && lane + 32 * e < grid)
-                        load_of[e] = static_cast<unsigned>(level);
-                if (before + batch >= grid) break;
-            }
-            for (int t = grid; ok; ++t) {
-                seek(t);
-                if (!more) break;
-                unsigned best = 0xFFFFFFFFu;
-#pragma unroll
-                for (int e = 0; e < kWgLoads; ++e) {
-                    const unsigned x = load_of[e] << 8 | static_cast<unsigned>(lane + 32 * e);
-                    best = x < best ? x : best;
+                    for (int e = 0; e < kWgLoads; ++e)
+                        if (lane + 32 * e >= before && lane + 32 * e < before + batch && lane + 32 * e < grid)
+                            load_of[e] = static_cast<unsigned>(level);
+                    if (before + batch >= grid) break;
                 }
-                best = __reduce_min_sync(0xffffffffu, best);
-                const int c = static_cast<int>(best & 255u);
+                for (; ok; ++t) {
+                    seek(t);
+                    if (!more || level < kWgGreedy || t >= kWgRounds * grid) break;
+                    unsigned best = 0xFFFFFFFFu;
 #pragma unroll
-                for (int e = 0; e < kWgLoads; ++e)
-                    if (c == lane + 32 * e) load_of[e] += static_cast<unsigned>(level);
-                if (c == me) ok = emit(t);
+                    for (int e = 0; e < kWgLoads; ++e) {
+                        const unsigned x = load_of[e] << 8 | static_cast<unsigned>(lane + 32 * e);
+                        best = x < best ? x : best;
+                    }
+                    best = __reduce_min_sync(0xffffffffu, best);
+                    const int c = static_cast<int>(best & 255u);
+#pragma unroll
+                    for (int e = 0; e < kWgLoads; ++e)
+                        if (c == lane + 32 * e) {
+                            const unsigned x = load_of[e] + static_cast<unsigned>(level);
+                            load_of[e] = x < kNone ? x : kNone - 1u;
+                        }
+                    if (c == me) ok = emit(t);
+                }
             }
-            if (ok) emit(0);
-        } else {
-            for (unsigned r = 1; ok && more; ++r) {
-                const int t = static_cast<int>(r * gridDim.x) + ((r & 1u) ? grid - 1 - me : me);
-                seek(t);
-                ok = emit(t);
+            // the others in snake order, up to the end
+            for (bool back = true; ok; t += grid, back = !back) {
+                const int mine = t + (back ? grid - 1 - me : me);
+                seek(mine);
+                ok = emit(mine);
+                if (!more) break;
             }
         }
         if (__any_sync(0xffffffffu, bad) && lane == 0) atomicCAS(&g_error_code, 0, static_cast<int>(ATTN_ERR_SHAPE));
