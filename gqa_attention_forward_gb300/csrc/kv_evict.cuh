@@ -58,6 +58,7 @@ struct EvictShared {
     int scan[2][kEvWarps];
     int pages[kEvList / 16 + 1];  // of the places that the listed rows go to
     int found[2];
+    int still;  // listed rows that stay where they are
 };
 
 // What a weight orders by: NaN and negative ones as 0.
@@ -310,6 +311,7 @@ __global__ void __launch_bounds__(kEvThreads, kChoose ? 3 : 4) kv_evict_kernel(c
                 // ------------------------------------------------ the listed rows move up
                 const int place0 = dst0 >> c.page_shift, place1 = (dst0 + fill + c.page - 1) >> c.page_shift;
                 for (int j = place0 + static_cast<int>(threadIdx.x); j < place1; j += kEvThreads) sm.pages[j - place0] = row[j];
+                if (threadIdx.x == 0) sm.still = 0;
                 __syncthreads();  // all are listed
                 // the weights, a block its share; positions become rows
                 const int r1 = rank * kEvThreads + static_cast<int>(threadIdx.x);
@@ -326,6 +328,7 @@ __global__ void __launch_bounds__(kEvThreads, kChoose ? 3 : 4) kv_evict_kernel(c
                             if (r0 + e * C * kEvThreads < fill) sm.w[r0 + e * C * kEvThreads] = v[e];
                     }
                 __syncthreads();
+                int still = 0;
                 for (int r0 = threadIdx.x; r0 < fill; r0 += 4 * kEvThreads) {
                     int pos[4], page[4];
 #pragma unroll
@@ -335,9 +338,16 @@ __global__ void __launch_bounds__(kEvThreads, kChoose ? 3 : 4) kv_evict_kernel(c
                     }
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        if (r0 + e * kEvThreads < fill) sm.src[r0 + e * kEvThreads] = row_of(page[e], pos[e]);
+                        if (r0 + e * kEvThreads < fill) {
+                            sm.src[r0 + e * kEvThreads] = row_of(page[e], pos[e]);
+                            still += pos[e] == dst0 + r0 + e * kEvThreads ? 1 : 0;
+                        }
                 }
+                // those before the first position that goes are where they belong
+                still = __reduce_add_sync(0xffffffffu, still);
+                if (lane == 0 && still > 0) atomicAdd(&sm.still, still);
                 if (w != nullptr) cluster.sync(); else __syncthreads();  // their weights have been read
+                still = sm.still;
                 if (w != nullptr)
                     for (int r = r1; r < fill; r += C * kEvThreads) w[dst0 + r] = sm.w[r];
                 for (int half = 0; half < (C == 1 ? 2 : 1); ++half) {
@@ -358,8 +368,8 @@ __global__ void __launch_bounds__(kEvThreads, kChoose ? 3 : 4) kv_evict_kernel(c
                         }
                     };
                     uint4 a[kEvMove], b[kEvMove];
-                    fetch(0, a);
-                    for (int r0 = 0; r0 < fill; r0 += 2 * per_step) {
+                    fetch(still, a);
+                    for (int r0 = still; r0 < fill; r0 += 2 * per_step) {
                         fetch(r0 + per_step, b);
                         __syncthreads();  // rows that these places hold have been read
                         store(r0, a);

@@ -487,7 +487,8 @@ attn_status_t attn_kv_weigh(const attn_kv_cache_t *cache, int layer, const void 
  * position's row then differs from head to head, but all have one length.  Weights behind the new
  * end, up to the old one, become 0; rows there stay as they are; the pages behind it are given back.
  * weights may be NULL when heavy is 0 (the oldest positions behind the first go).
- * A sequence of no more positions is left as it is, its pages too.  Pages from that of position
+ * Rows behind the first position that goes move up, whether one goes or many: let sequences grow
+ * between calls.  A sequence of no more positions is left as it is, its pages too.  Pages from that of position
  * `sinks` to the new end are written and must not be shared (those of whole pages of first positions
  * may be): ATTN_ERR_PAGE, also for one that is missing up to the old end; ATTN_ERR_SHAPE for a
  * sequence or length out of range and the second entry of a sequence named twice. */
