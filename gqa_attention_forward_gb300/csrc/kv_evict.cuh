@@ -1,4 +1,4 @@
-// Cutting sequences of the cache back to a budget (attn_kv_evict).
+// Cutting sequences of the cache back to a given length (attn_kv_evict).
 //
 // A sequence of L positions, more than keep = sinks + heavy + recent, keeps in every layer and kv
 // head its first `sinks`, its last `recent` and, of those between, the `heavy` ones with the

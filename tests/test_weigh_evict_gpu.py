@@ -332,7 +332,7 @@ def test_a_bounded_cache_as_it_is_used():
     """Prompts through the window and through all keys, their keys into pages, their weights; then steps
     of single tokens and drafted trees, weighed, cut back again and again; one step in a graph."""
     Hq, Hkv, D, dtype, page, scale = 8, 2, 128, "bf16", 16, 1 / math.sqrt(128)
-    lens, budget = [200, 90, 300], dict(sinks=4, heavy=40, recent=36)
+    lens, keeps = [200, 90, 300], dict(sinks=4, heavy=40, recent=36)
     cache = binding.KVPages.empty(1, 80, Hkv, page, D, 4, 40, torch.bfloat16)
     weights, rows = cache.weights(), i32([0, 1, 2])
     x = queries(sum(lens), Hq + 2 * Hkv, D, dtype, 21)
@@ -356,8 +356,8 @@ def test_a_bounded_cache_as_it_is_used():
         nonlocal host
         host = weights.cpu()
         model.__init__(cache)
-        binding.kv_evict(cache, rows, weights, **budget)
-        evict(model, host, range(3), **budget)
+        binding.kv_evict(cache, rows, weights, **keeps)
+        evict(model, host, range(3), **keeps)
         assert status() == binding.ATTN_OK
         model.same(cache)
         model.consistent()
@@ -376,7 +376,7 @@ def test_a_bounded_cache_as_it_is_used():
         binding.kv_append(cache, tk, tv, cu1, seqs=rows)
         binding.attention_tree(tq, cache, cu1, seqs=rows, out=out, lse_out=tlse, workspace=ws)
         binding.kv_weigh(cache, weights, tq, tlse, cu1, seqs=rows)
-        binding.kv_evict(cache, rows, weights, **budget)
+        binding.kv_evict(cache, rows, weights, **keeps)
 
     graph = None
     for turn in range(5):
