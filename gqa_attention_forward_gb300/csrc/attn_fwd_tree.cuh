@@ -658,12 +658,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 int left = u->L - kt * kBN;
                 left = left < 0 ? 0 : (left < kBN ? left : kBN);
                 // a token alone sees the keys outside [z0, z1) of a tile on the window's border, as all its heads do
+                // (rows of the tile, whatever the window is: the guard multiplies them)
                 int z0 = 0, z1 = 0;
                 if (kWindow && u->T <= 1) {
                     z0 = p.sinks - kt * kBN;
                     z1 = u->base - p.window + 1 - kt * kBN;
-                    z0 = z0 < 0 ? 0 : z0;
-                    z1 = z1 < kBN ? z1 : kBN;
+                    z0 = z0 < 0 ? 0 : (z0 < kBN ? z0 : kBN);
+                    z1 = z1 < 0 ? 0 : (z1 < kBN ? z1 : kBN);
                 }
                 const bool any = vl_guard_tile<D, kBF16>(smem + L::kKV + stage * L::kTileBytes, left, u->T > 1,
                                                          u->bad_rows[g & (kBad - 1)], lane, z0, z1);
