@@ -216,9 +216,6 @@ unsigned move_grid(const gqa::KvPool &p, long long pages, int sms) {
     return static_cast<unsigned>(blocks < most ? (blocks > 0 ? blocks : 1) : most);
 }
 
-// A window and a number of first keys as the kernels take them: no sum of theirs with a position
-// passes 32 bits.
-constexpr int kWindowMost = 1 << 30;
 bool window_ok(int window, int sinks) { return window >= 1 && sinks >= 0; }
 
 // attn_fwd_varlen (window 0) and attn_fwd_varlen_window.
@@ -273,10 +270,11 @@ attn_status_t run_varlen(const void *q, const void *k, const void *v, void *o, f
         return no_map();
     const unsigned grid = static_cast<unsigned>(units < g_dev_sms[dev] ? units : g_dev_sms[dev]);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    // a window that no sequence can leave, or first keys that are all keys: the causal mask
+    // a window that no sequence can leave, or first keys that are all keys: the causal mask.  What the
+    // window kernels get is below total_k, so that no sum with a position passes 32 bits.
     if (window >= total_k || sinks >= total_k) window = 0;
-    prm.window = window < kWindowMost ? window : kWindowMost;
-    prm.sinks = sinks < kWindowMost ? sinks : kWindowMost;
+    prm.window = window;
+    prm.sinks = sinks;
     const int kid = window > 0 ? 8 + (D == 128 ? 2 : 0) + (bf16 ? 1 : 0)
                                : (D == 128 ? 4 : 0) + (bf16 ? 2 : 0) + (causal ? 1 : 0);
     auto launch = [&]() {
@@ -375,10 +373,11 @@ attn_status_t run_tree(const void *q, const attn_kv_cache_t *cache, int layer, v
     const unsigned grid = static_cast<unsigned>(most < sms ? most : sms);
     prm.grid = static_cast<int>(grid);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    // a window that no sequence can leave, or first keys that are all keys: the plain call
+    // a window that no sequence can leave, or first keys that are all keys: the plain call.  What the
+    // window kernels get is below table_width * page, which is below 2^30 (check_cache).
     if (window >= cache->table_width * cache->page || sinks >= cache->table_width * cache->page) window = 0;
-    prm.window = window < kWindowMost ? window : kWindowMost;
-    prm.sinks = sinks < kWindowMost ? sinks : kWindowMost;
+    prm.window = window;
+    prm.sinks = sinks;
     const int kid = (window > 0 ? 4 : 0) + (D == 128 ? 2 : 0) + (bf16 ? 1 : 0);
     auto launch = [&]() {
         switch (kid) {
