@@ -1,13 +1,64 @@
-"""The window, weighing and eviction calls at the ends of what they take."""
+"""The window, weighing and eviction calls at the ends of what they take: the widest table, offsets
+past 32 bits, more large units than are dealt one by one, and what a wait that ran out leaves.
+
+Bound of a sum of weights, from the order in which kv_weigh_kernel adds (f = 2^-24): the terms are off
+as test_weigh_evict_gpu says.  A warpgroup has 64 columns of a row tile, in 4 chains of 16 that 2 sums
+join, and one sum per row tile; the two warpgroups' sums are added once, and the old value once more:
+(16 + 2 + tiles + 2) f of the sum."""
+import math
+
 import pytest
+import torch
 
 from gqa_attention_forward_gb300 import binding
-from packed_util import offsets
-from paged_util import build
+from packed_util import F, close, offsets
+from paged_util import build, gather
 from test_tree_gpu import i32, queries, status, trees
+from test_weigh_evict_gpu import logsumexps
 from test_window_gpu import check_trees
 
 pytestmark = pytest.mark.gpu
+
+
+def weights_in_64_bits(q, lse, k, scale):
+    """Sums [Hkv, n] that q [T, Hq, D], lse [Hq, T] give the keys k [n, Hkv, D], and their bounds."""
+    n, Hkv, D = k.shape
+    T, G = q.shape[0], q.shape[1] // Hkv
+    q = q.double().view(T, Hkv, G, D).permute(1, 2, 0, 3)
+    k, l = k.double().permute(1, 2, 0)[:, None], lse.double().view(Hkv, G, T, 1)
+    s = q @ k * scale
+    e = (D + 2) * F * (q.abs() @ k.abs()) * scale
+    see = torch.ones(T, n, dtype=torch.bool, device=q.device).tril(n - T)
+    p = torch.where(see, torch.exp(s - l), 0.0)
+    d = e + F * s.abs() + 2 * F * l.abs() + F * (s - l).abs() + 2.0 ** -22
+    tiles = -(-T // (128 // G))
+    sums = p.sum((1, 2))
+    return sums.cpu(), ((p * d * (1 + d)).sum((1, 2)) + (20 + tiles) * F * sums + 1e-30).cpu()
+
+
+def test_more_large_units_than_are_dealt_one_by_one():
+    """A group of 65 heads leaves one token to a row tile: ten times as many units of 8 row tiles and more
+    as there are SMs, of which the first eighty percent are dealt one by one, and units of fewer behind them."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    Hkv, G, D, scale = 2, 65, 64, 0.125
+    blocks = -(-10 * sms // (24 * Hkv))
+    lens = [256 * blocks + 16 + 3 * i for i in range(24)] + [700 + i for i in range(8)]
+    T = [8 + i % 5 for i in range(24)] + [1 + i % 7 for i in range(8)]
+    cache = build(lens, 64, Hkv, D, "bf16", seed=91)
+    q = queries(sum(T), Hkv * G, D, "bf16", 92)
+    lse, a = torch.empty((Hkv * G, sum(T)), device="cuda"), 0
+    for s, t in enumerate(T):
+        lse[:, a:a + t] = logsumexps(q[a:a + t], gather(cache, s)[0], t, scale)
+        a += t
+    weights = torch.full_like(cache.weights(), -3.0)
+    binding.kv_weigh(cache, weights, q, lse, offsets(T), accumulate=False)
+    assert status() == binding.ATTN_OK
+    a = 0
+    for s, (n, t) in enumerate(zip(lens, T)):
+        want, tol = weights_in_64_bits(q[a:a + t], lse[:, a:a + t], gather(cache, s)[0], scale)
+        close(weights[0, s, :, :n], want, tol, f"sequence {s}")
+        assert bool((weights[0, s, :, n:] == -3).all())
+        a += t
 
 
 @pytest.mark.parametrize("window,sinks", [(None, 0), (None, 300), (1, None), (700, None), (None, None)])
@@ -22,3 +73,74 @@ def test_windows_of_the_widest_table(window, sinks):
     o, lse = binding.attention_tree(q, cache, offsets(T), parents=i32([x for p in par for x in p]), window=window, sinks=sinks)
     assert status() == binding.ATTN_OK
     check_trees(q, cache, o, lse, range(2), par, "f16", 1 / 8, window, sinks)
+
+
+def test_offsets_beyond_32_bits():
+    """The last pages of pools of 2.5e9 elements a layer, and the last row of 2^31 weights."""
+    layers, n_pages, Hkv, page, D, n_rows, width = 2, 600, 8, 4096, 128, 8, 4096
+    n, row, T, scale = 9000, 7, 3, 1 / math.sqrt(128)
+    cache = binding.KVPages.empty(layers, n_pages, Hkv, page, D, n_rows, width, torch.bfloat16)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(96)
+    pages = [599, 597, 598]
+    for x in (cache.k, cache.v):
+        for p in pages:
+            x[:, p] = torch.randn((layers, Hkv, page, D), generator=g, device="cuda").to(x.dtype)
+    cache.table[row, :3] = i32(pages)
+    cache.lens[row] = n
+    cache.refs[597:] = 1
+    q, seqs = queries(T, Hkv, D, "bf16", 97), i32([row])
+    o, lse = binding.attention_tree(q, cache, offsets([T]), seqs=seqs, layer=1, window=1500, sinks=7)
+    assert status() == binding.ATTN_OK
+    check_trees(q, cache, o, lse, [row], [[-1, 0, 1]], "bf16", scale, 1500, 7, layer=1)
+    o, lse = binding.attention_tree(q, cache, offsets([T]), seqs=seqs, layer=1)
+    weights = cache.weights()
+    assert weights.numel() == 2 ** 31
+    weights[1, row, :, :n - T] = 0.5
+    binding.kv_weigh(cache, weights, q, lse, offsets([T]), seqs=seqs, layer=1)
+    assert status() == binding.ATTN_OK
+    want, tol = weights_in_64_bits(q, lse, gather(cache, row, 1)[0], scale)
+    want[:, :n - T] += 0.5
+    close(weights[1, row, :, :n], want, tol + F * want, "weights")
+    weights[0, row, :, :n] = torch.rand((Hkv, n), generator=g, device="cuda")
+    w = weights[:, row, :, :n].clone()
+    old = [torch.stack([x.transpose(0, 1) for x in pair]) for pair in zip(*(gather(cache, row, i) for i in (0, 1)))]
+    sinks, heavy, recent = 5, 4000, 300
+    binding.kv_evict(cache, seqs, weights, sinks=sinks, heavy=heavy, recent=recent)
+    assert status() == binding.ATTN_OK
+    keep = sinks + heavy + recent
+    best = torch.sort(w[:, :, sinks:n - recent], dim=-1, descending=True, stable=True).indices[:, :, :heavy] + sinks
+    at = torch.arange(n, device="cuda").expand(layers, Hkv, n)
+    src = torch.cat([at[:, :, :sinks], best.sort(-1).values, at[:, :, n - recent:]], -1)
+    new = [torch.stack([x.transpose(0, 1) for x in pair]) for pair in zip(*(gather(cache, row, i) for i in (0, 1)))]
+    for a, b in zip(old, new):
+        assert torch.equal(torch.gather(a, 2, src[..., None].expand(-1, -1, -1, D)), b)
+    assert torch.equal(weights[:, row, :, :keep], torch.gather(w, 2, src)) and not bool(weights[:, row, :, keep:].any())
+    assert not bool(weights[:, :row].any())
+    assert cache.lens.tolist() == [0] * 7 + [keep] and cache.table[row, :3].tolist() == [599, 597, -1]
+    assert cache.refs[597:].tolist() == [1, 0, 1]
+
+
+def test_sums_that_a_wait_cut_short_are_restored_and_added_again():
+    """A call that gave up leaves undefined the sums of the listed sequences, in its layer, and no others."""
+    lens, T = [900, 300, 400], [40, 3]
+    cache = build(lens, 64, 2, 128, "bf16", n_layers=2, seed=98)
+    q, lse, seqs = queries(43, 8, 128, "bf16", 99), torch.full((8, 43), 6.0, device="cuda"), i32([2, 0])
+    weights, lib = cache.weights().uniform_(0.0, 2.0), binding.load()
+    before, good = weights.clone(), weights.clone()
+    binding.kv_weigh(cache, good, q, lse, offsets(T), seqs=seqs, layer=1)
+    assert status() == binding.ATTN_OK
+    try:
+        lib.attn_test_set_wait_timeout_ns(20_000_000)
+        lib.attn_test_inject_stall(1)
+        binding.kv_weigh(cache, weights, q, lse, offsets(T), seqs=seqs, layer=1)
+    finally:
+        lib.attn_test_inject_stall(0)
+        lib.attn_test_set_wait_timeout_ns(0)
+    assert status() == binding.ATTN_ERR_TIMEOUT
+    assert torch.equal(weights[0], before[0]) and torch.equal(weights[1, 1], before[1, 1])
+    for s in (0, 2):
+        assert torch.equal(weights[1, s, :, lens[s]:], before[1, s, :, lens[s]:])
+    weights.copy_(before)
+    binding.kv_weigh(cache, weights, q, lse, offsets(T), seqs=seqs, layer=1)
+    assert status() == binding.ATTN_OK and torch.equal(weights, good)
