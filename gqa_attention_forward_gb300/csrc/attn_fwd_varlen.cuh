@@ -52,7 +52,8 @@
 // of the steps).  Masked tiles go in one pass, as a word of bits per row and 32 columns: with windows
 // they are too many of all tiles for the two passes of the plain kernel (12 prompts of 1 to 4096,
 // Hq 16, D 128, window 512: 84.4 us in two passes, 82.1 in one; one prompt of 200, window 64, D 64
-// 11.0 and 9.0; two of 16384 and 9001, Hq 32, window 2048 611 and 587, 1.37 PFLOP/s).  Taking the first
+// 11.0 and 9.0; two of 16384 and 9001, Hq 32, window 2048 611 and 587, 1.37 PFLOP/s; the 12 prompts with
+// D 64 69, where the kernel loads 512 bytes of spills in all).  Taking the first
 // keys' tile as products of 16 ceil(n / 16) keys saves a sixth of the first case's MMAs and costs
 // time (84.7): the steps' round trips between the roles bound short units, not their products.
 //

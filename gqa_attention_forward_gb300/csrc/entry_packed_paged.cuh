@@ -406,9 +406,9 @@ attn_status_t run_tree(const void *q, const attn_kv_cache_t *cache, int layer, v
 
 // Blocks of a cluster of kv_evict_kernel.  With a choice to make, all of them look for it, and more
 // than one pays only where the sequences, layers and heads leave SMs without work (32 of them, of
-// 65000 positions: 510 us with 1 block, 293, 191, 153 with 2, 4, 8; 512 of 1000 to 8000 111, 115, 150,
-// 220; 256 of 65000 820, 937, 827, 964); without one, more and smaller blocks even out the end (512 of
-// 2000 to 4000: 182, 167, 174, 204; 2560 759, 751, 770, 960).
+// 65000 positions: 497 us with 1 block, 285, 186, 149 with 2, 4, 8; 512 of 1000 to 8000 105, 109, 144,
+// 214; 256 of 65000 812, 929, 823, 955); without one, more and smaller blocks even out the end (512 of
+// 2000 to 4000: 179, 164, 171, 201; 2560 759, 748, 767, 948).
 unsigned evict_cluster(long long problems, bool choose, int sms) {
     unsigned c = 1;
     while (c < gqa::kEvClusterMost && problems * c < (choose ? 1ll : 6ll) * sms) c *= 2;

@@ -19,10 +19,12 @@
 // ascend, and place d takes a row from position d or behind, so that the rows of a step are stored
 // once all of the step's loads have been issued, while the next step's are under way.
 //
-// Measured, GB300: 16 sequences of 65 to 8192 to 1024 positions in 4 layers of 8 heads 111 us, in 20
-// layers 436 (5.6 TB/s over the call; before its rows move a block spends about 20 us on the choice,
+// Measured, GB300, captured, with the copies that start each pass from the same state (5 and 28 us;
+// without weights 2): 16 sequences of 65 to 8192 to 1024 positions in 4 layers of 8 heads 103 us, in 20
+// layers 418 (6.3 TB/s without those copies; before its rows move a block spends about 20 us on the choice,
 // which the rows of other blocks hide where there are more of them than fit at once); 16 of 2048 to
-// 4000 to 2048 without weights 166 and 751 (6.7 TB/s, the copy rate).
+// 4000 to 2048 without weights 168 and 760 (6.6 TB/s, near the copy rate); 65000 to 16016 148 us, in 32
+// layers 810.
 #pragma once
 #include <cooperative_groups.h>
 
@@ -193,8 +195,9 @@ __device__ __forceinline__ uint32_t evict_select(const float *w, int m, int heav
     return prefix;
 }
 
-// kChoose: heavy is not 0.
-// (3 blocks per SM: 124 us instead of 111 with the 64 registers of 4, which spill; without a choice 4: 166, with 3 181.)
+// kChoose: heavy is not 0.  Blocks per SM: with a choice 3 (80 registers, no spills); with 4 (64 registers,
+// which spill) the 16 sequences take 109 us instead of 103, and 65000 positions 173 instead of 148.  Without
+// one 4: 167 us, although 64 registers spill 28 bytes (48 loaded); with 3 175.
 template <bool kChoose>
 __global__ void __launch_bounds__(kEvThreads, kChoose ? 3 : 4) kv_evict_kernel(const KvPool c, const KvEvict x) {
     extern __shared__ __align__(16) uint8_t evict_raw[];

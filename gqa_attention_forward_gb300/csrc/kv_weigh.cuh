@@ -12,10 +12,10 @@
 // the tensor cores and the exponentials alike (2 D flops and one exp2 per row and key, of which an
 // SM does about 8192 and 32 a cycle: 512 cycles of each for 128 keys and 128 rows).
 //
-// Measured, GB300: 16 sequences of 2 to 8192 positions and a token each (Hq 32, Hkv 8, D 128) 37 us
+// Measured, GB300: 16 sequences of 2 to 8192 positions and a token each (Hq 32, Hkv 8, D 128) 35 us
 // with the copy that resets the case, 1.5 us per 64 KB of K and SM while it streams (6.6 TB/s), 4 us
-// until the first tile; the last 32 tokens of 32000 15 us; 12 whole prompts of 1 to 4096 (Hq 16) 81
-// us, 0.86 PFLOP/s; one of 32768 (Hq 32) 3327 us, 1.32 PFLOP/s; one of 512 beside 31 sequences of 32768
+// until the first tile; the last 32 tokens of 32000 15 us; 12 whole prompts of 1 to 4096 (Hq 16) 80
+// us, 0.87 PFLOP/s; one of 32768 (Hq 32) 3330 to 3400 us, 1.3 PFLOP/s; one of 512 beside 31 sequences of 32768
 // with a token each 318 us, 6.66 TB/s.  A step of 256 keys and 128 rows takes 1800 to 2200 cycles, of
 // which the tensor pipe and the exponentials are busy for about 1000 each, and its two halves, the
 // issuer's waits, products and commits (1800) and the sums' barriers, TMEM loads and exponentials
@@ -26,7 +26,7 @@
 // The product is taken transposed, S^T = K Q^T: a TMEM lane, and so a thread, owns a key, and the
 // sum over the rows is a sum over a thread's own columns, without shuffles, atomics or a second
 // pass; the rows' log-sum-exps are the same for all threads and come from shared memory.  A unit is
-// 256 keys of a kv head (two 128-key tiles that share every Q tile, one warpgroup each) against all
+// 256 keys of a kv head (two 128-key tiles that share every Q tile, two warpgroups each) against all
 // row tiles that see one of them, so that every position's sum has one owner and a fixed order.
 // Row tiles hold 128 / G tokens (row = token * G + head in the group).
 //
@@ -34,7 +34,7 @@
 // sequence's blocks of keys have fewer and fewer, so that lane s of the scheduler finds sequence s's
 // block of a level in closed form), large ones to the CTA with the least work, the rest in snake
 // order; those of more sequences in the order of these, as a pass over all for each level would
-// take too long.
+// take too long (32 prompts of 1 to 4096, Hq 16: 296 us, 0.99 PFLOP/s; 33 of them 331, 0.91; 64 775, 0.90).
 //
 // Roles (640 threads): warp 0 MMA issuer, warp 1 TMA producer of Q, and the rows' log-sum-exps,
 // warp 2 TMA producer of K (the lanes issue one page box each), warp 3 scheduler (and TMEM), and
@@ -42,6 +42,10 @@
 // 128 x 128 scores, mostly its own latencies, the products 504).  K has two buffers of a unit, Q a
 // ring of three tiles.  TMEM: S^T of tile a, buffer b in columns [256 a + 128 b, + 128).  At a
 // unit's end the second warpgroup of a tile hands its sums to the first through a column of its buffer.
+//
+// Rounding: all in fp32.  A warpgroup adds 64 columns of a row tile in 4 chains of 16, joins them (2
+// sums) and adds one sum per row tile; the other's and the old value come last: a sum is off by at most
+// (16 + 2 + row tiles + 2) 2^-24 of itself, beside what the scores and exponentials are off by.
 #pragma once
 #include <cuda.h>  // CUtensorMap
 

@@ -436,8 +436,9 @@ attn_status_t attn_fwd_tree(const void *q, const attn_kv_cache_t *cache, int lay
  *
  * window  at least 1; one of table_width * page or more is attn_fwd_tree.  sinks: at least 0.
  * Positions count the rows that the cache holds: where attn_kv_evict has cut a sequence, its
- * rows have moved up.  Of the pages, those that hold a part of a run of 128 positions (from a
- * multiple of 128) of which some token sees one are read; the others may be missing.
+ * rows have moved up (see its note on rotary positions).  Of the pages, those that hold a part of
+ * a run of 128 positions (from a multiple of 128) of which some token sees one are read; the
+ * others may be missing.
  * Everything else: as attn_fwd_tree; ATTN_ERR_SHAPE also for window < 1 or sinks < 0.
  */
 attn_status_t attn_fwd_tree_window(const void *q, const attn_kv_cache_t *cache, int layer, void *o,
@@ -473,7 +474,9 @@ attn_status_t attn_fwd_tree_window(const void *q, const attn_kv_cache_t *cache, 
  * Errors: as attn_fwd_tree; attn_last_device_error reports ATTN_ERR_SHAPE for offsets, lengths
  * and sequences out of range, T above the sequence's length and a sequence named twice (its first
  * entry counts), whose weights are then left as they were, and ATTN_ERR_PAGE for a missing page,
- * whose positions' weights are then undefined.
+ * whose positions' weights are then undefined.  After ATTN_ERR_TIMEOUT the layer's weights of all
+ * listed sequences, up to their ends, are undefined (some may hold the new sums and some the old ones):
+ * restore them, or weigh from zero, before they are added to or evicted by again.
  */
 attn_status_t attn_kv_weigh(const attn_kv_cache_t *cache, int layer, const void *q, const float *lse,
                             float *weights, const int *cu, const int *seqs, int n, int total_q,
@@ -488,10 +491,14 @@ attn_status_t attn_kv_weigh(const attn_kv_cache_t *cache, int layer, const void 
  * end, up to the old one, become 0; rows there stay as they are; the pages behind it are given back.
  * weights may be NULL when heavy is 0 (the oldest positions behind the first go).
  * Rows behind the first position that goes move up, whether one goes or many: let sequences grow
- * between calls.  A sequence of no more positions is left as it is, its pages too.  Pages from that of position
- * `sinks` to the new end are written and must not be shared (those of whole pages of first positions
+ * between calls.  A sequence of no more positions is left as it is, its pages too.  Pages from that of
+ * position `sinks` to the new end are written and must not be shared (those of whole pages of first positions
  * may be): ATTN_ERR_PAGE, also for one that is missing up to the old end; ATTN_ERR_SHAPE for a
- * sequence or length out of range and the second entry of a sequence named twice. */
+ * sequence or length out of range and the second entry of a sequence named twice.
+ * Rotary positions: a row keeps the rotation that its key was written with, while lengths, windows and
+ * first keys count the rows of the cache.  Where new tokens go on with positions of their own (and not with
+ * the cut length), the program keeps count of them.
+ * Limits (ATTN_ERR_SHAPE): n * n_layers * Hkv below 2^28, rows of a layer (n_pages * Hkv * page) below 2^32. */
 attn_status_t attn_kv_evict(const attn_kv_cache_t *cache, const int *seqs, int n, float *weights,
                             int sinks, int heavy, int recent, void *stream);
 
