@@ -144,3 +144,82 @@ def test_sums_that_a_wait_cut_short_are_restored_and_added_again():
     weights.copy_(before)
     binding.kv_weigh(cache, weights, q, lse, offsets(T), seqs=seqs, layer=1)
     assert status() == binding.ATTN_OK and torch.equal(weights, good)
+
+
+def test_a_sequence_that_fills_the_widest_table():
+    """2^30 positions over one page that every entry names: each of its rows stands for as many equal keys as
+    a token sees of them.  Attention with windows, weights of every position, and a cut to 5093 of them,
+    which moves the rows of the shared page into the sequence's own first two."""
+    page, width, D, scale, T = 4096, (2 ** 30 - 1) // 4096, 64, 1 / 8, 2
+    n = page * width - 3  # a last page that is not full
+    i = dict(dtype=torch.int32, device="cuda")
+    cache = binding.KVPages.empty(1, 3, 1, page, D, 1, width, torch.float16)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(101)
+    for x in (cache.k, cache.v):
+        x.copy_(torch.randn(x.shape, generator=g, device="cuda"))
+    cache.table.zero_()
+    cache.lens.fill_(n)
+    cache.refs.copy_(torch.tensor([width, 0, 0], **i))
+    q = queries(T, 2, D, "f16", 102)
+    rows = torch.arange(page, device="cuda")
+
+    def copies(a, b):
+        """How often each row of the page stands in positions [a, b)."""
+        return ((b - rows + page - 1) // page - (a - rows + page - 1) // page).double()
+
+    s = torch.einsum("thd,rd->thr", q.double(), cache.k[0, 0, 0].double()) * scale
+    most = float(s.abs().max())
+    e = (D + 2) * F * float((q.double().abs() @ cache.k[0, 0, 0].double().abs().T).max()) * scale
+    lse = None
+    for window, sinks in ((1, 0), (5000, 777), (n // 2 + 9, 10 ** 6 + 1), (n - 5, 3), (None, 0)):
+        o, lse = binding.attention_tree(q, cache, offsets([T]), window=window, sinks=sinks)
+        assert status() == binding.ATTN_OK
+        for t in range(T):
+            pos = n - T + t
+            lo = 0 if window is None else max(0, pos - window + 1)
+            seen = copies(lo, pos + 1) + copies(0, min(sinks, lo))
+            want = torch.logsumexp(s[t] + seen.log(), -1)
+            p = torch.exp(s[t] - want[:, None]) * seen
+            ref, size = p @ cache.v[0, 0, 0].double(), p @ cache.v[0, 0, 0].double().abs()
+            # the bounds of packed_util over so many keys and 152 pieces; an fp16 weight below the smallest
+            # normal number is off by 2^-25 of the row's largest, so each copy of a row by that in all
+            count, u = float(seen.sum()), 2.0 ** -11
+            add = (72 + count / 128 + 152 + 8) * F + 2.0 ** -21
+            tiny = 2.0 ** -25 * count / torch.exp(want - s[t].amax(-1))[:, None] * float(cache.v[0, 0].abs().max())
+            close(o[t], ref.cpu(), (u * ref.abs() + (1 + u) * (u + 2 * (e + 4 * F * most) + 2 * add) * size + tiny + 2.0 ** -25).cpu(),
+                  f"O of token {t}, window {window}")
+            close(lse[:, t], want.cpu(), (e + (8 * most + 2 * want.abs()) * F + add).cpu(), f"LSE of token {t}, window {window}")
+    weights = cache.weights()
+    binding.kv_weigh(cache, weights, q, lse, offsets([T]), accumulate=False)
+    assert status() == binding.ATTN_OK
+    p = torch.exp(s - lse.double().T[..., None])  # [T, 2, rows]
+    want = p.sum((0, 1))
+    tol = want * 1.01 * (e + 4 * F * most + 4 * F * float(lse.abs().max()) + 2.0 ** -22 + 21 * F)
+    got = weights.view(width, page)
+    off = (got.double() - want).abs() <= tol
+    off[-1, page - 4:] = True  # the last token's position, which the first one does not join, and those behind the end
+    assert bool(off.all())
+    last = p[1, :, (n - 1) % page].sum()
+    assert abs(float(weights.view(-1)[n - 1] - last)) <= float(tol[(n - 1) % page]) and not bool(weights.view(-1)[n:].any())
+    # the cut
+    cache.table[0, :2] = torch.tensor([1, 2], **i)
+    cache.refs.copy_(torch.tensor([width - 2, 1, 1], **i))
+    sinks, heavy, recent = 3, 5000, 90
+    keep = sinks + heavy + recent
+    w = weights.view(-1)
+    w.uniform_(generator=g)
+    middle = w[sinks:n - recent]
+    border = torch.topk(middle, heavy).values[-1]
+    above, equal = (middle > border).nonzero()[:, 0], (middle == border).nonzero()[:, 0]
+    best = torch.cat([above, equal[:heavy - above.numel()]]).sort().values + sinks
+    src = torch.cat([torch.arange(sinks, device="cuda"), best, torch.arange(n - recent, n, device="cuda")])
+    at = cache.table[0].long()[src // page]
+    want = [x[0, at, 0, src % page] for x in (cache.k, cache.v)] + [w[src]]
+    binding.kv_evict(cache, None, weights, sinks=sinks, heavy=heavy, recent=recent)
+    assert status() == binding.ATTN_OK
+    k, v = gather(cache, 0)
+    for a, b in zip(want, (k[:, 0], v[:, 0], w[:keep])):
+        assert a.shape == b.shape and torch.equal(a, b)
+    assert not bool(w[keep:n].any()) and cache.lens.tolist() == [keep]
+    assert cache.refs.tolist() == [0, 1, 1] and bool((cache.table[0, 2:] == -1).all())
